@@ -14,6 +14,7 @@ torch and then call the same entry points.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -51,6 +52,19 @@ class moe_weights(ctypes.Structure):
     _fields_ = [("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
                 ("s_gate", ctypes.c_void_p), ("s_up", ctypes.c_void_p), ("s_down", ctypes.c_void_p),
                 ("layout", ctypes.c_int32)]
+
+
+class moe_mx_weights(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("num_experts", ctypes.c_int32), ("n_out", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("swiglu", ctypes.c_int32), ("packed", ctypes.c_void_p),
+                ("alpha", ctypes.c_void_p), ("alpha_up", ctypes.c_void_p)]
+
+
+# microscaled formats (include/moe_mx.h)
+MOE_MX_BF16, MOE_MX_MXFP8, MOE_MX_MXFP4, MOE_MX_NVFP4 = range(4)
+MX_FORMATS = {"bf16": MOE_MX_BF16, "mxfp8": MOE_MX_MXFP8, "mxfp4": MOE_MX_MXFP4, "nvfp4": MOE_MX_NVFP4}
+MOE_MX_OUT_BF16, MOE_MX_OUT_F16 = 0, 1
+MOE_MX_PRODUCT_WORKSPACE = 256
 
 
 class moe_trace(ctypes.Structure):
@@ -104,6 +118,30 @@ _SIGS = {
     "moe_ep_combine": (ctypes.c_int, [ctypes.POINTER(moe_dims), ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
                                       ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                       ctypes.c_void_p]),
+    "moe_mx_code_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int64]),
+    "moe_mx_scale_pitch": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int64]),
+    "moe_mx_quantise": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                       ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64]
+                        + [ctypes.c_void_p] * 3),
+    "moe_mx_add_rmsnorm": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                          ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                          ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_int64] + [ctypes.c_void_p] * 4),
+    "moe_mx_dequantise": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32] + [ctypes.c_void_p] * 4
+                          + [ctypes.c_int64, ctypes.c_void_p]),
+    "moe_mx_packed_bytes": (ctypes.c_size_t, [ctypes.POINTER(moe_mx_weights)]),
+    "moe_mx_pack_weights": (ctypes.c_int, [ctypes.POINTER(moe_mx_weights)] + [ctypes.c_void_p] * 6),
+    "moe_mx_grouped_product": (ctypes.c_int, [ctypes.POINTER(moe_mx_weights), ctypes.c_int64] + [ctypes.c_void_p] * 5
+                               + [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64] + [ctypes.c_void_p] * 3
+                               + [ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_mx_grouped_swiglu": (ctypes.c_int, [ctypes.POINTER(moe_mx_weights), ctypes.c_int64] + [ctypes.c_void_p] * 8
+                              + [ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_mx_layer_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(moe_mx_weights), ctypes.POINTER(moe_mx_weights),
+                                                      ctypes.c_int32, ctypes.c_int64]),
+    "moe_mx_layer_forward": (ctypes.c_int, [ctypes.POINTER(moe_mx_weights), ctypes.POINTER(moe_mx_weights),
+                                            ctypes.c_int32, ctypes.c_int64] + [ctypes.c_void_p] * 3
+                             + [ctypes.c_float] + [ctypes.c_void_p] * 6
+                             + [ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "moe_check_bounded_wait": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "moe_get_error": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
 }
@@ -296,6 +334,77 @@ def moe_get_error(ws, stream=None) -> int:
     return load_library().moe_get_error(_ptr(ws), _stream(stream))
 
 
+# microscaled formats
+
+def moe_mx_code_bytes(fmt: int, cols: int) -> int:
+    return load_library().moe_mx_code_bytes(fmt, cols)
+
+
+def moe_mx_scale_pitch(fmt: int, cols: int) -> int:
+    return load_library().moe_mx_scale_pitch(fmt, cols)
+
+
+def moe_mx_quantise(fmt, n, k, d, x, x_ld, positions, global_scale, out_rows, codes, scales, stream=None):
+    st = load_library().moe_mx_quantise(fmt, n, k, d, _ptr(x), x_ld, _ptr(positions), _ptr(global_scale), out_rows,
+                                        _ptr(codes), _ptr(scales), _stream(stream))
+    _check(st, "moe_mx_quantise")
+
+
+def moe_mx_add_rmsnorm(fmt, n, k, d, x, x_ld, residual, r_ld, gain, eps, positions, global_scale, out_rows, sum_out,
+                       codes, scales, stream=None):
+    st = load_library().moe_mx_add_rmsnorm(fmt, n, k, d, _ptr(x), x_ld, _ptr(residual), r_ld, _ptr(gain), float(eps),
+                                           _ptr(positions), _ptr(global_scale), out_rows, _ptr(sum_out), _ptr(codes),
+                                           _ptr(scales), _stream(stream))
+    _check(st, "moe_mx_add_rmsnorm")
+
+
+def moe_mx_dequantise(fmt, rows, d, codes, scales, global_scale, out, out_ld, stream=None):
+    st = load_library().moe_mx_dequantise(fmt, rows, d, _ptr(codes), _ptr(scales), _ptr(global_scale), _ptr(out),
+                                          out_ld, _stream(stream))
+    _check(st, "moe_mx_dequantise")
+
+
+def moe_mx_packed_bytes(w: moe_mx_weights) -> int:
+    return load_library().moe_mx_packed_bytes(ctypes.byref(w))
+
+
+def moe_mx_pack_weights(w: moe_mx_weights, codes, scales, codes_up, scales_up, packed, stream=None):
+    st = load_library().moe_mx_pack_weights(ctypes.byref(w), _ptr(codes), _ptr(scales), _ptr(codes_up),
+                                            _ptr(scales_up), _ptr(packed), _stream(stream))
+    _check(st, "moe_mx_pack_weights")
+
+
+def moe_mx_grouped_product(w: moe_mx_weights, rows, x_codes, x_scales, x_global, expert_offsets, out, out_type,
+                           out_rows, out_ld, out_pos, row_weight, ws, stream=None):
+    st = load_library().moe_mx_grouped_product(ctypes.byref(w), rows, _ptr(x_codes), _ptr(x_scales), _ptr(x_global),
+                                               _ptr(expert_offsets), _ptr(out), out_type, out_rows, out_ld,
+                                               _ptr(out_pos), _ptr(row_weight), _ptr(ws),
+                                               ws.numel() * ws.element_size(), _stream(stream))
+    _check(st, "moe_mx_grouped_product")
+
+
+def moe_mx_grouped_swiglu(w: moe_mx_weights, rows, x_codes, x_scales, x_global, expert_offsets, h_global, h_codes,
+                          h_scales, ws, stream=None):
+    st = load_library().moe_mx_grouped_swiglu(ctypes.byref(w), rows, _ptr(x_codes), _ptr(x_scales), _ptr(x_global),
+                                              _ptr(expert_offsets), _ptr(h_global), _ptr(h_codes), _ptr(h_scales),
+                                              _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+    _check(st, "moe_mx_grouped_swiglu")
+
+
+def moe_mx_layer_workspace_size(gate_up: moe_mx_weights, down: moe_mx_weights, top_k: int, n_tokens: int) -> int:
+    return load_library().moe_mx_layer_workspace_size(ctypes.byref(gate_up), ctypes.byref(down), top_k, n_tokens)
+
+
+def moe_mx_layer_forward(gate_up: moe_mx_weights, down: moe_mx_weights, top_k, n_tokens, x, residual, gain, eps,
+                         topk_ids, topk_weight, x_global, h_global, sum_out, out, ws, out_is_fp32=False, stream=None):
+    st = load_library().moe_mx_layer_forward(ctypes.byref(gate_up), ctypes.byref(down), top_k, n_tokens, _ptr(x),
+                                             _ptr(residual), _ptr(gain), float(eps), _ptr(topk_ids),
+                                             _ptr(topk_weight), _ptr(x_global), _ptr(h_global), _ptr(sum_out),
+                                             _ptr(out), int(bool(out_is_fp32)), _ptr(ws),
+                                             ws.numel() * ws.element_size(), _stream(stream))
+    _check(st, "moe_mx_layer_forward")
+
+
 # ---------------------------------------------------------------- allocating conveniences
 
 class TiledBank:
@@ -394,3 +503,290 @@ def layer_forward(hidden, gain, eps, topk_ids, topk_weight, bank, shared=None, w
     moe_layer_forward(dm, n, hidden, gain, eps, topk_ids, topk_weight, weights(bank),
                       weights(shared) if shared is not None else None, dff_sh, out, ws, out_is_fp32, stream)
     return out
+
+
+# ---------------------------------------------------------------- microscaled formats
+
+class MxRows:
+    """Rows of `cols` columns in a microscaled format: uint8 codes [rows, .] and scales [rows, pitch] (None for
+    bf16), and NVFP4's fp32 factor [1] (None = 1)."""
+
+    def __init__(self, fmt, cols, codes, scales=None, global_scale=None):
+        self.fmt, self.cols, self.codes, self.scales, self.global_scale = fmt, cols, codes, scales, global_scale
+
+    @property
+    def rows(self):
+        return self.codes.shape[0]
+
+
+class MxWeights:
+    """Experts' matrices [num_experts, n_out, k] (two of them, gate and up, with swiglu) in the packed layout;
+    alpha, alpha_up: fp32 [num_experts] factors of the products (None = 1)."""
+
+    def __init__(self, fmt, num_experts, n_out, k, packed, alpha=None, alpha_up=None, swiglu=False):
+        self.fmt, self.num_experts, self.n_out, self.k = fmt, num_experts, n_out, k
+        self.packed, self.alpha, self.alpha_up, self.swiglu = packed, alpha, alpha_up, bool(swiglu)
+
+    def struct(self) -> moe_mx_weights:
+        p = [t.data_ptr() if t is not None else None for t in (self.packed, self.alpha, self.alpha_up)]
+        return moe_mx_weights(self.fmt, self.num_experts, self.n_out, self.k, int(self.swiglu), *p)
+
+
+def _on_stream(fn):
+    """What the call allocates (results, a workspace of its own) belongs to the stream that it launches on."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        import torch
+        if stream is None:
+            return fn(*args, **kw)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _mx_want(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _mx_tensor(t, name, dtype, shape, device):
+    """The tensor that a library call reads through its pointer: dense, on the device, of this type and shape."""
+    _mx_want(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous() and t.device == device,
+             f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
+             f"{tuple(t.shape)} on {t.device}")
+
+
+def _mx_strided(t, name, shape, device):
+    import torch
+    _mx_want(t.dtype == torch.bfloat16 and tuple(t.shape) == tuple(shape) and t.device == device
+             and (shape[1] == 1 or t.stride(1) == 1), f"{name}: expected bf16 rows {tuple(shape)} on {device}")
+
+
+def _ld(t):
+    # the stride of a single row is not used, and torch may report any
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _mx_scalar(t, name, device, count=1):
+    import torch
+    if t is not None:
+        _mx_want(t.dtype == torch.float32 and t.numel() == count and t.is_contiguous() and t.device == device,
+                 f"{name}: expected {count} fp32 value(s) on {device}")
+
+
+def _mx_check_rows(r: MxRows):
+    import torch
+    dev = r.codes.device
+    cb = moe_mx_code_bytes(r.fmt, r.cols)
+    if cb == 0:
+        raise MoeError(2, "moe_mx_code_bytes")
+    _mx_tensor(r.codes, "codes", torch.uint8, (r.rows, cb), dev)
+    if r.fmt != MOE_MX_BF16:
+        _mx_want(r.scales is not None, "scales: missing")
+        _mx_tensor(r.scales, "scales", torch.uint8, (r.rows, moe_mx_scale_pitch(r.fmt, r.cols)), dev)
+    _mx_scalar(r.global_scale, "global_scale", dev)
+
+
+def _mx_check_weights(w: MxWeights, dev):
+    nbytes = moe_mx_packed_bytes(w.struct())
+    if nbytes == 0:
+        raise MoeError(2, "moe_mx_packed_bytes")
+    _mx_want(w.packed.numel() * w.packed.element_size() == nbytes and w.packed.is_contiguous()
+             and w.packed.device == dev, f"packed: expected {nbytes} contiguous bytes on {dev}")
+    _mx_scalar(w.alpha, "alpha", dev, w.num_experts)
+    _mx_scalar(w.alpha_up, "alpha_up", dev, w.num_experts)
+
+
+def mx_rows(fmt, rows, cols, device="cuda", global_scale=None) -> MxRows:
+    """Uninitialised rows."""
+    import torch
+    cb = moe_mx_code_bytes(fmt, cols)
+    if cb == 0:
+        raise MoeError(2, "moe_mx_code_bytes")
+    codes = torch.empty(rows, cb, dtype=torch.uint8, device=device)
+    scales = None
+    if fmt != MOE_MX_BF16:
+        scales = torch.empty(rows, moe_mx_scale_pitch(fmt, cols), dtype=torch.uint8, device=device)
+    return MxRows(fmt, cols, codes, scales, global_scale)
+
+
+def _mx_positions(positions, n, out_rows, device):
+    import torch
+    if positions is None:
+        return 1, n if out_rows is None else out_rows
+    _mx_want(positions.dim() == 2, "positions: expected [n, k]")
+    _mx_tensor(positions, "positions", torch.int32, (n, positions.shape[1]), device)
+    return positions.shape[1], positions.numel() if out_rows is None else out_rows
+
+
+@_on_stream
+def mx_quantise(x, fmt, positions=None, out_rows=None, global_scale=None, out: Optional[MxRows] = None) -> MxRows:
+    """bf16 rows x [n, d] (any row stride that is a multiple of 8) into a format; row t goes to each of positions[t]
+    (int32 [n, k], default its own place) of `out` (out_rows rows, default n * k)."""
+    n, d = x.shape
+    dev = x.device
+    _mx_strided(x, "x", (n, d), dev)
+    _mx_scalar(global_scale, "global_scale", dev)
+    k, m = _mx_positions(positions, n, out_rows if out is None else out.rows, dev)
+    if out is None:
+        out = mx_rows(fmt, m, d, dev)
+    out.global_scale = global_scale
+    _mx_want(out.fmt == fmt and out.cols == d and out.codes.device == dev, "out: of another format, width or device")
+    _mx_check_rows(out)
+    moe_mx_quantise(fmt, n, k, d, x, _ld(x), positions, global_scale, m, out.codes, out.scales)
+    return out
+
+
+@_on_stream
+def mx_add_rmsnorm(x, residual, gain, eps, fmt, positions=None, out_rows=None, global_scale=None, sum_out=None,
+                   out: Optional[MxRows] = None):
+    """(rows of the normalised sum, the sum): sum = bf16(x + residual) (residual may be None), rows = Q(rmsnorm(sum))
+    written as by mx_quantise.  sum_out may be x or residual."""
+    import torch
+    n, d = x.shape
+    dev = x.device
+    _mx_strided(x, "x", (n, d), dev)
+    if residual is not None:
+        _mx_strided(residual, "residual", (n, d), dev)
+    _mx_tensor(gain, "gain", torch.bfloat16, (d,), dev)
+    _mx_scalar(global_scale, "global_scale", dev)
+    k, m = _mx_positions(positions, n, out_rows if out is None else out.rows, dev)
+    if out is None:
+        out = mx_rows(fmt, m, d, dev)
+    out.global_scale = global_scale
+    _mx_want(out.fmt == fmt and out.cols == d and out.codes.device == dev, "out: of another format, width or device")
+    _mx_check_rows(out)
+    r_ld = _ld(residual) if residual is not None else d
+    if sum_out is None:
+        sum_out = torch.empty_strided((n, d), (r_ld, 1), dtype=torch.bfloat16, device=dev)
+    _mx_strided(sum_out, "sum_out", (n, d), dev)
+    if residual is None:
+        r_ld = _ld(sum_out)
+    _mx_want(_ld(sum_out) == r_ld or n == 1, "sum_out: its row stride differs from residual's")
+    moe_mx_add_rmsnorm(fmt, n, k, d, x, _ld(x), residual, r_ld, gain, eps, positions, global_scale, m, sum_out,
+                       out.codes, out.scales)
+    return out, sum_out
+
+
+@_on_stream
+def mx_dequantise(r: MxRows, out=None):
+    """bf16 values of rows."""
+    import torch
+    _mx_check_rows(r)
+    if out is None:
+        out = torch.empty(r.rows, r.cols, dtype=torch.bfloat16, device=r.codes.device)
+    _mx_strided(out, "out", (r.rows, r.cols), r.codes.device)
+    moe_mx_dequantise(r.fmt, r.rows, r.cols, r.codes, r.scales, r.global_scale, out, _ld(out))
+    return out
+
+
+@_on_stream
+def mx_pack(rows: MxRows, num_experts, up: Optional[MxRows] = None, alpha=None, alpha_up=None) -> MxWeights:
+    """Packed weights from rows [num_experts * n_out] of a format (up: the SwiGLU pair's second matrix)."""
+    import torch
+    _mx_check_rows(rows)
+    _mx_want(num_experts >= 1 and rows.rows % num_experts == 0, "rows: not a multiple of num_experts")
+    dev = rows.codes.device
+    if up is not None:
+        _mx_check_rows(up)
+        _mx_want((up.fmt, up.cols, up.rows, up.codes.device) == (rows.fmt, rows.cols, rows.rows, dev),
+                 "up: not like the first matrix")
+    w = MxWeights(rows.fmt, num_experts, rows.rows // num_experts, rows.cols, None, alpha, alpha_up, up is not None)
+    nbytes = moe_mx_packed_bytes(w.struct())
+    if nbytes == 0:
+        raise MoeError(2, "moe_mx_packed_bytes")
+    w.packed = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _mx_check_weights(w, dev)
+    moe_mx_pack_weights(w.struct(), rows.codes, rows.scales, up.codes if up else None, up.scales if up else None,
+                        w.packed)
+    return w
+
+
+def _mx_operands(x: MxRows, w: MxWeights, offsets):
+    import torch
+    _mx_check_rows(x)
+    dev = x.codes.device
+    _mx_check_weights(w, dev)
+    _mx_want(x.fmt == w.fmt and x.cols == w.k, "x: of another format or width than the weights")
+    _mx_tensor(offsets, "offsets", torch.int32, (w.num_experts + 1,), dev)
+    return dev
+
+
+def mx_workspace(device="cuda"):
+    import torch
+    return torch.zeros(MOE_MX_PRODUCT_WORKSPACE, dtype=torch.uint8, device=device)
+
+
+@_on_stream
+def mx_grouped_product(x: MxRows, w: MxWeights, offsets, out=None, out_pos=None, row_weight=None, ws=None,
+                       out_type=MOE_MX_OUT_BF16):
+    """out[p(r)] = row_weight[p(r)] * x[r] W_e^T for the rows offsets[e] .. offsets[e + 1] - 1 of each expert e;
+    p = out_pos (int32 [rows], default r)."""
+    import torch
+    dev = _mx_operands(x, w, offsets)
+    dtype = torch.float16 if out_type == MOE_MX_OUT_F16 else torch.bfloat16
+    if out is None:
+        out = torch.empty(x.rows, w.n_out, dtype=dtype, device=dev)
+    _mx_want(out.dtype == dtype and out.dim() == 2 and out.shape[1] == w.n_out and out.device == dev
+             and (w.n_out == 1 or out.stride(1) == 1), "out: of another type, width or device")
+    if out_pos is not None:
+        _mx_tensor(out_pos, "out_pos", torch.int32, (x.rows,), dev)
+    _mx_scalar(row_weight, "row_weight", dev, out.shape[0])
+    if ws is None:
+        ws = mx_workspace(dev)
+    moe_mx_grouped_product(w.struct(), x.rows, x.codes, x.scales, x.global_scale, offsets, out, out_type, out.shape[0],
+                           _ld(out), out_pos, row_weight, ws)
+    return out
+
+
+@_on_stream
+def mx_grouped_swiglu(x: MxRows, w: MxWeights, offsets, h_global=None, out: Optional[MxRows] = None, ws=None) -> MxRows:
+    """Rows of silu(x Wg_e^T) * (x Wu_e^T) in the format of x."""
+    dev = _mx_operands(x, w, offsets)
+    _mx_scalar(h_global, "h_global", dev)
+    if out is None:
+        out = mx_rows(w.fmt, x.rows, w.n_out, dev)
+    out.global_scale = h_global
+    _mx_want(out.fmt == w.fmt and out.cols == w.n_out and out.rows == x.rows and out.codes.device == dev,
+             "out: of another format, shape or device")
+    _mx_check_rows(out)
+    if ws is None:
+        ws = mx_workspace(dev)
+    moe_mx_grouped_swiglu(w.struct(), x.rows, x.codes, x.scales, x.global_scale, offsets, h_global, out.codes,
+                          out.scales, ws)
+    return out
+
+
+@_on_stream
+def mx_layer_forward(x, residual, gain, eps, topk_ids, topk_weight, gate_up: MxWeights, down: MxWeights,
+                     x_global=None, h_global=None, ws=None, out_is_fp32=False):
+    """The MoE block on microscaled experts: (sum, out) with sum = bf16(x + residual) and out = sum + the routed
+    experts on rmsnorm(sum); with gain None (and residual None) (None, the routed experts on x)."""
+    import torch
+    n, d = x.shape
+    dev = x.device
+    _mx_tensor(x, "x", torch.bfloat16, (n, d), dev)
+    _mx_want(d == gate_up.k, "x: of another width than the experts")
+    if residual is not None:
+        _mx_tensor(residual, "residual", torch.bfloat16, (n, d), dev)
+    if gain is not None:
+        _mx_tensor(gain, "gain", torch.bfloat16, (d,), dev)
+    _mx_tensor(topk_ids, "topk_ids", torch.int32, (n, topk_ids.shape[1]), dev)
+    _mx_tensor(topk_weight, "topk_weight", torch.float32, tuple(topk_ids.shape), dev)
+    _mx_check_weights(gate_up, dev)
+    _mx_check_weights(down, dev)
+    _mx_scalar(x_global, "x_global", dev)
+    _mx_scalar(h_global, "h_global", dev)
+    gs, ds, k = gate_up.struct(), down.struct(), topk_ids.shape[1]
+    if ws is None:
+        nbytes = moe_mx_layer_workspace_size(gs, ds, k, n)
+        if nbytes == 0:
+            raise MoeError(2, "moe_mx_layer_workspace_size")
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    total = torch.empty(n, d, dtype=torch.bfloat16, device=dev) if gain is not None else None
+    out = torch.empty(n, d, dtype=torch.float32 if out_is_fp32 else torch.bfloat16, device=dev)
+    moe_mx_layer_forward(gs, ds, k, n, x, residual, gain, eps, topk_ids, topk_weight, x_global, h_global, total, out,
+                         ws, out_is_fp32)
+    return total, out

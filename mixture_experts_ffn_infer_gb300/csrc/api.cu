@@ -389,6 +389,23 @@ moe_status shared_pass(const moe_dims* d, int64_t n, const moe_weights* w, int32
 }
 
 }  // namespace
+
+// [rows][row_bytes] of bytes, box 128 bytes x box_rows, 128-byte swizzle; reads past
+// either end give zeros (mx_gemm.cu's rows).
+bool encode_rows_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows) {
+  EncodeFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {row_bytes, rows};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int device_sms() { return num_sms(); }
+
 }  // namespace moe
 
 // Scratch of moe_infer_static: a fixed device array in this library, so that

@@ -1,0 +1,673 @@
+// Products grouped by expert on microscaled operands (moe_mx.h).
+//
+//   D[r][n] = sum_k X[r][k] W_e[n][k],  X = codes * scales, W = codes * scales
+//
+// The tensor core multiplies the codes and applies both operands' scales inside
+// the product (tcgen05.mma block_scale, fp32 accumulators), so nothing is widened
+// on chip: a byte of weights read from HBM is a byte the tensor core consumes.
+//
+//  * Unit = a tile of up to 128 rows of one expert x one packed block row (256
+//    weight rows, or 128 gate + 128 up): M = 128 rows, N = 256.  Rows are the M
+//    side whatever their number: padding one token to 128 costs tensor time only,
+//    and at these rates (a 32 KB weight block is 4 MMAs of 128 cycles) less than
+//    half of what its bytes take from HBM.
+//  * A chunk is 128 bytes of codes along K: one bulk copy brings the packed weight
+//    block with its scales (33 to 36 KB), one TMA box the tile's rows.  Four stages.
+//  * Weight scales go from shared to tensor memory by tcgen05.cp (the packed order is
+//    the one it wants).  Row scales start at any row, so no copy shape fits them:
+//    warps 4-7 read them from global memory, each for its own 32-lane quarter (the
+//    tensor core wants them in all four), and store them with tcgen05.st, four chunks
+//    in flight.  Each stage has its own scale columns, so a stage's barrier covers them.
+//  * One accumulator of 256 columns beside the scales (bf16: two, no scales).  The
+//    epilogue empties it into registers, 128 columns a thread, and releases it before
+//    it computes, so the next unit's products wait for the read alone.
+//  * An epilogue thread owns a row and 64 + 64 weight rows: gate and up of the same
+//    64 features, whose groups of 16 or 32 lie within the thread.
+//
+// Warps (512 threads, one CTA per SM, persistent over units):
+//   0 weight copies   1 MMA issue   2 row copies   3 idle   4-7 row scales   8-15 epilogue
+// Within an expert up to eight tiles run a weight block one after another, so that
+// they take place at the same time and share it through L2.  Every wait is bounded
+// (common.cuh); after one gives up all roles drain and the kernel ends.
+#include "mx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kStages = 4;
+constexpr int kTile = 128;
+constexpr int kMaxExperts = 1024;
+constexpr int kChunkTiles = 8;
+constexpr int kABytes = kTile * 128;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kWarpWeights = 0, kWarpIssue = 1, kWarpRows = 2, kWarpScales = 4, kWarpEpi = 8;
+constexpr int kRegsLow = 56, kRegsScales = 104, kRegsEpi = 176;
+static_assert(128 * (kRegsLow + kRegsScales + 2 * kRegsEpi) <= 65536, "register split");
+
+template <int FMT>
+struct Cfg {
+  static constexpr int kWords = Mx<FMT>::words;
+  static constexpr int kWBytes = kMxCodeBlock + 1024 * kWords;
+  static constexpr int kStage = kWBytes + kABytes;
+  static constexpr int kAcc = FMT == MOE_MX_BF16 ? 2 : 1;
+  static constexpr uint32_t kScaleCols = 12 * kWords;  // 4 words columns of row scales, 8 of weight scales
+  static constexpr int kNumBars = 2 * kStages + 2 * kAcc + 1;
+  static constexpr int kBarOff = kStages * kStage;
+  static constexpr int kPlanOff = kBarOff + kNumBars * 8 + 16;  // tile prefix, row starts
+  static constexpr int kSmem = 1024 + kPlanOff + 2 * (kMaxExperts + 1) * 4 + 64 * 4;
+  static_assert(kStage % 1024 == 0, "operand tiles stay 1024-byte aligned");
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+  static_assert(256 * kAcc + kStages * kScaleCols <= kTmemCols, "tensor memory");
+};
+
+struct Args {
+  const uint8_t* packed;
+  const float* alpha;
+  const float* alpha_up;
+  int32_t experts, n_out, upt, chunks, groups;  // upt: packed block rows; groups: scales of a row
+  int32_t rows;
+  const uint8_t* x_scales;
+  int64_t x_pitch;
+  const float* x_global;
+  const int32_t* offsets;
+  void* out;
+  int32_t out_f16, out_vec;
+  int64_t out_rows, out_ld;
+  const int32_t* out_pos;
+  const float* row_weight;
+  const float* h_global;
+  uint8_t* h_codes;
+  uint8_t* h_scales;
+  int64_t h_row_bytes, h_pitch;
+  uint32_t* err;
+  int32_t overlap;
+};
+
+// Rows' maps with boxes of 16, 32, 64 and 128 rows: a tile's copy brings its own
+// rows and few others.
+struct RowMaps {
+  CUtensorMap box[4];
+};
+
+__device__ __forceinline__ void mma_block_scaled_nv(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
+                                                    uint32_t sb, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_block_scaled_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
+                                                     uint32_t sb, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_block_scaled_mx8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
+                                                     uint32_t sb, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// 32 rows x 16 bytes of shared memory to four tensor-memory columns, in all four lane quarters.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Descriptor of 512 contiguous bytes as 32 rows of 16: no swizzle, groups of 8 rows 128 bytes apart.
+__device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(128 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  return d;
+}
+
+// Instruction descriptors, M = 128, N = 256, both operands K-major.  Block-scaled
+// kinds: formats at bits 7 and 10 (e4m3 0; e2m1 1), N / 8 at 17, the scales' type at
+// 23 (e4m3 0, e8m0 1), M / 16 at 24, and which byte (1X) or half (2X) of the 4-byte
+// scale column an MMA reads at 4 (B) and 29 (A).
+template <int FMT>
+__device__ __forceinline__ constexpr uint32_t idesc_of(int kk) {
+  constexpr uint32_t mn = (static_cast<uint32_t>(256 >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+  if constexpr (FMT == MOE_MX_BF16) return mn | (1u << 4) | (1u << 7) | (1u << 10);
+  else if constexpr (FMT == MOE_MX_MXFP8)
+    return mn | (1u << 23) | (static_cast<uint32_t>(kk) << 4) | (static_cast<uint32_t>(kk) << 29);
+  else if constexpr (FMT == MOE_MX_MXFP4)
+    return mn | (1u << 23) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(2 * (kk & 1)) << 4) |
+           (static_cast<uint32_t>(2 * (kk & 1)) << 29);
+  else return mn | (1u << 7) | (1u << 10);
+}
+
+template <int FMT>
+__device__ __forceinline__ void issue_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t sa, uint32_t sb, int kk,
+                                          uint32_t acc) {
+  if constexpr (FMT == MOE_MX_BF16) mma_bf16(d, a, b, idesc_of<FMT>(kk), acc);
+  else if constexpr (FMT == MOE_MX_MXFP8) mma_block_scaled_mx8(d, a, b, idesc_of<FMT>(kk), sa, sb, acc);
+  else if constexpr (FMT == MOE_MX_MXFP4)
+    mma_block_scaled_mx4(d, a, b, idesc_of<FMT>(kk), sa + 4 * (kk >> 1), sb + 8 * (kk >> 1), acc);
+  else mma_block_scaled_nv(d, a, b, idesc_of<FMT>(kk), sa + 4 * kk, sb + 8 * kk, acc);
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t c0, int32_t c1,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+template <int COLS>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[COLS]) {
+  if constexpr (COLS == 16) {
+    tmem_st16(taddr, r);
+  } else if constexpr (COLS == 8) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  } else {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+  }
+}
+
+__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (clock64() - t0 > kWaitLimitCycles) return;
+}
+
+// silu(g) = g / (1 + e^-g); for g < -87 the denominator overflows and the result is 0.
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
+struct Unit {
+  int e, row0, nv, u;
+};
+
+// Unit number x.  Expert e's units are consecutive, T tiles x upt block rows: its
+// tiles in chunks of eight, block row after block row within a chunk, tile after
+// tile within a block row.
+__device__ __forceinline__ Unit unit_of(const int32_t* first_tile, const int32_t* row_at, int experts, int upt, int x) {
+  const int t = x / upt;
+  int lo = 0, hi = experts;  // first_tile[lo] <= t < first_tile[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first_tile[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  const int l = x - first_tile[lo] * upt, tiles = first_tile[lo + 1] - first_tile[lo];
+  const int chunk = l / (kChunkTiles * upt), in = l - chunk * kChunkTiles * upt;
+  const int nc = min(kChunkTiles, tiles - chunk * kChunkTiles);
+  const int tile = chunk * kChunkTiles + in % nc;
+  Unit un;
+  un.e = lo;
+  un.u = in / nc;
+  un.row0 = row_at[lo] + tile * kTile;
+  un.nv = min(kTile, row_at[lo + 1] - un.row0);
+  return un;
+}
+
+template <int FMT, bool SWIGLU>
+__global__ void __launch_bounds__(kThreads, 1)
+mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
+  using C = Cfg<FMT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::kBarOff;
+  auto full = [&](int i) { return bar0 + 8u * i; };
+  auto empty = [&](int i) { return bar0 + 8u * (kStages + i); };
+  auto acc_full = [&](int i) { return bar0 + 8u * (2 * kStages + i); };
+  auto acc_empty = [&](int i) { return bar0 + 8u * (2 * kStages + C::kAcc + i); };
+  const uint32_t drain_bar = bar0 + 8u * (C::kNumBars - 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + C::kNumBars * 8);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  int32_t* first_tile = reinterpret_cast<int32_t*>(smem + C::kPlanOff);
+  int32_t* row_at = first_tile + kMaxExperts + 1;
+  int32_t* warp_sum = row_at + kMaxExperts + 1;
+
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(full(i), FMT == MOE_MX_BF16 ? 2 : 6);  // weights, rows (and the four scale warps)
+      mbar_init(empty(i), 1);
+    }
+    for (int i = 0; i < C::kAcc; ++i) {
+      mbar_init(acc_full(i), 1);
+      mbar_init(acc_empty(i), 8);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == kWarpRows && lane < 4) prefetch_tmap(&maps.box[lane]);
+  if (warp == kWarpIssue) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  if (!a.overlap) pdl_wait();  // else only what the kernel in front writes is waited for, by its readers
+  // The tile plan: thread i counts the tiles of experts 2 i and 2 i + 1.
+  {
+    int n[2] = {0, 0};
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int e = 2 * threadIdx.x + j;
+      if (e < a.experts) {
+        const int lo = __ldg(a.offsets + e), hi = __ldg(a.offsets + e + 1);
+        bad |= lo < 0 || hi < lo || hi > a.rows;
+        n[j] = bad ? 0 : (hi - lo + kTile - 1) / kTile;
+        row_at[e] = lo;
+        if (e == a.experts - 1) row_at[e + 1] = hi;
+      }
+    }
+    const int mine = n[0] + n[1];
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    bad = __syncthreads_or(bad);
+    int base = 0;
+    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    const int excl = base + incl - mine;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int e = 2 * threadIdx.x + j;
+      if (e < a.experts) {
+        first_tile[e + 1] = bad ? 0 : excl + n[0] + (j ? n[1] : 0);
+        if (e == 0) first_tile[0] = 0;
+      }
+    }
+    if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, DEV_ERR_ROUTING);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int upt = a.upt, chunks = a.chunks;
+  const int total = first_tile[a.experts] * upt;
+  const int stride = gridDim.x;
+  auto unit_at = [&](int x) { return unit_of(first_tile, row_at, a.experts, upt, x); };
+
+  if (warp < kWarpScales) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+    if (warp == kWarpWeights) {
+      if (lane == 0) {
+        const uint64_t pol = policy_evict_first();
+        uint32_t it = 0;
+        bool ok = true;
+        for (int x = blockIdx.x; ok && x < total; x += stride) {
+          const Unit un = unit_at(x);
+          const uint8_t* src = a.packed + (static_cast<int64_t>(un.e) * upt + un.u) * chunks * C::kWBytes;
+          for (int c = 0; c < chunks; ++c, ++it) {
+            const int s = it % kStages;
+            if (!wait_bounded(empty(s), ((it / kStages) & 1) ^ 1, abort_flag, a.err)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(full(s), C::kWBytes);
+            bulk_load(sbase + s * C::kStage, src + static_cast<int64_t>(c) * C::kWBytes, C::kWBytes, full(s), pol);
+          }
+        }
+        if (!ok)
+          for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) wait_drain(full(i % kStages), (i / kStages) & 1);
+      }
+      __syncwarp();
+    } else if (warp == kWarpRows) {
+      if (a.overlap) pdl_wait();
+      if (lane == 0) {
+        const uint64_t pol = policy_evict_last();
+        uint32_t it = 0;
+        bool ok = true;
+        for (int x = blockIdx.x; ok && x < total; x += stride) {
+          const Unit un = unit_at(x);
+          const int b = un.nv <= 16 ? 0 : un.nv <= 32 ? 1 : un.nv <= 64 ? 2 : 3;
+          const uint32_t bytes = (16u << b) * 128u;
+          for (int c = 0; c < chunks; ++c, ++it) {
+            const int s = it % kStages;
+            if (!wait_bounded(empty(s), ((it / kStages) & 1) ^ 1, abort_flag, a.err)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(full(s), bytes);
+            tma_load_2d(sbase + s * C::kStage + C::kWBytes, &maps.box[b], full(s), c * 128, un.row0, pol);
+          }
+        }
+        if (!ok)
+          for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) wait_drain(full(i % kStages), (i / kStages) & 1);
+      }
+      __syncwarp();
+    } else if (warp == kWarpIssue) {
+      if (elect_one()) {
+        uint32_t it = 0, ui = 0;
+        bool ok = true;
+        for (int x = blockIdx.x; ok && x < total; x += stride, ++ui) {
+          const int ab = ui % C::kAcc;
+          if (!wait_bounded(acc_empty(ab), ((ui / C::kAcc) & 1) ^ 1, abort_flag, a.err)) break;
+          const uint32_t d = tmem + 256u * ab;
+          for (int c = 0; c < chunks; ++c, ++it) {
+            const int s = it % kStages;
+            if (!wait_bounded(full(s), (it / kStages) & 1, abort_flag, a.err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t w = sbase + s * C::kStage;
+            const uint32_t sa = tmem + 256u * C::kAcc + s * C::kScaleCols, sb = sa + 4u * C::kWords;
+            if constexpr (FMT != MOE_MX_BF16) {
+              const uint64_t sd = desc_scales(w + kMxCodeBlock);
+#pragma unroll
+              for (int i = 0; i < 2 * C::kWords; ++i) tmem_copy_scales(sb + 4 * i, desc_advance(sd, 512 * i));
+            }
+            const uint64_t ad = desc_kmajor_sw128(w + C::kWBytes), bd = desc_kmajor_sw128(w);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              issue_mma<FMT>(d, desc_advance(ad, 32 * kk), desc_advance(bd, 32 * kk), sa, sb, kk, c > 0 || kk > 0);
+            tc_commit(empty(s));
+          }
+          if (ok) tc_commit(acc_full(ab));
+        }
+        tc_commit(drain_bar);  // every MMA issued above has completed once this arrives
+        wait_drain(drain_bar, 0);
+      }
+      __syncwarp();
+    }
+  } else if (warp < kWarpEpi) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsScales));
+    if constexpr (FMT != MOE_MX_BF16) {
+      pdl_wait();
+      constexpr int W = C::kWords;
+      const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t cols = tmem + quarter + 256u * C::kAcc;
+      // what is loaded runs four chunks ahead of what is stored
+      int lx = blockIdx.x, lc = 0;
+      Unit un{};
+      uint32_t buf[4][4 * W];
+      auto load = [&](uint32_t (&r)[4 * W]) {
+        if (lx >= total) return;
+        if (lc == 0) un = unit_at(lx);
+        const int left = a.groups - lc * 4 * W;  // scales of this chunk that exist
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint32_t w[W];
+#pragma unroll
+          for (int i = 0; i < W; ++i) w[i] = 0;
+          if (32 * b + lane < un.nv) {
+            const uint8_t* p = a.x_scales + (static_cast<int64_t>(un.row0) + 32 * b + lane) * a.x_pitch + lc * 4 * W;
+            if constexpr (W == 4) {
+              const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+              w[0] = q.x;
+              w[1] = q.y;
+              w[2] = q.z;
+              w[3] = q.w;
+            } else if constexpr (W == 2) {
+              const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+              w[0] = q.x;
+              w[1] = q.y;
+            } else {
+              w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < W; ++i) r[4 * i + b] = w[i];
+        }
+        if (left < 4 * W) {  // the row's last chunk: bytes past its scales are padding
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            const int k = left - 4 * i;
+            const uint32_t mask = k >= 4 ? 0xffffffffu : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) r[4 * i + b] &= mask;
+          }
+        }
+        if (++lc == chunks) {
+          lc = 0;
+          lx += stride;
+        }
+      };
+      const int64_t mine = blockIdx.x < total ? (total - 1 - static_cast<int>(blockIdx.x)) / stride + 1 : 0;
+      const int64_t iters = mine * chunks;
+      bool ok = true;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) load(buf[j]);
+      for (int64_t it = 0; ok && it < iters; it += 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (ok && it + j < iters) {
+            // stage j: kStages == 4
+            ok = __all_sync(0xffffffffu, wait_bounded(empty(j), ((it / 4) & 1) ^ 1, abort_flag, a.err));
+            if (ok) {
+              tc_fence_after();
+              tmem_st_cols<4 * W>(cols + j * C::kScaleCols, buf[j]);
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(full(j));
+              load(buf[j]);
+            }
+          }
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+    if (a.overlap) pdl_wait();
+    const int q = warp & 3, hf = (warp - kWarpEpi) >> 2;
+    const int tok = q * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+    const float xg = a.x_global ? __ldg(a.x_global) : 1.f;
+    const float hg = SWIGLU && a.h_global ? __ldg(a.h_global) : 1.f;
+    uint32_t ui = 0;
+    for (int x = blockIdx.x; x < total; x += stride, ++ui) {
+      const Unit un = unit_at(x);
+      const bool valid = tok < un.nv;
+      const int64_t row = static_cast<int64_t>(un.row0) + tok;
+      const float f0 = xg * (a.alpha ? __ldg(a.alpha + un.e) : 1.f);
+      float f1 = f0;
+      int64_t dst = row;
+      if constexpr (SWIGLU) {
+        f1 = xg * (a.alpha_up ? __ldg(a.alpha_up + un.e) : 1.f);
+      } else {
+        if (valid && a.out_pos) dst = __ldg(a.out_pos + row);
+      }
+      const bool store = valid && (SWIGLU || (dst >= 0 && dst < a.out_rows));
+      float wgt = 1.f;
+      if (!SWIGLU && store && a.row_weight) wgt = __ldg(a.row_weight + dst);
+      const int ab = ui % C::kAcc;
+      if (!__all_sync(0xffffffffu, wait_bounded(acc_full(ab), (ui / C::kAcc) & 1, abort_flag, a.err))) break;
+      tc_fence_after();
+      const uint32_t tcol = tmem + lane_base + 256u * ab + 64u * hf;
+      uint32_t p0[64], p1[64];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        tmem_ld16(tcol + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(&p0[16 * i]));
+        tmem_ld16(tcol + 128 + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(&p1[16 * i]));
+      }
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty(ab));
+      bool overflow = false;
+      if constexpr (SWIGLU) {
+        const int n0 = 128 * un.u + 64 * hf;  // first of this thread's 64 features
+        if (store && n0 < a.n_out) {
+          uint8_t* hc = a.h_codes + row * a.h_row_bytes;
+          uint8_t* hs = a.h_scales + row * a.h_pitch;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (n0 + 32 * half < a.n_out) {
+              const int at = n0 + 32 * half;
+              float h[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                h[i] = silu(__uint_as_float(p0[32 * half + i]) * f0) * (__uint_as_float(p1[32 * half + i]) * f1);
+              if constexpr (FMT == MOE_MX_BF16) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                  *reinterpret_cast<uint4*>(hc + 2 * at + 16 * v) =
+                      make_uint4(pack_bf16(h[8 * v], h[8 * v + 1]), pack_bf16(h[8 * v + 2], h[8 * v + 3]),
+                                 pack_bf16(h[8 * v + 4], h[8 * v + 5]), pack_bf16(h[8 * v + 6], h[8 * v + 7]));
+              } else {
+                constexpr int G = Mx<FMT>::group;
+                uint32_t out[8];
+                uint32_t sbytes = 0;
+#pragma unroll
+                for (int g = 0; g < 32 / G; ++g) {
+                  uint32_t m = 0;
+#pragma unroll
+                  for (int i = 0; i < G; ++i) m = max(m, abs_bits(h[G * g + i]));
+                  const GroupScale sc = group_scale<FMT>(m, hg);
+                  sbytes |= sc.byte << (8 * g);
+#pragma unroll
+                  for (int v = 0; v < G / 8; ++v) {
+                    uint32_t w[2];
+                    codes8<FMT>(*reinterpret_cast<const float(*)[8]>(&h[G * g + 8 * v]), sc, w);
+                    if constexpr (FMT == MOE_MX_MXFP8) {
+                      out[2 * v] = w[0];
+                      out[2 * v + 1] = w[1];
+                    } else {
+                      out[(G / 8) * g + v] = w[0];
+                    }
+                  }
+                }
+                if constexpr (FMT == MOE_MX_MXFP8) {
+                  *reinterpret_cast<uint4*>(hc + at) = make_uint4(out[0], out[1], out[2], out[3]);
+                  *reinterpret_cast<uint4*>(hc + at + 16) = make_uint4(out[4], out[5], out[6], out[7]);
+                } else {
+                  *reinterpret_cast<uint4*>(hc + at / 2) = make_uint4(out[0], out[1], out[2], out[3]);
+                }
+                if constexpr (G == 16) *reinterpret_cast<uint16_t*>(hs + at / 16) = static_cast<uint16_t>(sbytes);
+                else hs[at / 32] = static_cast<uint8_t>(sbytes);
+              }
+            }
+          }
+        }
+      } else if (store) {
+        uint16_t* o = static_cast<uint16_t*>(a.out) + dst * a.out_ld;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int n0 = 256 * un.u + 128 * m + 64 * hf;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int at = n0 + 16 * v;
+            if (at < a.n_out) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t r0 = m ? p1[16 * v + 2 * i] : p0[16 * v + 2 * i];
+                const uint32_t r1 = m ? p1[16 * v + 2 * i + 1] : p0[16 * v + 2 * i + 1];
+                const float y0 = __uint_as_float(r0) * f0 * wgt, y1 = __uint_as_float(r1) * f0 * wgt;
+                if (a.out_f16) {
+                  overflow |= (fabsf(y0) >= 65520.f) || (fabsf(y1) >= 65520.f && at + 2 * i + 1 < a.n_out);
+                  const __half2 h2 = __floats2half2_rn(y0, y1);
+                  w[i] = *reinterpret_cast<const uint32_t*>(&h2);
+                } else {
+                  w[i] = pack_bf16(y0, y1);
+                }
+              }
+              if (a.out_vec && at + 16 <= a.n_out) {
+                stg256(o + at, w);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  if (at + 2 * i < a.n_out) o[at + 2 * i] = static_cast<uint16_t>(w[i]);
+                  if (at + 2 * i + 1 < a.n_out) o[at + 2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+                }
+              }
+            }
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, overflow) && lane == 0) atomicOr(a.err, DEV_ERR_RANGE);
+    }
+  }
+  __syncthreads();
+  if (warp == kWarpIssue) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int FMT, bool SWIGLU>
+cudaError_t launch(const MxProductLaunch& g, cudaStream_t s) {
+  using C = Cfg<FMT>;
+  auto kern = mx_product_kernel<FMT, SWIGLU>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  // an increase of the register split that cannot be met never returns
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs * kThreads < 128 * (kRegsLow + kRegsScales + 2 * kRegsEpi)) return cudaErrorInvalidConfiguration;
+  const moe_mx_weights* w = g.w;
+  Args a{};
+  a.packed = static_cast<const uint8_t*>(w->packed);
+  a.alpha = w->alpha;
+  a.alpha_up = w->alpha_up;
+  a.experts = w->num_experts;
+  a.n_out = w->n_out;
+  a.upt = static_cast<int32_t>(mx_unit_rows(w));
+  a.chunks = static_cast<int32_t>(mx_chunks(w));
+  a.groups = Mx<FMT>::group ? w->k / (Mx<FMT>::group ? Mx<FMT>::group : 1) : 0;
+  a.rows = g.rows;
+  a.x_scales = g.x_scales;
+  a.x_pitch = static_cast<int64_t>(moe_mx_scale_pitch(FMT, w->k));
+  a.x_global = FMT == MOE_MX_NVFP4 ? g.x_global : nullptr;
+  a.offsets = g.offsets;
+  a.out = g.out;
+  a.out_f16 = g.out_f16;
+  a.out_vec = reinterpret_cast<uintptr_t>(g.out) % 32 == 0 && g.out_ld % 16 == 0;
+  a.out_rows = g.out_rows;
+  a.out_ld = g.out_ld;
+  a.out_pos = g.out_pos;
+  a.row_weight = g.row_weight;
+  a.h_global = FMT == MOE_MX_NVFP4 ? g.h_global : nullptr;
+  a.h_codes = g.h_codes;
+  a.h_scales = g.h_scales;
+  a.h_row_bytes = static_cast<int64_t>(moe_mx_code_bytes(FMT, w->n_out));
+  a.h_pitch = static_cast<int64_t>(moe_mx_scale_pitch(FMT, w->n_out));
+  a.err = g.err;
+  a.overlap = g.overlap ? 1 : 0;
+  RowMaps maps;
+  for (int i = 0; i < 4; ++i)
+    if (!encode_rows_map(&maps.box[i], g.x_codes, moe_mx_code_bytes(FMT, w->k), g.rows, 16u << i))
+      return cudaErrorInvalidValue;
+  // no more CTAs than units there can be: an expert's last tile may be short
+  const int64_t tiles = static_cast<int64_t>(g.rows) / kTile + (g.rows < w->num_experts ? g.rows : w->num_experts);
+  const int64_t units = tiles * a.upt;
+  const int grid = static_cast<int>(units < g.num_sms ? units : g.num_sms);
+  return launch_maybe_overlapped(kern, grid, kThreads, C::kSmem, s, g.overlap, maps, a);
+}
+
+}  // namespace
+
+cudaError_t launch_mx_product(const MxProductLaunch& g, cudaStream_t s) {
+  const bool sw = g.w->swiglu != 0;
+  switch (g.w->format) {
+    case MOE_MX_BF16: return sw ? launch<MOE_MX_BF16, true>(g, s) : launch<MOE_MX_BF16, false>(g, s);
+    case MOE_MX_MXFP8: return sw ? launch<MOE_MX_MXFP8, true>(g, s) : launch<MOE_MX_MXFP8, false>(g, s);
+    case MOE_MX_MXFP4: return sw ? launch<MOE_MX_MXFP4, true>(g, s) : launch<MOE_MX_MXFP4, false>(g, s);
+    case MOE_MX_NVFP4: return sw ? launch<MOE_MX_NVFP4, true>(g, s) : launch<MOE_MX_NVFP4, false>(g, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace moe
