@@ -183,6 +183,19 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, t):
+    """The stream's handle; by default that of the current stream of t's device (the lookup that torch's own stream
+    object wraps: a fifth of its cost)."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else None
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _check(status: int, where: str):
     if status != MOE_OK:
         raise MoeError(status, where)
@@ -345,23 +358,27 @@ def moe_mx_scale_pitch(fmt: int, cols: int) -> int:
 
 
 def moe_mx_quantise(fmt, n, k, d, x, x_ld, positions, global_scale, out_rows, codes, scales, stream=None):
-    st = load_library().moe_mx_quantise(fmt, n, k, d, _ptr(x), x_ld, _ptr(positions), _ptr(global_scale), out_rows,
-                                        _ptr(codes), _ptr(scales), _stream(stream))
-    _check(st, "moe_mx_quantise")
+    st = (_lib or load_library()).moe_mx_quantise(
+        fmt, n, k, d, x.data_ptr(), x_ld, _addr(positions), _addr(global_scale), out_rows, codes.data_ptr(),
+        _addr(scales), _raw_stream(stream, x))
+    if st:
+        raise MoeError(st, "moe_mx_quantise")
 
 
 def moe_mx_add_rmsnorm(fmt, n, k, d, x, x_ld, residual, r_ld, gain, eps, positions, global_scale, out_rows, sum_out,
                        codes, scales, stream=None):
-    st = load_library().moe_mx_add_rmsnorm(fmt, n, k, d, _ptr(x), x_ld, _ptr(residual), r_ld, _ptr(gain), float(eps),
-                                           _ptr(positions), _ptr(global_scale), out_rows, _ptr(sum_out), _ptr(codes),
-                                           _ptr(scales), _stream(stream))
-    _check(st, "moe_mx_add_rmsnorm")
+    st = (_lib or load_library()).moe_mx_add_rmsnorm(
+        fmt, n, k, d, x.data_ptr(), x_ld, _addr(residual), r_ld, gain.data_ptr(), eps, _addr(positions),
+        _addr(global_scale), out_rows, _addr(sum_out), codes.data_ptr(), _addr(scales), _raw_stream(stream, x))
+    if st:
+        raise MoeError(st, "moe_mx_add_rmsnorm")
 
 
 def moe_mx_dequantise(fmt, rows, d, codes, scales, global_scale, out, out_ld, stream=None):
-    st = load_library().moe_mx_dequantise(fmt, rows, d, _ptr(codes), _ptr(scales), _ptr(global_scale), _ptr(out),
-                                          out_ld, _stream(stream))
-    _check(st, "moe_mx_dequantise")
+    st = (_lib or load_library()).moe_mx_dequantise(fmt, rows, d, codes.data_ptr(), _addr(scales), _addr(global_scale),
+                                                    out.data_ptr(), out_ld, _raw_stream(stream, out))
+    if st:
+        raise MoeError(st, "moe_mx_dequantise")
 
 
 def moe_mx_packed_bytes(w: moe_mx_weights) -> int:
@@ -370,25 +387,27 @@ def moe_mx_packed_bytes(w: moe_mx_weights) -> int:
 
 def moe_mx_pack_weights(w: moe_mx_weights, codes, scales, codes_up, scales_up, packed, stream=None):
     st = load_library().moe_mx_pack_weights(ctypes.byref(w), _ptr(codes), _ptr(scales), _ptr(codes_up),
-                                            _ptr(scales_up), _ptr(packed), _stream(stream))
+                                            _ptr(scales_up), _ptr(packed), _raw_stream(stream, packed))
     _check(st, "moe_mx_pack_weights")
 
 
 def moe_mx_grouped_product(w: moe_mx_weights, rows, x_codes, x_scales, x_global, expert_offsets, out, out_type,
                            out_rows, out_ld, out_pos, row_weight, ws, stream=None):
-    st = load_library().moe_mx_grouped_product(ctypes.byref(w), rows, _ptr(x_codes), _ptr(x_scales), _ptr(x_global),
-                                               _ptr(expert_offsets), _ptr(out), out_type, out_rows, out_ld,
-                                               _ptr(out_pos), _ptr(row_weight), _ptr(ws),
-                                               ws.numel() * ws.element_size(), _stream(stream))
-    _check(st, "moe_mx_grouped_product")
+    st = (_lib or load_library()).moe_mx_grouped_product(
+        w, rows, x_codes.data_ptr(), _addr(x_scales), _addr(x_global), expert_offsets.data_ptr(), out.data_ptr(),
+        out_type, out_rows, out_ld, _addr(out_pos), _addr(row_weight), ws.data_ptr(), ws.nbytes,
+        _raw_stream(stream, out))
+    if st:
+        raise MoeError(st, "moe_mx_grouped_product")
 
 
 def moe_mx_grouped_swiglu(w: moe_mx_weights, rows, x_codes, x_scales, x_global, expert_offsets, h_global, h_codes,
                           h_scales, ws, stream=None):
-    st = load_library().moe_mx_grouped_swiglu(ctypes.byref(w), rows, _ptr(x_codes), _ptr(x_scales), _ptr(x_global),
-                                              _ptr(expert_offsets), _ptr(h_global), _ptr(h_codes), _ptr(h_scales),
-                                              _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
-    _check(st, "moe_mx_grouped_swiglu")
+    st = (_lib or load_library()).moe_mx_grouped_swiglu(
+        w, rows, x_codes.data_ptr(), _addr(x_scales), _addr(x_global), expert_offsets.data_ptr(), _addr(h_global),
+        h_codes.data_ptr(), _addr(h_scales), ws.data_ptr(), ws.nbytes, _raw_stream(stream, h_codes))
+    if st:
+        raise MoeError(st, "moe_mx_grouped_swiglu")
 
 
 def moe_mx_layer_workspace_size(gate_up: moe_mx_weights, down: moe_mx_weights, top_k: int, n_tokens: int) -> int:
@@ -397,12 +416,12 @@ def moe_mx_layer_workspace_size(gate_up: moe_mx_weights, down: moe_mx_weights, t
 
 def moe_mx_layer_forward(gate_up: moe_mx_weights, down: moe_mx_weights, top_k, n_tokens, x, residual, gain, eps,
                          topk_ids, topk_weight, x_global, h_global, sum_out, out, ws, out_is_fp32=False, stream=None):
-    st = load_library().moe_mx_layer_forward(ctypes.byref(gate_up), ctypes.byref(down), top_k, n_tokens, _ptr(x),
-                                             _ptr(residual), _ptr(gain), float(eps), _ptr(topk_ids),
-                                             _ptr(topk_weight), _ptr(x_global), _ptr(h_global), _ptr(sum_out),
-                                             _ptr(out), int(bool(out_is_fp32)), _ptr(ws),
-                                             ws.numel() * ws.element_size(), _stream(stream))
-    _check(st, "moe_mx_layer_forward")
+    st = (_lib or load_library()).moe_mx_layer_forward(
+        gate_up, down, top_k, n_tokens, x.data_ptr(), _addr(residual), _addr(gain), eps, topk_ids.data_ptr(),
+        topk_weight.data_ptr(), _addr(x_global), _addr(h_global), _addr(sum_out), out.data_ptr(), bool(out_is_fp32),
+        ws.data_ptr(), ws.nbytes, _raw_stream(stream, x))
+    if st:
+        raise MoeError(st, "moe_mx_layer_forward")
 
 
 # ---------------------------------------------------------------- allocating conveniences
@@ -506,10 +525,25 @@ def layer_forward(hidden, gain, eps, topk_ids, topk_weight, bank, shared=None, w
 
 
 # ---------------------------------------------------------------- microscaled formats
+# A decode step's call is a few microseconds of GPU time: the checks below are written to cost little on the host
+# (no message is formatted, and no library call made, for arguments that pass).
+
+_MX_BITS = (16, 8, 4, 4)
+_MX_GROUP = (0, 32, 32, 16)
+
+
+def _mx_width(fmt, cols):
+    """(code bytes, scale pitch) of a row, as moe_mx_code_bytes and moe_mx_scale_pitch give them."""
+    if not 0 <= fmt <= 3 or cols <= 0 or cols & 31:
+        raise MoeError(2, "moe_mx_code_bytes")
+    return cols * _MX_BITS[fmt] >> 3, (-(-(cols // _MX_GROUP[fmt]) // 16) * 16 if fmt else 0)
+
 
 class MxRows:
     """Rows of `cols` columns in a microscaled format: uint8 codes [rows, .] and scales [rows, pitch] (None for
     bf16), and NVFP4's fp32 factor [1] (None = 1)."""
+
+    __slots__ = ("fmt", "cols", "codes", "scales", "global_scale")
 
     def __init__(self, fmt, cols, codes, scales=None, global_scale=None):
         self.fmt, self.cols, self.codes, self.scales, self.global_scale = fmt, cols, codes, scales, global_scale
@@ -527,18 +561,37 @@ class MxWeights:
         self.fmt, self.num_experts, self.n_out, self.k = fmt, num_experts, n_out, k
         self.packed, self.alpha, self.alpha_up, self.swiglu = packed, alpha, alpha_up, bool(swiglu)
 
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        self.__dict__["_checked"] = None       # the struct below is of the attributes as they were
+
     def struct(self) -> moe_mx_weights:
-        p = [t.data_ptr() if t is not None else None for t in (self.packed, self.alpha, self.alpha_up)]
-        return moe_mx_weights(self.fmt, self.num_experts, self.n_out, self.k, int(self.swiglu), *p)
+        return moe_mx_weights(self.fmt, self.num_experts, self.n_out, self.k, int(self.swiglu), _addr(self.packed),
+                              _addr(self.alpha), _addr(self.alpha_up))
+
+    def checked(self, dev):
+        """The struct, once the tensors have been checked against it."""
+        got = self._checked
+        if got is None or got[1] != dev:
+            st = self.struct()
+            nbytes = moe_mx_packed_bytes(st)
+            if nbytes == 0:
+                raise MoeError(2, "moe_mx_packed_bytes")
+            if self.packed.nbytes != nbytes or not self.packed.is_contiguous() or self.packed.get_device() != dev:
+                raise ValueError(f"packed: expected {nbytes} contiguous bytes on device {dev}")
+            _mx_scalar(self.alpha, "alpha", dev, self.num_experts)
+            _mx_scalar(self.alpha_up, "alpha_up", dev, self.num_experts)
+            got = self.__dict__["_checked"] = (st, dev)
+        return got[0]
 
 
 def _on_stream(fn):
     """What the call allocates (results, a workspace of its own) belongs to the stream that it launches on."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        import torch
         if stream is None:
             return fn(*args, **kw)
+        import torch
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream))
         with torch.cuda.stream(stream):
@@ -546,79 +599,71 @@ def _on_stream(fn):
     return call
 
 
-def _mx_want(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
-def _mx_tensor(t, name, dtype, shape, device):
+def _mx_tensor(t, name, dtype, shape, dev):
     """The tensor that a library call reads through its pointer: dense, on the device, of this type and shape."""
-    _mx_want(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous() and t.device == device,
-             f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
-             f"{tuple(t.shape)} on {t.device}")
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on device {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
 
 
-def _mx_strided(t, name, shape, device):
+def _mx_strided(t, name, shape, dev):
+    """bf16 rows: the row stride in elements (that of a single row is not used, and torch may report any)."""
     import torch
-    _mx_want(t.dtype == torch.bfloat16 and tuple(t.shape) == tuple(shape) and t.device == device
-             and (shape[1] == 1 or t.stride(1) == 1), f"{name}: expected bf16 rows {tuple(shape)} on {device}")
+    if t.dtype != torch.bfloat16 or t.shape != shape or t.get_device() != dev or t.stride(1) != 1:
+        raise ValueError(f"{name}: expected bf16 rows {tuple(shape)} on device {dev}, got {t.dtype} {tuple(t.shape)} "
+                         f"on {t.device}")
+    ld = t.stride(0)
+    return ld if shape[0] > 1 else max(ld, shape[1])
 
 
-def _ld(t):
-    # the stride of a single row is not used, and torch may report any
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _mx_scalar(t, name, device, count=1):
-    import torch
+def _mx_scalar(t, name, dev, count=1):
     if t is not None:
-        _mx_want(t.dtype == torch.float32 and t.numel() == count and t.is_contiguous() and t.device == device,
-                 f"{name}: expected {count} fp32 value(s) on {device}")
+        import torch
+        if t.dtype != torch.float32 or t.numel() != count or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"{name}: expected {count} fp32 value(s) on device {dev}")
 
 
-def _mx_check_rows(r: MxRows):
+def _mx_check_rows(r: MxRows, dev):
     import torch
-    dev = r.codes.device
-    cb = moe_mx_code_bytes(r.fmt, r.cols)
-    if cb == 0:
-        raise MoeError(2, "moe_mx_code_bytes")
-    _mx_tensor(r.codes, "codes", torch.uint8, (r.rows, cb), dev)
-    if r.fmt != MOE_MX_BF16:
-        _mx_want(r.scales is not None, "scales: missing")
-        _mx_tensor(r.scales, "scales", torch.uint8, (r.rows, moe_mx_scale_pitch(r.fmt, r.cols)), dev)
-    _mx_scalar(r.global_scale, "global_scale", dev)
-
-
-def _mx_check_weights(w: MxWeights, dev):
-    nbytes = moe_mx_packed_bytes(w.struct())
-    if nbytes == 0:
-        raise MoeError(2, "moe_mx_packed_bytes")
-    _mx_want(w.packed.numel() * w.packed.element_size() == nbytes and w.packed.is_contiguous()
-             and w.packed.device == dev, f"packed: expected {nbytes} contiguous bytes on {dev}")
-    _mx_scalar(w.alpha, "alpha", dev, w.num_experts)
-    _mx_scalar(w.alpha_up, "alpha_up", dev, w.num_experts)
+    codes = r.codes
+    n = codes.shape[0]
+    cb, pitch = _mx_width(r.fmt, r.cols)
+    _mx_tensor(codes, "codes", torch.uint8, (n, cb), dev)
+    if pitch:
+        if r.scales is None:
+            raise ValueError("scales: missing")
+        _mx_tensor(r.scales, "scales", torch.uint8, (n, pitch), dev)
+    if r.global_scale is not None:
+        _mx_scalar(r.global_scale, "global_scale", dev)
+    return n
 
 
 def mx_rows(fmt, rows, cols, device="cuda", global_scale=None) -> MxRows:
     """Uninitialised rows."""
     import torch
-    cb = moe_mx_code_bytes(fmt, cols)
-    if cb == 0:
-        raise MoeError(2, "moe_mx_code_bytes")
-    codes = torch.empty(rows, cb, dtype=torch.uint8, device=device)
-    scales = None
-    if fmt != MOE_MX_BF16:
-        scales = torch.empty(rows, moe_mx_scale_pitch(fmt, cols), dtype=torch.uint8, device=device)
-    return MxRows(fmt, cols, codes, scales, global_scale)
+    cb, pitch = _mx_width(fmt, cols)
+    codes = torch.empty((rows, cb), dtype=torch.uint8, device=device)
+    return MxRows(fmt, cols, codes, torch.empty((rows, pitch), dtype=torch.uint8, device=device) if pitch else None,
+                  global_scale)
 
 
-def _mx_positions(positions, n, out_rows, device):
+def _mx_out(fmt, n, d, positions, out_rows, global_scale, out, device, dev):
+    """(k, rows, the rows to write) of a call that writes n tokens' rows."""
     import torch
-    if positions is None:
-        return 1, n if out_rows is None else out_rows
-    _mx_want(positions.dim() == 2, "positions: expected [n, k]")
-    _mx_tensor(positions, "positions", torch.int32, (n, positions.shape[1]), device)
-    return positions.shape[1], positions.numel() if out_rows is None else out_rows
+    if global_scale is not None:
+        _mx_scalar(global_scale, "global_scale", dev)
+    k = 1
+    if positions is not None:
+        k = positions.shape[1] if positions.dim() == 2 else 0
+        _mx_tensor(positions, "positions", torch.int32, (n, k), dev)
+    if out is None:
+        m = n * k if out_rows is None else out_rows
+        return k, m, mx_rows(fmt, m, d, device, global_scale)
+    if out.fmt != fmt or out.cols != d:
+        raise ValueError("out: of another format or width")
+    m = _mx_check_rows(out, dev)
+    out.global_scale = global_scale
+    return k, m, out
 
 
 @_on_stream
@@ -626,16 +671,10 @@ def mx_quantise(x, fmt, positions=None, out_rows=None, global_scale=None, out: O
     """bf16 rows x [n, d] (any row stride that is a multiple of 8) into a format; row t goes to each of positions[t]
     (int32 [n, k], default its own place) of `out` (out_rows rows, default n * k)."""
     n, d = x.shape
-    dev = x.device
-    _mx_strided(x, "x", (n, d), dev)
-    _mx_scalar(global_scale, "global_scale", dev)
-    k, m = _mx_positions(positions, n, out_rows if out is None else out.rows, dev)
-    if out is None:
-        out = mx_rows(fmt, m, d, dev)
-    out.global_scale = global_scale
-    _mx_want(out.fmt == fmt and out.cols == d and out.codes.device == dev, "out: of another format, width or device")
-    _mx_check_rows(out)
-    moe_mx_quantise(fmt, n, k, d, x, _ld(x), positions, global_scale, m, out.codes, out.scales)
+    dev = x.get_device()
+    ld = _mx_strided(x, "x", (n, d), dev)
+    k, m, out = _mx_out(fmt, n, d, positions, out_rows, global_scale, out, x.device, dev)
+    moe_mx_quantise(fmt, n, k, d, x, ld, positions, global_scale, m, out.codes, out.scales)
     return out
 
 
@@ -645,28 +684,22 @@ def mx_add_rmsnorm(x, residual, gain, eps, fmt, positions=None, out_rows=None, g
     """(rows of the normalised sum, the sum): sum = bf16(x + residual) (residual may be None), rows = Q(rmsnorm(sum))
     written as by mx_quantise.  sum_out may be x or residual."""
     import torch
-    n, d = x.shape
-    dev = x.device
-    _mx_strided(x, "x", (n, d), dev)
-    if residual is not None:
-        _mx_strided(residual, "residual", (n, d), dev)
+    n, d = shape = x.shape
+    dev = x.get_device()
+    ld = _mx_strided(x, "x", shape, dev)
+    r_ld = None if residual is None else _mx_strided(residual, "residual", shape, dev)
     _mx_tensor(gain, "gain", torch.bfloat16, (d,), dev)
-    _mx_scalar(global_scale, "global_scale", dev)
-    k, m = _mx_positions(positions, n, out_rows if out is None else out.rows, dev)
-    if out is None:
-        out = mx_rows(fmt, m, d, dev)
-    out.global_scale = global_scale
-    _mx_want(out.fmt == fmt and out.cols == d and out.codes.device == dev, "out: of another format, width or device")
-    _mx_check_rows(out)
-    r_ld = _ld(residual) if residual is not None else d
     if sum_out is None:
-        sum_out = torch.empty_strided((n, d), (r_ld, 1), dtype=torch.bfloat16, device=dev)
-    _mx_strided(sum_out, "sum_out", (n, d), dev)
-    if residual is None:
-        r_ld = _ld(sum_out)
-    _mx_want(_ld(sum_out) == r_ld or n == 1, "sum_out: its row stride differs from residual's")
-    moe_mx_add_rmsnorm(fmt, n, k, d, x, _ld(x), residual, r_ld, gain, eps, positions, global_scale, m, sum_out,
-                       out.codes, out.scales)
+        sum_out = torch.empty_strided(shape, (r_ld or d, 1), dtype=torch.bfloat16, device=x.device)
+        r_ld = r_ld or d
+    else:
+        s_ld = _mx_strided(sum_out, "sum_out", shape, dev)
+        if r_ld is not None and s_ld != r_ld and n > 1:
+            raise ValueError("sum_out: its row stride differs from residual's")
+        r_ld = r_ld or s_ld
+    k, m, out = _mx_out(fmt, n, d, positions, out_rows, global_scale, out, x.device, dev)
+    moe_mx_add_rmsnorm(fmt, n, k, d, x, ld, residual, r_ld, gain, eps, positions, global_scale, m, sum_out, out.codes,
+                       out.scales)
     return out, sum_out
 
 
@@ -674,11 +707,13 @@ def mx_add_rmsnorm(x, residual, gain, eps, fmt, positions=None, out_rows=None, g
 def mx_dequantise(r: MxRows, out=None):
     """bf16 values of rows."""
     import torch
-    _mx_check_rows(r)
+    dev = r.codes.get_device()
+    n, d = _mx_check_rows(r, dev), r.cols
     if out is None:
-        out = torch.empty(r.rows, r.cols, dtype=torch.bfloat16, device=r.codes.device)
-    _mx_strided(out, "out", (r.rows, r.cols), r.codes.device)
-    moe_mx_dequantise(r.fmt, r.rows, r.cols, r.codes, r.scales, r.global_scale, out, _ld(out))
+        out, ld = torch.empty((n, d), dtype=torch.bfloat16, device=r.codes.device), d
+    else:
+        ld = _mx_strided(out, "out", (n, d), dev)
+    moe_mx_dequantise(r.fmt, n, d, r.codes, r.scales, r.global_scale, out, ld)
     return out
 
 
@@ -686,32 +721,33 @@ def mx_dequantise(r: MxRows, out=None):
 def mx_pack(rows: MxRows, num_experts, up: Optional[MxRows] = None, alpha=None, alpha_up=None) -> MxWeights:
     """Packed weights from rows [num_experts * n_out] of a format (up: the SwiGLU pair's second matrix)."""
     import torch
-    _mx_check_rows(rows)
-    _mx_want(num_experts >= 1 and rows.rows % num_experts == 0, "rows: not a multiple of num_experts")
-    dev = rows.codes.device
+    dev = rows.codes.get_device()
+    n = _mx_check_rows(rows, dev)
+    if num_experts < 1 or n % num_experts != 0:
+        raise ValueError("rows: not a multiple of num_experts")
     if up is not None:
-        _mx_check_rows(up)
-        _mx_want((up.fmt, up.cols, up.rows, up.codes.device) == (rows.fmt, rows.cols, rows.rows, dev),
-                 "up: not like the first matrix")
-    w = MxWeights(rows.fmt, num_experts, rows.rows // num_experts, rows.cols, None, alpha, alpha_up, up is not None)
+        if (up.fmt, up.cols) != (rows.fmt, rows.cols) or _mx_check_rows(up, dev) != n:
+            raise ValueError("up: not like the first matrix")
+    w = MxWeights(rows.fmt, num_experts, n // num_experts, rows.cols, None, alpha, alpha_up, up is not None)
     nbytes = moe_mx_packed_bytes(w.struct())
     if nbytes == 0:
         raise MoeError(2, "moe_mx_packed_bytes")
-    w.packed = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _mx_check_weights(w, dev)
-    moe_mx_pack_weights(w.struct(), rows.codes, rows.scales, up.codes if up else None, up.scales if up else None,
+    w.packed = torch.empty(nbytes, dtype=torch.uint8, device=rows.codes.device)
+    moe_mx_pack_weights(w.checked(dev), rows.codes, rows.scales, up.codes if up else None, up.scales if up else None,
                         w.packed)
     return w
 
 
 def _mx_operands(x: MxRows, w: MxWeights, offsets):
+    """(device, rows, the weights' struct) of checked operands."""
     import torch
-    _mx_check_rows(x)
-    dev = x.codes.device
-    _mx_check_weights(w, dev)
-    _mx_want(x.fmt == w.fmt and x.cols == w.k, "x: of another format or width than the weights")
+    dev = x.codes.get_device()
+    n = _mx_check_rows(x, dev)
+    st = w.checked(dev)
+    if x.fmt != w.fmt or x.cols != w.k:
+        raise ValueError("x: of another format or width than the weights")
     _mx_tensor(offsets, "offsets", torch.int32, (w.num_experts + 1,), dev)
-    return dev
+    return dev, n, st
 
 
 def mx_workspace(device="cuda"):
@@ -725,37 +761,37 @@ def mx_grouped_product(x: MxRows, w: MxWeights, offsets, out=None, out_pos=None,
     """out[p(r)] = row_weight[p(r)] * x[r] W_e^T for the rows offsets[e] .. offsets[e + 1] - 1 of each expert e;
     p = out_pos (int32 [rows], default r)."""
     import torch
-    dev = _mx_operands(x, w, offsets)
+    dev, n, st = _mx_operands(x, w, offsets)
     dtype = torch.float16 if out_type == MOE_MX_OUT_F16 else torch.bfloat16
+    cols = w.n_out
     if out is None:
-        out = torch.empty(x.rows, w.n_out, dtype=dtype, device=dev)
-    _mx_want(out.dtype == dtype and out.dim() == 2 and out.shape[1] == w.n_out and out.device == dev
-             and (w.n_out == 1 or out.stride(1) == 1), "out: of another type, width or device")
+        out, out_rows, ld = torch.empty((n, cols), dtype=dtype, device=x.codes.device), n, cols
+    else:
+        if out.dtype != dtype or out.dim() != 2 or out.shape[1] != cols or out.get_device() != dev or (
+                cols > 1 and out.stride(1) != 1):
+            raise ValueError("out: of another type, width or device")
+        out_rows, ld = out.shape[0], max(out.stride(0), cols) if out.shape[0] < 2 else out.stride(0)
     if out_pos is not None:
-        _mx_tensor(out_pos, "out_pos", torch.int32, (x.rows,), dev)
-    _mx_scalar(row_weight, "row_weight", dev, out.shape[0])
+        _mx_tensor(out_pos, "out_pos", torch.int32, (n,), dev)
+    if row_weight is not None:
+        _mx_scalar(row_weight, "row_weight", dev, out_rows)
     if ws is None:
-        ws = mx_workspace(dev)
-    moe_mx_grouped_product(w.struct(), x.rows, x.codes, x.scales, x.global_scale, offsets, out, out_type, out.shape[0],
-                           _ld(out), out_pos, row_weight, ws)
+        ws = mx_workspace(x.codes.device)
+    moe_mx_grouped_product(st, n, x.codes, x.scales, x.global_scale, offsets, out, out_type, out_rows, ld, out_pos,
+                           row_weight, ws)
     return out
 
 
 @_on_stream
 def mx_grouped_swiglu(x: MxRows, w: MxWeights, offsets, h_global=None, out: Optional[MxRows] = None, ws=None) -> MxRows:
     """Rows of silu(x Wg_e^T) * (x Wu_e^T) in the format of x."""
-    dev = _mx_operands(x, w, offsets)
-    _mx_scalar(h_global, "h_global", dev)
-    if out is None:
-        out = mx_rows(w.fmt, x.rows, w.n_out, dev)
-    out.global_scale = h_global
-    _mx_want(out.fmt == w.fmt and out.cols == w.n_out and out.rows == x.rows and out.codes.device == dev,
-             "out: of another format, shape or device")
-    _mx_check_rows(out)
+    dev, n, st = _mx_operands(x, w, offsets)
+    _, m, out = _mx_out(w.fmt, n, w.n_out, None, None, h_global, out, x.codes.device, dev)
+    if m != n:
+        raise ValueError("out: of another number of rows")
     if ws is None:
-        ws = mx_workspace(dev)
-    moe_mx_grouped_swiglu(w.struct(), x.rows, x.codes, x.scales, x.global_scale, offsets, h_global, out.codes,
-                          out.scales, ws)
+        ws = mx_workspace(x.codes.device)
+    moe_mx_grouped_swiglu(st, n, x.codes, x.scales, x.global_scale, offsets, h_global, out.codes, out.scales, ws)
     return out
 
 
@@ -765,28 +801,32 @@ def mx_layer_forward(x, residual, gain, eps, topk_ids, topk_weight, gate_up: MxW
     """The MoE block on microscaled experts: (sum, out) with sum = bf16(x + residual) and out = sum + the routed
     experts on rmsnorm(sum); with gain None (and residual None) (None, the routed experts on x)."""
     import torch
-    n, d = x.shape
-    dev = x.device
-    _mx_tensor(x, "x", torch.bfloat16, (n, d), dev)
-    _mx_want(d == gate_up.k, "x: of another width than the experts")
+    n, d = shape = x.shape
+    dev = x.get_device()
+    bf16 = torch.bfloat16
+    _mx_tensor(x, "x", bf16, shape, dev)
+    if d != gate_up.k:
+        raise ValueError("x: of another width than the experts")
     if residual is not None:
-        _mx_tensor(residual, "residual", torch.bfloat16, (n, d), dev)
+        _mx_tensor(residual, "residual", bf16, shape, dev)
     if gain is not None:
-        _mx_tensor(gain, "gain", torch.bfloat16, (d,), dev)
-    _mx_tensor(topk_ids, "topk_ids", torch.int32, (n, topk_ids.shape[1]), dev)
-    _mx_tensor(topk_weight, "topk_weight", torch.float32, tuple(topk_ids.shape), dev)
-    _mx_check_weights(gate_up, dev)
-    _mx_check_weights(down, dev)
-    _mx_scalar(x_global, "x_global", dev)
-    _mx_scalar(h_global, "h_global", dev)
-    gs, ds, k = gate_up.struct(), down.struct(), topk_ids.shape[1]
+        _mx_tensor(gain, "gain", bf16, (d,), dev)
+    k = topk_ids.shape[1]
+    _mx_tensor(topk_ids, "topk_ids", torch.int32, (n, k), dev)
+    _mx_tensor(topk_weight, "topk_weight", torch.float32, (n, k), dev)
+    gs, ds = gate_up.checked(dev), down.checked(dev)
+    if x_global is not None:
+        _mx_scalar(x_global, "x_global", dev)
+    if h_global is not None:
+        _mx_scalar(h_global, "h_global", dev)
+    device = x.device
     if ws is None:
         nbytes = moe_mx_layer_workspace_size(gs, ds, k, n)
         if nbytes == 0:
             raise MoeError(2, "moe_mx_layer_workspace_size")
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    total = torch.empty(n, d, dtype=torch.bfloat16, device=dev) if gain is not None else None
-    out = torch.empty(n, d, dtype=torch.float32 if out_is_fp32 else torch.bfloat16, device=dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    total = torch.empty(shape, dtype=bf16, device=device) if gain is not None else None
+    out = torch.empty(shape, dtype=torch.float32 if out_is_fp32 else bf16, device=device)
     moe_mx_layer_forward(gs, ds, k, n, x, residual, gain, eps, topk_ids, topk_weight, x_global, h_global, total, out,
                          ws, out_is_fp32)
     return total, out

@@ -29,6 +29,8 @@
 // Within an expert up to eight tiles run a weight block one after another, so that
 // they take place at the same time and share it through L2.  Every wait is bounded
 // (common.cuh); after one gives up all roles drain and the kernel ends.
+#include <atomic>
+
 #include "mx.cuh"
 
 namespace moe {
@@ -55,7 +57,8 @@ struct Cfg {
   static constexpr int kNumBars = 2 * kStages + 2 * kAcc + 1;
   static constexpr int kBarOff = kStages * kStage;
   static constexpr int kPlanOff = kBarOff + kNumBars * 8 + 16;  // tile prefix, row starts
-  static constexpr int kSmem = 1024 + kPlanOff + 2 * (kMaxExperts + 1) * 4 + 64 * 4;
+  static constexpr int kTurnOff = (kPlanOff + 2 * (kMaxExperts + 1) * 4 + 64 * 4 + 15) / 16 * 16;  // 1 KB an epilogue warp
+  static constexpr int kSmem = 1024 + kTurnOff + 8 * 1024;
   static_assert(kStage % 1024 == 0, "operand tiles stay 1024-byte aligned");
   static_assert(kSmem <= 232448, "shared memory per CTA");
   static_assert(256 * kAcc + kStages * kScaleCols <= kTmemCols, "tensor memory");
@@ -560,37 +563,45 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
             }
           }
         }
-      } else if (store) {
-        uint16_t* o = static_cast<uint16_t*>(a.out) + dst * a.out_ld;
+      } else {
+        uint16_t* o = static_cast<uint16_t*>(a.out);
+        uint16_t* mine = reinterpret_cast<uint16_t*>(smem + C::kTurnOff + (warp - kWarpEpi) * 1024);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          const int n0 = 256 * un.u + 128 * m + 64 * hf;
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const int at = n0 + 16 * v;
-            if (at < a.n_out) {
-              uint32_t w[8];
+            const int at = 256 * un.u + 128 * m + 64 * hf + 16 * v;
+            if (at >= a.n_out) continue;
+            uint32_t w[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint32_t r0 = m ? p1[16 * v + 2 * i] : p0[16 * v + 2 * i];
-                const uint32_t r1 = m ? p1[16 * v + 2 * i + 1] : p0[16 * v + 2 * i + 1];
-                const float y0 = __uint_as_float(r0) * f0 * wgt, y1 = __uint_as_float(r1) * f0 * wgt;
-                if (a.out_f16) {
-                  overflow |= (fabsf(y0) >= 65520.f) || (fabsf(y1) >= 65520.f && at + 2 * i + 1 < a.n_out);
-                  const __half2 h2 = __floats2half2_rn(y0, y1);
-                  w[i] = *reinterpret_cast<const uint32_t*>(&h2);
-                } else {
-                  w[i] = pack_bf16(y0, y1);
-                }
-              }
-              if (a.out_vec && at + 16 <= a.n_out) {
-                stg256(o + at, w);
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t r0 = m ? p1[16 * v + 2 * i] : p0[16 * v + 2 * i];
+              const uint32_t r1 = m ? p1[16 * v + 2 * i + 1] : p0[16 * v + 2 * i + 1];
+              const float y0 = __uint_as_float(r0) * f0 * wgt, y1 = __uint_as_float(r1) * f0 * wgt;
+              if (a.out_f16) {
+                overflow |= store && ((fabsf(y0) >= 65520.f) || (fabsf(y1) >= 65520.f));
+                const __half2 h2 = __floats2half2_rn(y0, y1);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h2);
               } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  if (at + 2 * i < a.n_out) o[at + 2 * i] = static_cast<uint16_t>(w[i]);
-                  if (at + 2 * i + 1 < a.n_out) o[at + 2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
-                }
+                w[i] = pack_bf16(y0, y1);
+              }
+            }
+            if (a.out_vec && at + 16 <= a.n_out) {
+              if (store) stg256(o + dst * a.out_ld + at, w);
+            } else {
+              // rows that are not aligned, or the last columns: turned through shared memory so
+              // that half a warp writes 16 columns of one row
+              __syncwarp();
+              reinterpret_cast<uint4*>(mine)[2 * lane] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(mine)[2 * lane + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+              __syncwarp();
+              const int col = lane & 15;
+#pragma unroll 4
+              for (int i = 0; i < 16; ++i) {
+                const int r = 2 * i + (lane >> 4);
+                const int64_t to = __shfl_sync(0xffffffffu, dst, r);
+                const bool on = __shfl_sync(0xffffffffu, static_cast<int>(store), r) != 0;
+                if (on && at + col < a.n_out) o[to * a.out_ld + at + col] = mine[16 * r + col];
               }
             }
           }
@@ -612,11 +623,17 @@ cudaError_t launch(const MxProductLaunch& g, cudaStream_t s) {
   auto kern = mx_product_kernel<FMT, SWIGLU>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  // an increase of the register split that cannot be met never returns
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs * kThreads < 128 * (kRegsLow + kRegsScales + 2 * kRegsEpi)) return cudaErrorInvalidConfiguration;
+  // An increase of the register split that cannot be met never returns: launch only if the kernel's own
+  // count covers it (a property of the binary, looked up until it is known).
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) * kThreads < 128 * (kRegsLow + kRegsScales + 2 * kRegsEpi))
+    return cudaErrorInvalidConfiguration;
   const moe_mx_weights* w = g.w;
   Args a{};
   a.packed = static_cast<const uint8_t*>(w->packed);

@@ -35,101 +35,116 @@ __device__ __forceinline__ int64_t scale_pitch(int d) {
 }
 
 constexpr int kRowsMaxThreads = 1024;
+constexpr int kRowsSplitThreads = 256;
 
-// ITER passes of blockDim.x * 8 columns cover the row; the sum of squares is
-// taken per thread in column order, then by shuffles, then over the warps.
+// ITER passes of blockDim.x * 8 columns cover the row, held as the bf16 pairs they
+// are read as (the stored sum is bf16 too).  The sum of squares is taken per thread
+// in column order, then by shuffles, then over the warps.
 template <int FMT, bool NORM, int ITER>
-__global__ void __launch_bounds__(kRowsMaxThreads)
+__global__ void __launch_bounds__(ITER <= 2 ? kRowsMaxThreads : kRowsSplitThreads)
 mx_rows_kernel(const MxRowsLaunch a) {
   __shared__ float part[32];
   pdl_launch_dependents();
   pdl_wait();
   const int64_t t = blockIdx.x;
   const int d = a.d, nc = d / 8;
-  float v[ITER][8];
-  float ss = 0.f;
+  uint4 raw[ITER];
 #pragma unroll
   for (int it = 0; it < ITER; ++it) {
     const int c = it * blockDim.x + threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[it][i] = 0.f;
-    if (c < nc) {
-      unpack8(__ldg(reinterpret_cast<const uint4*>(a.x + t * a.x_ld) + c), v[it]);
-      if constexpr (NORM) {
-        if (a.residual) {
-          float r[8];
-          unpack8(*(reinterpret_cast<const uint4*>(a.residual + t * a.r_ld) + c), r);
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // the stored sum is bf16, and the norm is that of what is stored
-            w[i] = pack_bf16(v[it][2 * i] + r[2 * i], v[it][2 * i + 1] + r[2 * i + 1]);
-            v[it][2 * i] = __uint_as_float(w[i] << 16);
-            v[it][2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-          }
-          if (a.sum) *(reinterpret_cast<uint4*>(a.sum + t * a.r_ld) + c) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else if (a.sum) {
-          *(reinterpret_cast<uint4*>(a.sum + t * a.r_ld) + c) =
-              *(reinterpret_cast<const uint4*>(a.x + t * a.x_ld) + c);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v[it][i], v[it][i], ss);
-      }
-    }
+    raw[it] = make_uint4(0u, 0u, 0u, 0u);
+    if (c < nc) raw[it] = *(reinterpret_cast<const uint4*>(a.x + t * a.x_ld) + c);
   }
   float rs = 1.f;
   if constexpr (NORM) {
+    float ss = 0.f;
+    if (a.residual) {
+      uint4 res[ITER];
+#pragma unroll
+      for (int it = 0; it < ITER; ++it) {
+        const int c = it * blockDim.x + threadIdx.x;
+        res[it] = make_uint4(0u, 0u, 0u, 0u);
+        if (c < nc) res[it] = *(reinterpret_cast<const uint4*>(a.residual + t * a.r_ld) + c);
+      }
+#pragma unroll
+      for (int it = 0; it < ITER; ++it) {
+        float v[8], r[8];
+        unpack8(raw[it], v);
+        unpack8(res[it], r);
+        raw[it] = make_uint4(pack_bf16(v[0] + r[0], v[1] + r[1]), pack_bf16(v[2] + r[2], v[3] + r[3]),
+                             pack_bf16(v[4] + r[4], v[5] + r[5]), pack_bf16(v[6] + r[6], v[7] + r[7]));
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < ITER; ++it) {
+      const int c = it * blockDim.x + threadIdx.x;
+      if (a.sum && c < nc) *(reinterpret_cast<uint4*>(a.sum + t * a.r_ld) + c) = raw[it];
+      float v[8];
+      unpack8(raw[it], v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (lane == 0) part[warp] = ss;
-    __syncthreads();
-    ss = lane < warps ? part[lane] : 0.f;
+    if (warps > 1) {
+      if (lane == 0) part[warp] = ss;
+      __syncthreads();
+      ss = lane < warps ? part[lane] : 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    }
     rs = rsqrtf(ss / static_cast<float>(d) + a.eps);
   }
   const float global = FMT == MOE_MX_NVFP4 && a.global ? __ldg(a.global) : 1.f;
 #pragma unroll
   for (int it = 0; it < ITER; ++it) {
     const int c = it * blockDim.x + threadIdx.x;
+    float v[8];
+    unpack8(raw[it], v);
     if constexpr (NORM) {
       if (c < nc) {
         float g[8];
         unpack8(__ldg(reinterpret_cast<const uint4*>(a.gain) + c), g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[it][i] = v[it][i] * rs * g[i];
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * rs * g[i];
       }
     }
     uint32_t w[4] = {0u, 0u, 0u, 0u};
     GroupScale sc{};
     if constexpr (FMT == MOE_MX_BF16) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[it][2 * i], v[it][2 * i + 1]);
+      for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     } else {
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[it][i]));
+      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       if constexpr (Mx<FMT>::group == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
       sc = group_scale<FMT>(m, global);
       uint32_t cw[2];
-      codes8<FMT>(v[it], sc, cw);
+      codes8<FMT>(v, sc, cw);
       w[0] = cw[0];
       w[1] = cw[1];
     }
     if (c >= nc) continue;
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t pos = a.positions ? __ldg(a.positions + t * a.k + j) : t;
-      if (pos < 0 || pos >= a.out_rows) continue;
-      uint8_t* row = a.codes + pos * code_pitch<FMT>(d);
-      if constexpr (FMT == MOE_MX_BF16) {
-        reinterpret_cast<uint4*>(row)[c] = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-        if constexpr (FMT == MOE_MX_MXFP8) reinterpret_cast<uint2*>(row)[c] = make_uint2(w[0], w[1]);
-        else reinterpret_cast<uint32_t*>(row)[c] = w[0];
-        constexpr int kLanes = Mx<FMT>::group / 8;
-        if (c % kLanes == 0) a.scales[pos * scale_pitch<FMT>(d) + c / kLanes] = static_cast<uint8_t>(sc.byte);
+    for (int j0 = 0; j0 < a.k; j0 += 8) {
+      int32_t at[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        at[j] = j0 + j >= a.k ? -1 : a.positions ? __ldg(a.positions + t * a.k + j0 + j) : static_cast<int32_t>(t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (at[j] < 0 || at[j] >= a.out_rows) continue;
+        uint8_t* row = a.codes + at[j] * code_pitch<FMT>(d);
+        if constexpr (FMT == MOE_MX_BF16) {
+          reinterpret_cast<uint4*>(row)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          if constexpr (FMT == MOE_MX_MXFP8) reinterpret_cast<uint2*>(row)[c] = make_uint2(w[0], w[1]);
+          else reinterpret_cast<uint32_t*>(row)[c] = w[0];
+          constexpr int kLanes = Mx<FMT>::group / 8;
+          if (c % kLanes == 0) a.scales[at[j] * scale_pitch<FMT>(d) + c / kLanes] = static_cast<uint8_t>(sc.byte);
+        }
       }
     }
   }
@@ -138,56 +153,84 @@ mx_rows_kernel(const MxRowsLaunch a) {
 template <int FMT, bool NORM>
 cudaError_t launch_rows(const MxRowsLaunch& a, cudaStream_t s) {
   const int nc = a.d / 8;
-  const int iters = (nc + kRowsMaxThreads - 1) / kRowsMaxThreads;
+  // Few rows: as many threads as the row has pieces, for the shortest way through one row.  More rows
+  // than SMs: 256 threads with several pieces each, so that an SM holds more rows in different phases.
+  const int most = a.n > 2 * device_sms() ? kRowsSplitThreads : kRowsMaxThreads;
+  int iters = 1;
+  while (iters * most < nc) iters *= 2;
   const int threads = ((nc + iters - 1) / iters + 31) / 32 * 32;
-  auto kern = iters == 1 ? mx_rows_kernel<FMT, NORM, 1> : mx_rows_kernel<FMT, NORM, 2>;
+  auto kern = iters == 1   ? mx_rows_kernel<FMT, NORM, 1>
+              : iters == 2 ? mx_rows_kernel<FMT, NORM, 2>
+              : iters == 4 ? mx_rows_kernel<FMT, NORM, 4>
+                           : mx_rows_kernel<FMT, NORM, 8>;
   return launch_maybe_overlapped(kern, static_cast<int>(a.n), threads, 0, s, a.overlap, a);
 }
+
+// A CTA covers 1024 pieces of eight columns, of as many rows as fit or of one row's
+// part, four pieces a thread: their loads are all under way before the first is used.
+constexpr int kDeqPieces = 1024;
 
 template <int FMT>
 __global__ void __launch_bounds__(256)
 mx_dequantise_kernel(int64_t rows, int32_t d, const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                      const float* __restrict__ global_p, uint16_t* __restrict__ out, int64_t out_ld) {
   const int nc = d / 8;
+  const int segs = (nc + kDeqPieces - 1) / kDeqPieces, rpb = nc < kDeqPieces ? kDeqPieces / nc : 1;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / segs) * rpb;
+  const int c0 = static_cast<int>(blockIdx.x % segs) * kDeqPieces;
   const float global = FMT == MOE_MX_NVFP4 && global_p ? __ldg(global_p) : 1.f;
-  const int64_t total = rows * nc, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
-    const int64_t r = i / nc;
-    const int c = static_cast<int>(i - r * nc);
-    const uint8_t* row = codes + r * code_pitch<FMT>(d);
-    uint4 o;
-    if constexpr (FMT == MOE_MX_BF16) {
-      o = __ldg(reinterpret_cast<const uint4*>(row) + c);
-    } else {
-      const uint32_t sb = __ldg(scales + r * scale_pitch<FMT>(d) + c / (Mx<FMT>::group / 8));
-      float sc;
-      if constexpr (FMT == MOE_MX_NVFP4) sc = e4m3_value(sb) * global;
-      else if (sb == 255u) sc = __uint_as_float(0x7fc00000u);
-      else sc = sb == 0u ? 0x1p-127f : __uint_as_float(sb << 23);
-      float v[8];
-      if constexpr (FMT == MOE_MX_MXFP8) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(row) + c);
+  int64_t r[4];
+  int c[4];
+  uint4 w[4];
+  uint32_t sb[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t pair = ((j < 2 ? w.x : w.y) >> (16 * (j & 1))) & 0xffffu;
-          const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair), __NV_E4M3));
-          v[2 * j] = __low2float(h);
-          v[2 * j + 1] = __high2float(h);
-        }
+  for (int u = 0; u < 4; ++u) {
+    const int i = 256 * u + threadIdx.x;
+    const int rl = nc < kDeqPieces ? i / nc : 0;
+    c[u] = nc < kDeqPieces ? i - rl * nc : c0 + i;
+    r[u] = rl < rpb && c[u] < nc && row0 + rl < rows ? row0 + rl : -1;
+    if (r[u] >= 0) {
+      const uint8_t* row = codes + r[u] * code_pitch<FMT>(d);
+      if constexpr (FMT == MOE_MX_BF16) {
+        w[u] = __ldg(reinterpret_cast<const uint4*>(row) + c[u]);
       } else {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(row) + c);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __half2 h = __half2(
-              __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>((w >> (8 * j)) & 0xffu), __NV_E2M1));
-          v[2 * j] = __low2float(h);
-          v[2 * j + 1] = __high2float(h);
+        if constexpr (FMT == MOE_MX_MXFP8) {
+          const uint2 q = __ldg(reinterpret_cast<const uint2*>(row) + c[u]);
+          w[u].x = q.x;
+          w[u].y = q.y;
+        } else {
+          w[u].x = __ldg(reinterpret_cast<const uint32_t*>(row) + c[u]);
         }
+        sb[u] = __ldg(scales + r[u] * scale_pitch<FMT>(d) + c[u] / (Mx<FMT>::group / 8));
       }
-      o = make_uint4(pack_bf16(v[0] * sc, v[1] * sc), pack_bf16(v[2] * sc, v[3] * sc), pack_bf16(v[4] * sc, v[5] * sc),
-                     pack_bf16(v[6] * sc, v[7] * sc));
     }
-    *(reinterpret_cast<uint4*>(out + r * out_ld) + c) = o;
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (r[u] < 0) continue;
+    uint4 o = w[u];
+    if constexpr (FMT != MOE_MX_BF16) {
+      float sc;
+      if constexpr (FMT == MOE_MX_NVFP4) sc = e4m3_value(sb[u]) * global;
+      else if (sb[u] == 255u) sc = __uint_as_float(0x7fc00000u);
+      else sc = sb[u] == 0u ? 0x1p-127f : __uint_as_float(sb[u] << 23);
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        __half2 h;
+        if constexpr (FMT == MOE_MX_MXFP8) {
+          const uint32_t pair = ((j < 2 ? w[u].x : w[u].y) >> (16 * (j & 1))) & 0xffffu;
+          h = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair), __NV_E4M3));
+        } else {
+          h = __half2(__nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>((w[u].x >> (8 * j)) & 0xffu),
+                                                 __NV_E2M1));
+        }
+        v[2 * j] = __low2float(h) * sc;
+        v[2 * j + 1] = __high2float(h) * sc;
+      }
+      o = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    }
+    *(reinterpret_cast<uint4*>(out + r[u] * out_ld) + c[u]) = o;
   }
 }
 
@@ -248,8 +291,11 @@ cudaError_t launch_mx_rows(int32_t fmt, const MxRowsLaunch& a, cudaStream_t s) {
 
 cudaError_t launch_mx_dequantise(int32_t fmt, int64_t rows, int32_t d, const uint8_t* codes, const uint8_t* scales,
                                  const float* global, uint16_t* out, int64_t out_ld, cudaStream_t s) {
-  const int64_t blocks = (rows * (d / 8) + 255) / 256;
-  const unsigned grid = static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20));
+  const int nc = d / 8;
+  const int64_t segs = (nc + kDeqPieces - 1) / kDeqPieces, rpb = nc < kDeqPieces ? kDeqPieces / nc : 1;
+  const int64_t blocks = (rows + rpb - 1) / rpb * segs;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(blocks);
   switch (fmt) {
     case MOE_MX_BF16: mx_dequantise_kernel<MOE_MX_BF16><<<grid, 256, 0, s>>>(rows, d, codes, scales, global, out, out_ld); break;
     case MOE_MX_MXFP8: mx_dequantise_kernel<MOE_MX_MXFP8><<<grid, 256, 0, s>>>(rows, d, codes, scales, global, out, out_ld); break;
