@@ -63,7 +63,7 @@ size_t moe_mx_scale_pitch(int32_t format, int64_t cols);
 /* Rows into a format:  Q(x[t]) written to row positions[t * k + j] for each j.
  *   x          [n] rows of d bf16, x_ld elements apart (>= d, a multiple of 8); 16-byte aligned
  *   positions  [n, k] int32; NULL: k = 1 and row t.  Entries outside [0, out_rows) are skipped.
- *   global     [1] fp32, NVFP4's factor g > 0 (NULL = 1); not read for other formats
+ *   global     [1] fp32, NVFP4's factor g, 2^-60 to 2^60 (NULL = 1); not read for other formats
  *   codes, scales  [out_rows] rows; scales not read for MOE_MX_BF16
  * d up to 16384. */
 moe_status moe_mx_quantise(int32_t format, int64_t n, int32_t k, int32_t d, const void *x, int64_t x_ld,

@@ -46,10 +46,10 @@ inline int64_t mx_chunks(const moe_mx_weights* w) { return (w->k + mx_cols(w->fo
 
 // ---------------------------------------------------------------- quantisation
 
-// What a group's codes are divided by, from the bits of its largest magnitude.
+// What a group's codes are divided by.
 struct GroupScale {
   uint32_t byte;  // the stored scale
-  float div;      // NVFP4: the divisor (0: all codes zero); MX formats: unused
+  float div;      // NVFP4: the divisor; MX formats: unused
   float mul;      // its reciprocal, exact for the MX formats; 0: all codes zero
 };
 
@@ -57,44 +57,48 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3)));
 }
 
+// a / b, correctly rounded, from b's correctly rounded reciprocal r: the quotient
+// a * r corrected by its own remainder (P. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990: q' = q + r (a - q b)).  b lies
+// within 2^-72 .. 2^72 here, and where a is so small that the remainder is not exact
+// the quotient rounds to zero in every format.  From `top` on, where the result
+// saturates, the quotient is left alone (it may be infinite).  Five instructions
+// against a division's twenty and a branch.
+__device__ __forceinline__ float quotient(float a, float b, float r, float top) {
+  const float q = a * r;
+  return fabsf(q) < top ? fmaf(fmaf(-q, b, a), r, q) : q;
+}
+
+// What all groups of an NVFP4 tensor share: its factor, six times it and that one's reciprocal.
+struct GroupFactor {
+  float g, six, inv;
+};
+template <int FMT>
+__device__ __forceinline__ GroupFactor group_factor(const float* global) {
+  if constexpr (FMT != MOE_MX_NVFP4) return GroupFactor{1.f, 6.f, 0.f};
+  const float g = global ? __ldg(global) : 1.f;
+  return GroupFactor{g, 6.0f * g, __frcp_rn(6.0f * g)};
+}
+
 // abs_bits: the largest of the group's |v| as fp32 bits.  Bits of non-negative
 // floats order as the floats do, with infinity and then NaN above all, so one
 // integer maximum finds the magnitude and a non-finite value alike.
 template <int FMT>
-__device__ __forceinline__ GroupScale group_scale(uint32_t abs_bits, float global) {
-  if (abs_bits >= 0x7f800000u) return GroupScale{FMT == MOE_MX_NVFP4 ? 0x7fu : 0xffu, 0.f, 0.f};
+__device__ __forceinline__ GroupScale group_scale(uint32_t abs_bits, const GroupFactor& f) {
+  const bool bad = abs_bits >= 0x7f800000u;
   if constexpr (FMT == MOE_MX_NVFP4) {
-    const float t = __fdiv_rn(__uint_as_float(abs_bits), 6.0f * global);
-    const uint32_t byte = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
-    const float div = e4m3_value(byte) * global;
-    return GroupScale{byte, div, div > 0.f ? __frcp_rn(div) : 0.f};
+    const float t = quotient(__uint_as_float(abs_bits), f.six, f.inv, 1024.f);
+    const uint32_t byte = bad ? 0x7fu : __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
+    const float div = e4m3_value(byte) * f.g;
+    return GroupScale{byte, div, !bad && div > 0.f ? __frcp_rn(div) : 0.f};
   } else {
     // The smallest k with a <= M 2^k: M = 1.75 2^8 or 1.5 2^2, so a = 1.m 2^e takes
     // k = e - 8 (e - 2) while 1.m is at most 1.75 (1.5), one more above that.
     constexpr uint32_t kTop = FMT == MOE_MX_MXFP8 ? 0x600000u : 0x400000u;
     constexpr int kExp = FMT == MOE_MX_MXFP8 ? 8 : 2;
     const int k127 = max(1, static_cast<int>(abs_bits >> 23) - kExp + ((abs_bits & 0x7fffffu) > kTop ? 1 : 0));
-    return GroupScale{static_cast<uint32_t>(k127), 0.f, __uint_as_float(static_cast<uint32_t>(254 - k127) << 23)};
-  }
-}
-
-// v / divisor, correctly rounded: the MX divisors are powers of two.  For NVFP4
-// the quotient v * r (r the correctly rounded reciprocal) is corrected by its
-// own remainder, which gives the correctly rounded quotient (P. Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor",
-// 1990, theorem on q' = q + r (a - q b)); a plain division costs about three
-// times as many instructions.  Outside the range where the remainder is exact
-// (|v| near the ends of fp32's range) the division itself is used.
-template <int FMT>
-__device__ __forceinline__ float scaled(float v, const GroupScale& s) {
-  if constexpr (FMT == MOE_MX_NVFP4) {
-    if (s.div >= 0x1p-80f && s.div <= 0x1p80f) {
-      const float q = v * s.mul;
-      return fmaf(fmaf(-q, s.div, v), s.mul, q);
-    }
-    return s.div > 0.f ? __fdiv_rn(v, s.div) : 0.f;
-  } else {
-    return s.mul == 0.f ? 0.f : v * s.mul;
+    return bad ? GroupScale{0xffu, 0.f, 0.f}
+               : GroupScale{static_cast<uint32_t>(k127), 0.f, __uint_as_float(static_cast<uint32_t>(254 - k127) << 23)};
   }
 }
 
@@ -105,12 +109,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // Codes of eight consecutive columns: 1 word of e2m1 or 2 of e4m3.
 template <int FMT>
-__device__ __forceinline__ void codes8(const float (&v)[8], const GroupScale& s, uint32_t (&w)[2]) {
-  // a non-finite group: zero codes whatever its values
-  const bool dead = s.mul == 0.f && s.div == 0.f;
+__device__ __forceinline__ void codes8(const float* v, const GroupScale& s, uint32_t (&w)[2]) {
   float t[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = dead ? 0.f : scaled<FMT>(v[i], s);
+  for (int i = 0; i < 8; ++i) {
+    const float q = FMT == MOE_MX_NVFP4 ? quotient(v[i], s.div, s.mul, 8.f) : v[i] * s.mul;
+    t[i] = s.mul == 0.f ? 0.f : q;  // a zero divisor, or a group that is not finite
+  }
   if constexpr (FMT == MOE_MX_MXFP8) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -146,7 +151,6 @@ struct MxRowsLaunch {
   uint16_t* sum;
   uint8_t* codes;
   uint8_t* scales;
-  bool overlap;  // dependent launch behind the routing plan
 };
 cudaError_t launch_mx_rows(int32_t fmt, const MxRowsLaunch& a, cudaStream_t s);
 cudaError_t launch_mx_dequantise(int32_t fmt, int64_t rows, int32_t d, const uint8_t* codes, const uint8_t* scales,
@@ -173,8 +177,9 @@ struct MxProductLaunch {
   uint8_t* h_scales;
   uint32_t* err;
   int num_sms;
-  // dependent launch whose offsets were complete before the kernel in front of it began
-  bool overlap;
+  // the offsets and weights were complete before the kernel in front began: they are read, and
+  // weights streamed, while that one still runs
+  bool early;
 };
 cudaError_t launch_mx_product(const MxProductLaunch& a, cudaStream_t s);
 

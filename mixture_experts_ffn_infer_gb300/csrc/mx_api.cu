@@ -323,7 +323,7 @@ moe_status moe_mx_layer_forward(const moe_mx_weights* gu, const moe_mx_weights* 
   g.h_scales = ws_at<uint8_t>(ws, L.h_scales);
   g.err = err;
   g.num_sms = device_sms();
-  g.overlap = true;  // the routing plan was complete before the rows' kernel began
+  g.early = true;  // the routing plan was complete before the rows' kernel began
   if (g.num_sms <= 0 || launch_mx_product(g, s) != cudaSuccess) return MOE_ERR_CUDA;
 
   MxProductLaunch q{};
@@ -341,7 +341,7 @@ moe_status moe_mx_layer_forward(const moe_mx_weights* gu, const moe_mx_weights* 
   q.row_weight = topk_weight;
   q.err = err;
   q.num_sms = g.num_sms;
-  q.overlap = true;
+  q.early = true;
   if (launch_mx_product(q, s) != cudaSuccess) return MOE_ERR_CUDA;
   return launch_combine(static_cast<const uint16_t*>(q.out), nullptr, static_cast<const uint16_t*>(sum),
                         static_cast<int32_t>(n), top_k, d, out, out_is_fp32, s) == cudaSuccess

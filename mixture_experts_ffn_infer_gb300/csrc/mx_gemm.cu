@@ -47,6 +47,8 @@ constexpr int kWarpWeights = 0, kWarpIssue = 1, kWarpRows = 2, kWarpScales = 4, 
 constexpr int kRegsLow = 56, kRegsScales = 104, kRegsEpi = 176;
 static_assert(128 * (kRegsLow + kRegsScales + 2 * kRegsEpi) <= 65536, "register split");
 
+constexpr int kOutBf16 = 0, kOutF16 = 1, kOutSwiglu = 2;
+
 template <int FMT>
 struct Cfg {
   static constexpr int kWords = Mx<FMT>::words;
@@ -75,7 +77,7 @@ struct Args {
   const float* x_global;
   const int32_t* offsets;
   void* out;
-  int32_t out_f16, out_vec;
+  int32_t out_vec;
   int64_t out_rows, out_ld;
   const int32_t* out_pos;
   const float* row_weight;
@@ -84,7 +86,7 @@ struct Args {
   uint8_t* h_scales;
   int64_t h_row_bytes, h_pitch;
   uint32_t* err;
-  int32_t overlap;
+  int32_t early;
 };
 
 // Rows' maps with boxes of 16, 32, 64 and 128 rows: a tile's copy brings its own
@@ -224,7 +226,7 @@ __device__ __forceinline__ Unit unit_of(const int32_t* first_tile, const int32_t
   return un;
 }
 
-template <int FMT, bool SWIGLU>
+template <int FMT, int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
   using C = Cfg<FMT>;
@@ -263,7 +265,7 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
-  if (!a.overlap) pdl_wait();  // else only what the kernel in front writes is waited for, by its readers
+  if (!a.early) pdl_wait();  // else only what the kernel in front writes is waited for, by its readers
   // The tile plan: thread i counts the tiles of experts 2 i and 2 i + 1.
   {
     int n[2] = {0, 0};
@@ -335,7 +337,7 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
       }
       __syncwarp();
     } else if (warp == kWarpRows) {
-      if (a.overlap) pdl_wait();
+      if (a.early) pdl_wait();
       if (lane == 0) {
         const uint64_t pol = policy_evict_last();
         uint32_t it = 0;
@@ -472,142 +474,183 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
-    if (a.overlap) pdl_wait();
+    if (a.early) pdl_wait();
     const int q = warp & 3, hf = (warp - kWarpEpi) >> 2;
     const int tok = q * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const float xg = a.x_global ? __ldg(a.x_global) : 1.f;
-    const float hg = SWIGLU && a.h_global ? __ldg(a.h_global) : 1.f;
-    uint32_t ui = 0;
-    for (int x = blockIdx.x; x < total; x += stride, ++ui) {
+    // What this thread needs for a unit besides the accumulators, fetched a unit ahead.
+    struct Mine {
+      int u, row, to;  // packed block row; the thread's row, and where it goes (-1: nowhere)
+      float f0, f1;    // factors of the two 128-column halves
+    };
+    auto mine_of = [&](int x) {
+      Mine m{0, 0, -1, 0.f, 0.f};
+      if (x >= total) return m;
       const Unit un = unit_at(x);
-      const bool valid = tok < un.nv;
-      const int64_t row = static_cast<int64_t>(un.row0) + tok;
-      const float f0 = xg * (a.alpha ? __ldg(a.alpha + un.e) : 1.f);
-      float f1 = f0;
-      int64_t dst = row;
-      if constexpr (SWIGLU) {
-        f1 = xg * (a.alpha_up ? __ldg(a.alpha_up + un.e) : 1.f);
-      } else {
-        if (valid && a.out_pos) dst = __ldg(a.out_pos + row);
+      m.u = un.u;
+      m.row = un.row0 + tok;
+      m.f0 = xg * (a.alpha ? __ldg(a.alpha + un.e) : 1.f);
+      if constexpr (OUT == kOutSwiglu) m.f1 = xg * (a.alpha_up ? __ldg(a.alpha_up + un.e) : 1.f);
+      if (tok < un.nv) {
+        m.to = OUT != kOutSwiglu && a.out_pos ? __ldg(a.out_pos + m.row) : m.row;
+        if (OUT != kOutSwiglu && m.to >= a.out_rows) m.to = -1;
+        if (OUT != kOutSwiglu && a.row_weight && m.to >= 0) m.f0 *= __ldg(a.row_weight + m.to);
       }
-      const bool store = valid && (SWIGLU || (dst >= 0 && dst < a.out_rows));
-      float wgt = 1.f;
-      if (!SWIGLU && store && a.row_weight) wgt = __ldg(a.row_weight + dst);
+      return m;
+    };
+    uint32_t ui = 0;
+    Mine me = mine_of(blockIdx.x);
+    for (int x = blockIdx.x; x < total; x += stride, ++ui) {
       const int ab = ui % C::kAcc;
       if (!__all_sync(0xffffffffu, wait_bounded(acc_full(ab), (ui / C::kAcc) & 1, abort_flag, a.err))) break;
       tc_fence_after();
       const uint32_t tcol = tmem + lane_base + 256u * ab + 64u * hf;
-      uint32_t p0[64], p1[64];
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty(ab));
+      };
+      const bool any = __any_sync(0xffffffffu, me.to >= 0);
+      Mine next;
+      if constexpr (OUT == kOutSwiglu) {
+        // 32 features at a time (the code of one pass is 10 KB: its first run on an SM costs as much as its work)
+        const GroupFactor hf_factor = group_factor<FMT>(a.h_global);
+        uint8_t* hc = a.h_codes + static_cast<int64_t>(me.row) * a.h_row_bytes;
+        uint8_t* hs = a.h_scales + static_cast<int64_t>(me.row) * a.h_pitch;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const int at = 128 * me.u + 64 * hf + 32 * half;
+          float h[32];
+          {
+            uint32_t g[32], u[32];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        tmem_ld16(tcol + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(&p0[16 * i]));
-        tmem_ld16(tcol + 128 + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(&p1[16 * i]));
-      }
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty(ab));
-      bool overflow = false;
-      if constexpr (SWIGLU) {
-        const int n0 = 128 * un.u + 64 * hf;  // first of this thread's 64 features
-        if (store && n0 < a.n_out) {
-          uint8_t* hc = a.h_codes + row * a.h_row_bytes;
-          uint8_t* hs = a.h_scales + row * a.h_pitch;
+            for (int i = 0; i < 2; ++i) {
+              tmem_ld16(tcol + 32 * half + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(&g[16 * i]));
+              tmem_ld16(tcol + 128 + 32 * half + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(&u[16 * i]));
+            }
+            tmem_ld_wait();
+            if (half == 1) release();
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (n0 + 32 * half < a.n_out) {
-              const int at = n0 + 32 * half;
-              float h[32];
+            for (int i = 0; i < 32; ++i) h[i] = silu(__uint_as_float(g[i]) * me.f0) * (__uint_as_float(u[i]) * me.f1);
+          }
+          if (me.to >= 0 && at < a.n_out) {
+            if constexpr (FMT == MOE_MX_BF16) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                h[i] = silu(__uint_as_float(p0[32 * half + i]) * f0) * (__uint_as_float(p1[32 * half + i]) * f1);
-              if constexpr (FMT == MOE_MX_BF16) {
+              for (int v = 0; v < 4; ++v)
+                *reinterpret_cast<uint4*>(hc + 2 * at + 16 * v) =
+                    make_uint4(pack_bf16(h[8 * v], h[8 * v + 1]), pack_bf16(h[8 * v + 2], h[8 * v + 3]),
+                               pack_bf16(h[8 * v + 4], h[8 * v + 5]), pack_bf16(h[8 * v + 6], h[8 * v + 7]));
+            } else {
+              constexpr int G = Mx<FMT>::group;
+              uint32_t out[8];
+              uint32_t sbytes = 0;
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                  *reinterpret_cast<uint4*>(hc + 2 * at + 16 * v) =
-                      make_uint4(pack_bf16(h[8 * v], h[8 * v + 1]), pack_bf16(h[8 * v + 2], h[8 * v + 3]),
-                                 pack_bf16(h[8 * v + 4], h[8 * v + 5]), pack_bf16(h[8 * v + 6], h[8 * v + 7]));
-              } else {
-                constexpr int G = Mx<FMT>::group;
-                uint32_t out[8];
-                uint32_t sbytes = 0;
+              for (int g = 0; g < 32 / G; ++g) {
+                uint32_t m = 0;
 #pragma unroll
-                for (int g = 0; g < 32 / G; ++g) {
-                  uint32_t m = 0;
+                for (int i = 0; i < G; ++i) m = max(m, abs_bits(h[G * g + i]));
+                const GroupScale sc = group_scale<FMT>(m, hf_factor);
+                sbytes |= sc.byte << (8 * g);
 #pragma unroll
-                  for (int i = 0; i < G; ++i) m = max(m, abs_bits(h[G * g + i]));
-                  const GroupScale sc = group_scale<FMT>(m, hg);
-                  sbytes |= sc.byte << (8 * g);
-#pragma unroll
-                  for (int v = 0; v < G / 8; ++v) {
-                    uint32_t w[2];
-                    codes8<FMT>(*reinterpret_cast<const float(*)[8]>(&h[G * g + 8 * v]), sc, w);
-                    if constexpr (FMT == MOE_MX_MXFP8) {
-                      out[2 * v] = w[0];
-                      out[2 * v + 1] = w[1];
-                    } else {
-                      out[(G / 8) * g + v] = w[0];
-                    }
+                for (int v = 0; v < G / 8; ++v) {
+                  uint32_t w[2];
+                  codes8<FMT>(h + G * g + 8 * v, sc, w);
+                  if constexpr (FMT == MOE_MX_MXFP8) {
+                    out[2 * v] = w[0];
+                    out[2 * v + 1] = w[1];
+                  } else {
+                    out[(G / 8) * g + v] = w[0];
                   }
                 }
-                if constexpr (FMT == MOE_MX_MXFP8) {
-                  *reinterpret_cast<uint4*>(hc + at) = make_uint4(out[0], out[1], out[2], out[3]);
-                  *reinterpret_cast<uint4*>(hc + at + 16) = make_uint4(out[4], out[5], out[6], out[7]);
-                } else {
-                  *reinterpret_cast<uint4*>(hc + at / 2) = make_uint4(out[0], out[1], out[2], out[3]);
-                }
-                if constexpr (G == 16) *reinterpret_cast<uint16_t*>(hs + at / 16) = static_cast<uint16_t>(sbytes);
-                else hs[at / 32] = static_cast<uint8_t>(sbytes);
               }
+              if constexpr (FMT == MOE_MX_MXFP8) {
+                *reinterpret_cast<uint4*>(hc + at) = make_uint4(out[0], out[1], out[2], out[3]);
+                *reinterpret_cast<uint4*>(hc + at + 16) = make_uint4(out[4], out[5], out[6], out[7]);
+              } else {
+                *reinterpret_cast<uint4*>(hc + at / 2) = make_uint4(out[0], out[1], out[2], out[3]);
+              }
+              if constexpr (G == 16) *reinterpret_cast<uint16_t*>(hs + at / 16) = static_cast<uint16_t>(sbytes);
+              else hs[at / 32] = static_cast<uint8_t>(sbytes);
             }
           }
         }
+        next = mine_of(x + stride);
       } else {
         uint16_t* o = static_cast<uint16_t*>(a.out);
-        uint16_t* mine = reinterpret_cast<uint16_t*>(smem + C::kTurnOff + (warp - kWarpEpi) * 1024);
+        float top = 0.f;  // largest magnitude, for f16's range
+        auto pack2 = [&](uint32_t r0, uint32_t r1) {
+          const float y0 = __uint_as_float(r0) * me.f0, y1 = __uint_as_float(r1) * me.f0;
+          if constexpr (OUT == kOutF16) {
+            top = fmaxf(top, fmaxf(fabsf(y0), fabsf(y1)));
+            const __half2 h2 = __floats2half2_rn(y0, y1);
+            return *reinterpret_cast<const uint32_t*>(&h2);
+          } else {
+            return pack_bf16(y0, y1);
+          }
+        };
+        if (a.out_vec && 256 * (me.u + 1) <= a.n_out) {
+          uint32_t p[2][64];
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
+          for (int i = 0; i < 4; ++i) {
+            tmem_ld16(tcol + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(&p[0][16 * i]));
+            tmem_ld16(tcol + 128 + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(&p[1][16 * i]));
+          }
+          tmem_ld_wait();
+          release();
+          next = mine_of(x + stride);
+          if (me.to >= 0) {
+            uint16_t* to = o + static_cast<int64_t>(me.to) * a.out_ld + 256 * me.u + 64 * hf;
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int at = 256 * un.u + 128 * m + 64 * hf + 16 * v;
-            if (at >= a.n_out) continue;
-            uint32_t w[8];
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t r0 = m ? p1[16 * v + 2 * i] : p0[16 * v + 2 * i];
-              const uint32_t r1 = m ? p1[16 * v + 2 * i + 1] : p0[16 * v + 2 * i + 1];
-              const float y0 = __uint_as_float(r0) * f0 * wgt, y1 = __uint_as_float(r1) * f0 * wgt;
-              if (a.out_f16) {
-                overflow |= store && ((fabsf(y0) >= 65520.f) || (fabsf(y1) >= 65520.f));
-                const __half2 h2 = __floats2half2_rn(y0, y1);
-                w[i] = *reinterpret_cast<const uint32_t*>(&h2);
-              } else {
-                w[i] = pack_bf16(y0, y1);
+              for (int v = 0; v < 4; ++v) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = pack2(p[m][16 * v + 2 * i], p[m][16 * v + 2 * i + 1]);
+                stg256(to + 128 * m + 16 * v, w);
               }
-            }
-            if (a.out_vec && at + 16 <= a.n_out) {
-              if (store) stg256(o + dst * a.out_ld + at, w);
-            } else {
-              // rows that are not aligned, or the last columns: turned through shared memory so
-              // that half a warp writes 16 columns of one row
+          }
+        } else {
+          // Rows that are not aligned, or the last block row: 16 columns at a time, turned through
+          // shared memory so that eight lanes write the 16 columns of one row.
+          uint8_t* turn = smem + C::kTurnOff + (warp - kWarpEpi) * 1024;
+          const uint32_t rows_on = __ballot_sync(0xffffffffu, me.to >= 0);
+          const int last = 32 - __clz(rows_on);  // rows up to the last that is written
+#pragma unroll 1
+          for (int v = 0; v < 8; ++v) {
+            uint32_t p[16], w[8];
+            tmem_ld16(tcol + 128 * (v >> 2) + 16 * (v & 3), p);
+            tmem_ld_wait();
+            const int at = 256 * me.u + 128 * (v >> 2) + 64 * hf + 16 * (v & 3);
+            if (any && at < a.n_out) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = pack2(p[2 * i], p[2 * i + 1]);
               __syncwarp();
-              reinterpret_cast<uint4*>(mine)[2 * lane] = make_uint4(w[0], w[1], w[2], w[3]);
-              reinterpret_cast<uint4*>(mine)[2 * lane + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+              reinterpret_cast<uint4*>(turn)[2 * lane] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(turn)[2 * lane + 1] = make_uint4(w[4], w[5], w[6], w[7]);
               __syncwarp();
-              const int col = lane & 15;
-#pragma unroll 4
-              for (int i = 0; i < 16; ++i) {
-                const int r = 2 * i + (lane >> 4);
-                const int64_t to = __shfl_sync(0xffffffffu, dst, r);
-                const bool on = __shfl_sync(0xffffffffu, static_cast<int>(store), r) != 0;
-                if (on && at + col < a.n_out) o[to * a.out_ld + at + col] = mine[16 * r + col];
+              const int col = at + 2 * (lane & 7);
+              for (int r0 = 0; r0 < last; r0 += 4) {
+                const int r = r0 + (lane >> 3);
+                const int to = __shfl_sync(0xffffffffu, me.to, r);
+                if (to < 0) continue;
+                const uint32_t two = *reinterpret_cast<const uint32_t*>(turn + 32 * r + 4 * (lane & 7));
+                uint16_t* at_row = o + static_cast<int64_t>(to) * a.out_ld;
+                if (col < a.n_out) at_row[col] = static_cast<uint16_t>(two);
+                if (col + 1 < a.n_out) at_row[col + 1] = static_cast<uint16_t>(two >> 16);
               }
             }
           }
+          release();
+          next = mine_of(x + stride);
+        }
+        if (OUT == kOutF16) {
+          const bool over = me.to >= 0 && top >= 65520.f;  // f16 rounds these to infinity
+          if (__any_sync(0xffffffffu, over) && lane == 0) atomicOr(a.err, DEV_ERR_RANGE);
         }
       }
-      if (__any_sync(0xffffffffu, overflow) && lane == 0) atomicOr(a.err, DEV_ERR_RANGE);
+      me = next;
     }
   }
   __syncthreads();
@@ -617,10 +660,10 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
   }
 }
 
-template <int FMT, bool SWIGLU>
+template <int FMT, int OUT>
 cudaError_t launch(const MxProductLaunch& g, cudaStream_t s) {
   using C = Cfg<FMT>;
-  auto kern = mx_product_kernel<FMT, SWIGLU>;
+  auto kern = mx_product_kernel<FMT, OUT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   // An increase of the register split that cannot be met never returns: launch only if the kernel's own
@@ -650,7 +693,6 @@ cudaError_t launch(const MxProductLaunch& g, cudaStream_t s) {
   a.x_global = FMT == MOE_MX_NVFP4 ? g.x_global : nullptr;
   a.offsets = g.offsets;
   a.out = g.out;
-  a.out_f16 = g.out_f16;
   a.out_vec = reinterpret_cast<uintptr_t>(g.out) % 32 == 0 && g.out_ld % 16 == 0;
   a.out_rows = g.out_rows;
   a.out_ld = g.out_ld;
@@ -662,7 +704,7 @@ cudaError_t launch(const MxProductLaunch& g, cudaStream_t s) {
   a.h_row_bytes = static_cast<int64_t>(moe_mx_code_bytes(FMT, w->n_out));
   a.h_pitch = static_cast<int64_t>(moe_mx_scale_pitch(FMT, w->n_out));
   a.err = g.err;
-  a.overlap = g.overlap ? 1 : 0;
+  a.early = g.early ? 1 : 0;
   RowMaps maps;
   for (int i = 0; i < 4; ++i)
     if (!encode_rows_map(&maps.box[i], g.x_codes, moe_mx_code_bytes(FMT, w->k), g.rows, 16u << i))
@@ -671,18 +713,23 @@ cudaError_t launch(const MxProductLaunch& g, cudaStream_t s) {
   const int64_t tiles = static_cast<int64_t>(g.rows) / kTile + (g.rows < w->num_experts ? g.rows : w->num_experts);
   const int64_t units = tiles * a.upt;
   const int grid = static_cast<int>(units < g.num_sms ? units : g.num_sms);
-  return launch_maybe_overlapped(kern, grid, kThreads, C::kSmem, s, g.overlap, maps, a);
+  return launch_maybe_overlapped(kern, grid, kThreads, C::kSmem, s, true, maps, a);
 }
 
 }  // namespace
 
+template <int FMT>
+static cudaError_t launch_format(const MxProductLaunch& g, cudaStream_t s) {
+  if (g.w->swiglu) return launch<FMT, kOutSwiglu>(g, s);
+  return g.out_f16 ? launch<FMT, kOutF16>(g, s) : launch<FMT, kOutBf16>(g, s);
+}
+
 cudaError_t launch_mx_product(const MxProductLaunch& g, cudaStream_t s) {
-  const bool sw = g.w->swiglu != 0;
   switch (g.w->format) {
-    case MOE_MX_BF16: return sw ? launch<MOE_MX_BF16, true>(g, s) : launch<MOE_MX_BF16, false>(g, s);
-    case MOE_MX_MXFP8: return sw ? launch<MOE_MX_MXFP8, true>(g, s) : launch<MOE_MX_MXFP8, false>(g, s);
-    case MOE_MX_MXFP4: return sw ? launch<MOE_MX_MXFP4, true>(g, s) : launch<MOE_MX_MXFP4, false>(g, s);
-    case MOE_MX_NVFP4: return sw ? launch<MOE_MX_NVFP4, true>(g, s) : launch<MOE_MX_NVFP4, false>(g, s);
+    case MOE_MX_BF16: return launch_format<MOE_MX_BF16>(g, s);
+    case MOE_MX_MXFP8: return launch_format<MOE_MX_MXFP8>(g, s);
+    case MOE_MX_MXFP4: return launch_format<MOE_MX_MXFP4>(g, s);
+    case MOE_MX_NVFP4: return launch_format<MOE_MX_NVFP4>(g, s);
   }
   return cudaErrorInvalidValue;
 }

@@ -1,5 +1,7 @@
 // Rows into and out of the microscaled formats (moe_mx.h), and the packed
-// weight layout.  All four kernels move bytes: HBM bounds them.
+// weight layout.  All four kernels move bytes: HBM bounds them.  Rows in and out
+// are dependent launches that wait before they read anything, so that in a
+// sequence of short calls one's launch overlaps the other's end.
 //
 // mx_rows_kernel       - [add the residual, RMS norm,] quantise, write to each
 //                        position of the token.  One CTA per token; a thread
@@ -96,7 +98,7 @@ mx_rows_kernel(const MxRowsLaunch a) {
     }
     rs = rsqrtf(ss / static_cast<float>(d) + a.eps);
   }
-  const float global = FMT == MOE_MX_NVFP4 && a.global ? __ldg(a.global) : 1.f;
+  const GroupFactor factor = group_factor<FMT>(a.global);
 #pragma unroll
   for (int it = 0; it < ITER; ++it) {
     const int c = it * blockDim.x + threadIdx.x;
@@ -121,7 +123,7 @@ mx_rows_kernel(const MxRowsLaunch a) {
       for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       if constexpr (Mx<FMT>::group == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      sc = group_scale<FMT>(m, global);
+      sc = group_scale<FMT>(m, factor);
       uint32_t cw[2];
       codes8<FMT>(v, sc, cw);
       w[0] = cw[0];
@@ -163,7 +165,7 @@ cudaError_t launch_rows(const MxRowsLaunch& a, cudaStream_t s) {
               : iters == 2 ? mx_rows_kernel<FMT, NORM, 2>
               : iters == 4 ? mx_rows_kernel<FMT, NORM, 4>
                            : mx_rows_kernel<FMT, NORM, 8>;
-  return launch_maybe_overlapped(kern, static_cast<int>(a.n), threads, 0, s, a.overlap, a);
+  return launch_maybe_overlapped(kern, static_cast<int>(a.n), threads, 0, s, true, a);
 }
 
 // A CTA covers 1024 pieces of eight columns, of as many rows as fit or of one row's
@@ -174,6 +176,8 @@ template <int FMT>
 __global__ void __launch_bounds__(256)
 mx_dequantise_kernel(int64_t rows, int32_t d, const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                      const float* __restrict__ global_p, uint16_t* __restrict__ out, int64_t out_ld) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int nc = d / 8;
   const int segs = (nc + kDeqPieces - 1) / kDeqPieces, rpb = nc < kDeqPieces ? kDeqPieces / nc : 1;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / segs) * rpb;
@@ -295,15 +299,12 @@ cudaError_t launch_mx_dequantise(int32_t fmt, int64_t rows, int32_t d, const uin
   const int64_t segs = (nc + kDeqPieces - 1) / kDeqPieces, rpb = nc < kDeqPieces ? kDeqPieces / nc : 1;
   const int64_t blocks = (rows + rpb - 1) / rpb * segs;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const unsigned grid = static_cast<unsigned>(blocks);
-  switch (fmt) {
-    case MOE_MX_BF16: mx_dequantise_kernel<MOE_MX_BF16><<<grid, 256, 0, s>>>(rows, d, codes, scales, global, out, out_ld); break;
-    case MOE_MX_MXFP8: mx_dequantise_kernel<MOE_MX_MXFP8><<<grid, 256, 0, s>>>(rows, d, codes, scales, global, out, out_ld); break;
-    case MOE_MX_MXFP4: mx_dequantise_kernel<MOE_MX_MXFP4><<<grid, 256, 0, s>>>(rows, d, codes, scales, global, out, out_ld); break;
-    case MOE_MX_NVFP4: mx_dequantise_kernel<MOE_MX_NVFP4><<<grid, 256, 0, s>>>(rows, d, codes, scales, global, out, out_ld); break;
-    default: return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
+  auto kern = fmt == MOE_MX_BF16    ? mx_dequantise_kernel<MOE_MX_BF16>
+              : fmt == MOE_MX_MXFP8 ? mx_dequantise_kernel<MOE_MX_MXFP8>
+              : fmt == MOE_MX_MXFP4 ? mx_dequantise_kernel<MOE_MX_MXFP4>
+                                    : mx_dequantise_kernel<MOE_MX_NVFP4>;
+  return launch_maybe_overlapped(kern, static_cast<int>(blocks), 256, 0, s, true, rows, d, codes, scales, global, out,
+                                 out_ld);
 }
 
 cudaError_t launch_mx_pack(const moe_mx_weights* w, const uint8_t* codes, const uint8_t* scales,
