@@ -14,7 +14,6 @@ torch and then call the same entry points.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 from typing import Optional
@@ -152,6 +151,8 @@ MOE_STATIC_SCRATCH_BYTES = 8 << 20
 def load_library(path: Optional[str] = None):
     """Load the CUDA library (raises if it is absent: there is no other implementation)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or LIB_PATH
@@ -524,309 +525,16 @@ def layer_forward(hidden, gain, eps, topk_ids, topk_weight, bank, shared=None, w
     return out
 
 
-# ---------------------------------------------------------------- microscaled formats
-# A decode step's call is a few microseconds of GPU time: the checks below are written to cost little on the host
-# (no message is formatted, and no library call made, for arguments that pass).
+# ---------------------------------------------------------------- microscaled formats (mx.py, which needs torch)
 
-_MX_BITS = (16, 8, 4, 4)
-_MX_GROUP = (0, 32, 32, 16)
+_MX_NAMES = ("MxRows", "MxWeights", "mx_rows", "mx_workspace", "mx_quantise", "mx_add_rmsnorm", "mx_dequantise",
+             "mx_pack", "mx_grouped_product", "mx_grouped_swiglu", "mx_layer_forward")
 
 
-def _mx_width(fmt, cols):
-    """(code bytes, scale pitch) of a row, as moe_mx_code_bytes and moe_mx_scale_pitch give them."""
-    if not 0 <= fmt <= 3 or cols <= 0 or cols & 31:
-        raise MoeError(2, "moe_mx_code_bytes")
-    return cols * _MX_BITS[fmt] >> 3, (-(-(cols // _MX_GROUP[fmt]) // 16) * 16 if fmt else 0)
-
-
-class MxRows:
-    """Rows of `cols` columns in a microscaled format: uint8 codes [rows, .] and scales [rows, pitch] (None for
-    bf16), and NVFP4's fp32 factor [1] (None = 1)."""
-
-    __slots__ = ("fmt", "cols", "codes", "scales", "global_scale")
-
-    def __init__(self, fmt, cols, codes, scales=None, global_scale=None):
-        self.fmt, self.cols, self.codes, self.scales, self.global_scale = fmt, cols, codes, scales, global_scale
-
-    @property
-    def rows(self):
-        return self.codes.shape[0]
-
-
-class MxWeights:
-    """Experts' matrices [num_experts, n_out, k] (two of them, gate and up, with swiglu) in the packed layout;
-    alpha, alpha_up: fp32 [num_experts] factors of the products (None = 1)."""
-
-    def __init__(self, fmt, num_experts, n_out, k, packed, alpha=None, alpha_up=None, swiglu=False):
-        self.fmt, self.num_experts, self.n_out, self.k = fmt, num_experts, n_out, k
-        self.packed, self.alpha, self.alpha_up, self.swiglu = packed, alpha, alpha_up, bool(swiglu)
-
-    def __setattr__(self, name, value):
-        self.__dict__[name] = value
-        self.__dict__["_checked"] = None       # the struct below is of the attributes as they were
-
-    def struct(self) -> moe_mx_weights:
-        return moe_mx_weights(self.fmt, self.num_experts, self.n_out, self.k, int(self.swiglu), _addr(self.packed),
-                              _addr(self.alpha), _addr(self.alpha_up))
-
-    def checked(self, dev):
-        """The struct, once the tensors have been checked against it."""
-        got = self._checked
-        if got is None or got[1] != dev:
-            st = self.struct()
-            nbytes = moe_mx_packed_bytes(st)
-            if nbytes == 0:
-                raise MoeError(2, "moe_mx_packed_bytes")
-            if self.packed.nbytes != nbytes or not self.packed.is_contiguous() or self.packed.get_device() != dev:
-                raise ValueError(f"packed: expected {nbytes} contiguous bytes on device {dev}")
-            _mx_scalar(self.alpha, "alpha", dev, self.num_experts)
-            _mx_scalar(self.alpha_up, "alpha_up", dev, self.num_experts)
-            got = self.__dict__["_checked"] = (st, dev)
-        return got[0]
-
-
-def _on_stream(fn):
-    """What the call allocates (results, a workspace of its own) belongs to the stream that it launches on."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        import torch
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream))
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
-
-
-def _mx_tensor(t, name, dtype, shape, dev):
-    """The tensor that a library call reads through its pointer: dense, on the device, of this type and shape."""
-    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on device {dev}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-
-
-def _mx_strided(t, name, shape, dev):
-    """bf16 rows: the row stride in elements (that of a single row is not used, and torch may report any)."""
-    import torch
-    if t.dtype != torch.bfloat16 or t.shape != shape or t.get_device() != dev or t.stride(1) != 1:
-        raise ValueError(f"{name}: expected bf16 rows {tuple(shape)} on device {dev}, got {t.dtype} {tuple(t.shape)} "
-                         f"on {t.device}")
-    ld = t.stride(0)
-    return ld if shape[0] > 1 else max(ld, shape[1])
-
-
-def _mx_scalar(t, name, dev, count=1):
-    if t is not None:
-        import torch
-        if t.dtype != torch.float32 or t.numel() != count or t.get_device() != dev or not t.is_contiguous():
-            raise ValueError(f"{name}: expected {count} fp32 value(s) on device {dev}")
-
-
-def _mx_check_rows(r: MxRows, dev):
-    import torch
-    codes = r.codes
-    n = codes.shape[0]
-    cb, pitch = _mx_width(r.fmt, r.cols)
-    _mx_tensor(codes, "codes", torch.uint8, (n, cb), dev)
-    if pitch:
-        if r.scales is None:
-            raise ValueError("scales: missing")
-        _mx_tensor(r.scales, "scales", torch.uint8, (n, pitch), dev)
-    if r.global_scale is not None:
-        _mx_scalar(r.global_scale, "global_scale", dev)
-    return n
-
-
-def mx_rows(fmt, rows, cols, device="cuda", global_scale=None) -> MxRows:
-    """Uninitialised rows."""
-    import torch
-    cb, pitch = _mx_width(fmt, cols)
-    codes = torch.empty((rows, cb), dtype=torch.uint8, device=device)
-    return MxRows(fmt, cols, codes, torch.empty((rows, pitch), dtype=torch.uint8, device=device) if pitch else None,
-                  global_scale)
-
-
-def _mx_out(fmt, n, d, positions, out_rows, global_scale, out, device, dev):
-    """(k, rows, the rows to write) of a call that writes n tokens' rows."""
-    import torch
-    if global_scale is not None:
-        _mx_scalar(global_scale, "global_scale", dev)
-    k = 1
-    if positions is not None:
-        k = positions.shape[1] if positions.dim() == 2 else 0
-        _mx_tensor(positions, "positions", torch.int32, (n, k), dev)
-    if out is None:
-        m = n * k if out_rows is None else out_rows
-        return k, m, mx_rows(fmt, m, d, device, global_scale)
-    if out.fmt != fmt or out.cols != d:
-        raise ValueError("out: of another format or width")
-    m = _mx_check_rows(out, dev)
-    out.global_scale = global_scale
-    return k, m, out
-
-
-@_on_stream
-def mx_quantise(x, fmt, positions=None, out_rows=None, global_scale=None, out: Optional[MxRows] = None) -> MxRows:
-    """bf16 rows x [n, d] (any row stride that is a multiple of 8) into a format; row t goes to each of positions[t]
-    (int32 [n, k], default its own place) of `out` (out_rows rows, default n * k)."""
-    n, d = x.shape
-    dev = x.get_device()
-    ld = _mx_strided(x, "x", (n, d), dev)
-    k, m, out = _mx_out(fmt, n, d, positions, out_rows, global_scale, out, x.device, dev)
-    moe_mx_quantise(fmt, n, k, d, x, ld, positions, global_scale, m, out.codes, out.scales)
-    return out
-
-
-@_on_stream
-def mx_add_rmsnorm(x, residual, gain, eps, fmt, positions=None, out_rows=None, global_scale=None, sum_out=None,
-                   out: Optional[MxRows] = None):
-    """(rows of the normalised sum, the sum): sum = bf16(x + residual) (residual may be None), rows = Q(rmsnorm(sum))
-    written as by mx_quantise.  sum_out may be x or residual."""
-    import torch
-    n, d = shape = x.shape
-    dev = x.get_device()
-    ld = _mx_strided(x, "x", shape, dev)
-    r_ld = None if residual is None else _mx_strided(residual, "residual", shape, dev)
-    _mx_tensor(gain, "gain", torch.bfloat16, (d,), dev)
-    if sum_out is None:
-        sum_out = torch.empty_strided(shape, (r_ld or d, 1), dtype=torch.bfloat16, device=x.device)
-        r_ld = r_ld or d
-    else:
-        s_ld = _mx_strided(sum_out, "sum_out", shape, dev)
-        if r_ld is not None and s_ld != r_ld and n > 1:
-            raise ValueError("sum_out: its row stride differs from residual's")
-        r_ld = r_ld or s_ld
-    k, m, out = _mx_out(fmt, n, d, positions, out_rows, global_scale, out, x.device, dev)
-    moe_mx_add_rmsnorm(fmt, n, k, d, x, ld, residual, r_ld, gain, eps, positions, global_scale, m, sum_out, out.codes,
-                       out.scales)
-    return out, sum_out
-
-
-@_on_stream
-def mx_dequantise(r: MxRows, out=None):
-    """bf16 values of rows."""
-    import torch
-    dev = r.codes.get_device()
-    n, d = _mx_check_rows(r, dev), r.cols
-    if out is None:
-        out, ld = torch.empty((n, d), dtype=torch.bfloat16, device=r.codes.device), d
-    else:
-        ld = _mx_strided(out, "out", (n, d), dev)
-    moe_mx_dequantise(r.fmt, n, d, r.codes, r.scales, r.global_scale, out, ld)
-    return out
-
-
-@_on_stream
-def mx_pack(rows: MxRows, num_experts, up: Optional[MxRows] = None, alpha=None, alpha_up=None) -> MxWeights:
-    """Packed weights from rows [num_experts * n_out] of a format (up: the SwiGLU pair's second matrix)."""
-    import torch
-    dev = rows.codes.get_device()
-    n = _mx_check_rows(rows, dev)
-    if num_experts < 1 or n % num_experts != 0:
-        raise ValueError("rows: not a multiple of num_experts")
-    if up is not None:
-        if (up.fmt, up.cols) != (rows.fmt, rows.cols) or _mx_check_rows(up, dev) != n:
-            raise ValueError("up: not like the first matrix")
-    w = MxWeights(rows.fmt, num_experts, n // num_experts, rows.cols, None, alpha, alpha_up, up is not None)
-    nbytes = moe_mx_packed_bytes(w.struct())
-    if nbytes == 0:
-        raise MoeError(2, "moe_mx_packed_bytes")
-    w.packed = torch.empty(nbytes, dtype=torch.uint8, device=rows.codes.device)
-    moe_mx_pack_weights(w.checked(dev), rows.codes, rows.scales, up.codes if up else None, up.scales if up else None,
-                        w.packed)
-    return w
-
-
-def _mx_operands(x: MxRows, w: MxWeights, offsets):
-    """(device, rows, the weights' struct) of checked operands."""
-    import torch
-    dev = x.codes.get_device()
-    n = _mx_check_rows(x, dev)
-    st = w.checked(dev)
-    if x.fmt != w.fmt or x.cols != w.k:
-        raise ValueError("x: of another format or width than the weights")
-    _mx_tensor(offsets, "offsets", torch.int32, (w.num_experts + 1,), dev)
-    return dev, n, st
-
-
-def mx_workspace(device="cuda"):
-    import torch
-    return torch.zeros(MOE_MX_PRODUCT_WORKSPACE, dtype=torch.uint8, device=device)
-
-
-@_on_stream
-def mx_grouped_product(x: MxRows, w: MxWeights, offsets, out=None, out_pos=None, row_weight=None, ws=None,
-                       out_type=MOE_MX_OUT_BF16):
-    """out[p(r)] = row_weight[p(r)] * x[r] W_e^T for the rows offsets[e] .. offsets[e + 1] - 1 of each expert e;
-    p = out_pos (int32 [rows], default r)."""
-    import torch
-    dev, n, st = _mx_operands(x, w, offsets)
-    dtype = torch.float16 if out_type == MOE_MX_OUT_F16 else torch.bfloat16
-    cols = w.n_out
-    if out is None:
-        out, out_rows, ld = torch.empty((n, cols), dtype=dtype, device=x.codes.device), n, cols
-    else:
-        if out.dtype != dtype or out.dim() != 2 or out.shape[1] != cols or out.get_device() != dev or (
-                cols > 1 and out.stride(1) != 1):
-            raise ValueError("out: of another type, width or device")
-        out_rows, ld = out.shape[0], max(out.stride(0), cols) if out.shape[0] < 2 else out.stride(0)
-    if out_pos is not None:
-        _mx_tensor(out_pos, "out_pos", torch.int32, (n,), dev)
-    if row_weight is not None:
-        _mx_scalar(row_weight, "row_weight", dev, out_rows)
-    if ws is None:
-        ws = mx_workspace(x.codes.device)
-    moe_mx_grouped_product(st, n, x.codes, x.scales, x.global_scale, offsets, out, out_type, out_rows, ld, out_pos,
-                           row_weight, ws)
-    return out
-
-
-@_on_stream
-def mx_grouped_swiglu(x: MxRows, w: MxWeights, offsets, h_global=None, out: Optional[MxRows] = None, ws=None) -> MxRows:
-    """Rows of silu(x Wg_e^T) * (x Wu_e^T) in the format of x."""
-    dev, n, st = _mx_operands(x, w, offsets)
-    _, m, out = _mx_out(w.fmt, n, w.n_out, None, None, h_global, out, x.codes.device, dev)
-    if m != n:
-        raise ValueError("out: of another number of rows")
-    if ws is None:
-        ws = mx_workspace(x.codes.device)
-    moe_mx_grouped_swiglu(st, n, x.codes, x.scales, x.global_scale, offsets, h_global, out.codes, out.scales, ws)
-    return out
-
-
-@_on_stream
-def mx_layer_forward(x, residual, gain, eps, topk_ids, topk_weight, gate_up: MxWeights, down: MxWeights,
-                     x_global=None, h_global=None, ws=None, out_is_fp32=False):
-    """The MoE block on microscaled experts: (sum, out) with sum = bf16(x + residual) and out = sum + the routed
-    experts on rmsnorm(sum); with gain None (and residual None) (None, the routed experts on x)."""
-    import torch
-    n, d = shape = x.shape
-    dev = x.get_device()
-    bf16 = torch.bfloat16
-    _mx_tensor(x, "x", bf16, shape, dev)
-    if d != gate_up.k:
-        raise ValueError("x: of another width than the experts")
-    if residual is not None:
-        _mx_tensor(residual, "residual", bf16, shape, dev)
-    if gain is not None:
-        _mx_tensor(gain, "gain", bf16, (d,), dev)
-    k = topk_ids.shape[1]
-    _mx_tensor(topk_ids, "topk_ids", torch.int32, (n, k), dev)
-    _mx_tensor(topk_weight, "topk_weight", torch.float32, (n, k), dev)
-    gs, ds = gate_up.checked(dev), down.checked(dev)
-    if x_global is not None:
-        _mx_scalar(x_global, "x_global", dev)
-    if h_global is not None:
-        _mx_scalar(h_global, "h_global", dev)
-    device = x.device
-    if ws is None:
-        nbytes = moe_mx_layer_workspace_size(gs, ds, k, n)
-        if nbytes == 0:
-            raise MoeError(2, "moe_mx_layer_workspace_size")
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    total = torch.empty(shape, dtype=bf16, device=device) if gain is not None else None
-    out = torch.empty(shape, dtype=torch.float32 if out_is_fp32 else bf16, device=device)
-    moe_mx_layer_forward(gs, ds, k, n, x, residual, gain, eps, topk_ids, topk_weight, x_global, h_global, total, out,
-                         ws, out_is_fp32)
-    return total, out
+def __getattr__(name):
+    if name not in _MX_NAMES:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import mx
+    for n in _MX_NAMES:
+        globals()[n] = getattr(mx, n)
+    return globals()[name]

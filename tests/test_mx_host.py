@@ -167,6 +167,18 @@ def test_binding_refusals(lib):
             call()
 
 
+def test_host_tensors_are_refused(lib):
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    r = mx.mx_rows(1, 4, 64, "cpu")
+    w = mx.MxWeights(1, 1, 64, 64, torch.zeros(mx.moe_mx_packed_bytes(W(1, 1, 64, 64)), dtype=torch.uint8))
+    ws = torch.zeros(512, dtype=torch.uint8)
+    for call in (lambda: mx.mx_quantise(x, 1), lambda: mx.mx_dequantise(r), lambda: mx.mx_pack(r, 1),
+                 lambda: mx.mx_add_rmsnorm(x, x, torch.ones(64, dtype=torch.bfloat16), 1e-6, 1),
+                 lambda: mx.mx_grouped_product(r, w, torch.zeros(2, dtype=torch.int32), ws=ws)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+
+
 def test_header_is_c99(tmp_path):
     src = tmp_path / "a.c"
     src.write_text('#include "moe_mx.h"\nint main(void) { moe_mx_weights w = {MOE_MX_NVFP4, 1, 256, 256, 0, 0, 0, 0};\n'
