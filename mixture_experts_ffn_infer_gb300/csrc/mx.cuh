@@ -80,14 +80,13 @@ __device__ __forceinline__ GroupFactor group_factor(const float* global) {
   return GroupFactor{g, 6.0f * g, __frcp_rn(6.0f * g)};
 }
 
-// abs_bits: the largest of the group's |v| as fp32 bits.  Bits of non-negative
-// floats order as the floats do, with infinity and then NaN above all, so one
-// integer maximum finds the magnitude and a non-finite value alike.
+// amax: the largest of the group's |v|, NaN where one is (abs_max).
 template <int FMT>
-__device__ __forceinline__ GroupScale group_scale(uint32_t abs_bits, const GroupFactor& f) {
+__device__ __forceinline__ GroupScale group_scale(float amax, const GroupFactor& f) {
+  const uint32_t abs_bits = __float_as_uint(amax);
   const bool bad = abs_bits >= 0x7f800000u;
   if constexpr (FMT == MOE_MX_NVFP4) {
-    const float t = quotient(__uint_as_float(abs_bits), f.six, f.inv, 1024.f);
+    const float t = quotient(amax, f.six, f.inv, 1024.f);
     const uint32_t byte = bad ? 0x7fu : __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
     const float div = e4m3_value(byte) * f.g;
     return GroupScale{byte, div, !bad && div > 0.f ? __frcp_rn(div) : 0.f};
@@ -107,33 +106,41 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Codes of eight consecutive columns: 1 word of e2m1 or 2 of e4m3.
-template <int FMT>
-__device__ __forceinline__ void codes8(const float* v, const GroupScale& s, uint32_t (&w)[2]) {
-  float t[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float q = FMT == MOE_MX_NVFP4 ? quotient(v[i], s.div, s.mul, 8.f) : v[i] * s.mul;
-    t[i] = s.mul == 0.f ? 0.f : q;  // a zero divisor, or a group that is not finite
-  }
+// Codes of N consecutive columns, all of one group, into N / 8 (e2m1) or N / 4 (e4m3) words.
+// mul: s.mul, or for the MX formats s.mul times any factor that v still lacks.
+template <int FMT, int N>
+__device__ __forceinline__ void codes_of(const float* v, const GroupScale& s, float mul, uint32_t* w) {
+  auto scaled = [&](int i) { return FMT == MOE_MX_NVFP4 ? quotient(v[i], s.div, mul, 8.f) : v[i] * mul; };
+  const bool none = s.mul == 0.f;  // a zero divisor, or a group that is not finite
   if constexpr (FMT == MOE_MX_MXFP8) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * i], t[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * i + 2], t[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
-      w[i] = lo | (hi << 16);
+    for (int i = 0; i < N / 4; ++i) {
+      const uint32_t lo =
+          __nv_cvt_float2_to_fp8x2(make_float2(scaled(4 * i), scaled(4 * i + 1)), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi =
+          __nv_cvt_float2_to_fp8x2(make_float2(scaled(4 * i + 2), scaled(4 * i + 3)), __NV_SATFINITE, __NV_E4M3);
+      w[i] = none ? 0u : lo | (hi << 16);
     }
   } else {
-    w[0] = w[1] = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[0] |= static_cast<uint32_t>(
-                  __nv_cvt_float2_to_fp4x2(make_float2(t[2 * i], t[2 * i + 1]), __NV_E2M1, cudaRoundNearest))
-              << (8 * i);
+    for (int i = 0; i < N / 8; ++i) {
+      uint32_t word = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        word |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(
+                    make_float2(scaled(8 * i + 2 * j), scaled(8 * i + 2 * j + 1)), __NV_E2M1, cudaRoundNearest))
+                << (8 * j);
+      w[i] = none ? 0u : word;
+    }
   }
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// The larger magnitude, NaN if either is: as bits it is above every finite value's.
+__device__ __forceinline__ float abs_max(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
+}
 
 // ---------------------------------------------------------------- launchers
 struct MxRowsLaunch {
@@ -151,6 +158,7 @@ struct MxRowsLaunch {
   uint16_t* sum;
   uint8_t* codes;
   uint8_t* scales;
+  int32_t wide_x, wide_r, wide_gain, wide_out;  // set by the launcher: rows on 32-byte boundaries
 };
 cudaError_t launch_mx_rows(int32_t fmt, const MxRowsLaunch& a, cudaStream_t s);
 cudaError_t launch_mx_dequantise(int32_t fmt, int64_t rows, int32_t d, const uint8_t* codes, const uint8_t* scales,

@@ -547,22 +547,12 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
               uint32_t sbytes = 0;
 #pragma unroll
               for (int g = 0; g < 32 / G; ++g) {
-                uint32_t m = 0;
+                float m = 0.f;
 #pragma unroll
-                for (int i = 0; i < G; ++i) m = max(m, abs_bits(h[G * g + i]));
+                for (int i = 0; i < G; ++i) m = abs_max(m, h[G * g + i]);
                 const GroupScale sc = group_scale<FMT>(m, hf_factor);
                 sbytes |= sc.byte << (8 * g);
-#pragma unroll
-                for (int v = 0; v < G / 8; ++v) {
-                  uint32_t w[2];
-                  codes8<FMT>(h + G * g + 8 * v, sc, w);
-                  if constexpr (FMT == MOE_MX_MXFP8) {
-                    out[2 * v] = w[0];
-                    out[2 * v + 1] = w[1];
-                  } else {
-                    out[(G / 8) * g + v] = w[0];
-                  }
-                }
+                codes_of<FMT, G>(h + G * g, sc, sc.mul, out + (FMT == MOE_MX_MXFP8 ? 8 : G / 8) * g);
               }
               if constexpr (FMT == MOE_MX_MXFP8) {
                 *reinterpret_cast<uint4*>(hc + at) = make_uint4(out[0], out[1], out[2], out[3]);

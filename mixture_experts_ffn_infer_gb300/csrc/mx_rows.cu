@@ -5,24 +5,48 @@
 //
 // mx_rows_kernel       - [add the residual, RMS norm,] quantise, write to each
 //                        position of the token.  One CTA per token; a thread
-//                        holds eight consecutive columns in registers (one
-//                        16-byte load) from the first read to the codes, so x
-//                        is read once.  A group is two (16 columns) or four (32)
-//                        neighbouring lanes: its maximum takes one or two
-//                        shuffles.
-// mx_dequantise_kernel - codes and scales to bf16, eight columns a thread.
+//                        holds 16 consecutive columns at a time (32 bytes) in
+//                        registers from the first read to the codes, so x is
+//                        read once, and a group is the thread's own columns
+//                        (16) or its and its neighbour's (32).  With eight
+//                        columns and fp32 sums the kernel took 37
+//                        instructions a column and the issue slots bounded it
+//                        (67 % busy, DRAM 58 %).
+// mx_dequantise_kernel - codes and scales to bf16, 16 columns at a time.
 // mx_pack_kernel       - one CTA per packed block.
 #include "mx.cuh"
 
 namespace moe {
 namespace {
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+constexpr int kPiece = 16;  // columns a thread holds together
+
+__device__ __forceinline__ void unpack(const uint32_t (&w)[8], float (&v)[16]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(u[i] << 16);
-    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// 16 bf16: one 32-byte access where rows are aligned for it, else two of 16.
+__device__ __forceinline__ void load_piece(const uint16_t* p, bool wide, uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store_piece(void* p, bool wide, const uint32_t (&w)[8]) {
+  if (wide) {
+    stg256(p, w);
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
@@ -39,52 +63,71 @@ __device__ __forceinline__ int64_t scale_pitch(int d) {
 constexpr int kRowsMaxThreads = 1024;
 constexpr int kRowsSplitThreads = 256;
 
-// ITER passes of blockDim.x * 8 columns cover the row, held as the bf16 pairs they
-// are read as (the stored sum is bf16 too).  The sum of squares is taken per thread
-// in column order, then by shuffles, then over the warps.
+// One piece's codes (and its group's scale) to row `pos`.
+template <int FMT>
+__device__ __forceinline__ void store_codes(const MxRowsLaunch& a, int64_t pos, int c, const uint32_t (&w)[8],
+                                            uint32_t scale) {
+  if (pos < 0 || pos >= a.out_rows) return;
+  uint8_t* row = a.codes + pos * code_pitch<FMT>(a.d);
+  if constexpr (FMT == MOE_MX_BF16) {
+    store_piece(row + 32 * c, a.wide_out != 0, w);
+  } else {
+    if constexpr (FMT == MOE_MX_MXFP8) reinterpret_cast<uint4*>(row)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+    else reinterpret_cast<uint2*>(row)[c] = make_uint2(w[0], w[1]);
+    constexpr int kLanes = Mx<FMT>::group / kPiece;
+    if (c % kLanes == 0) a.scales[pos * scale_pitch<FMT>(a.d) + c / kLanes] = static_cast<uint8_t>(scale);
+  }
+}
+
+// ITER passes of blockDim.x pieces cover the row, held as the bf16 pairs they are
+// read as (the stored sum is bf16 too).  The sum of squares is taken per thread in
+// column order, then by shuffles, then over the warps.
 template <int FMT, bool NORM, int ITER>
-__global__ void __launch_bounds__(ITER <= 2 ? kRowsMaxThreads : kRowsSplitThreads)
+__global__ void __launch_bounds__(ITER == 1 ? kRowsMaxThreads : kRowsSplitThreads)
 mx_rows_kernel(const MxRowsLaunch a) {
   __shared__ float part[32];
   pdl_launch_dependents();
   pdl_wait();
   const int64_t t = blockIdx.x;
-  const int d = a.d, nc = d / 8;
-  uint4 raw[ITER];
+  const int d = a.d, np = d / kPiece;
+  uint32_t raw[ITER][8];
 #pragma unroll
   for (int it = 0; it < ITER; ++it) {
     const int c = it * blockDim.x + threadIdx.x;
-    raw[it] = make_uint4(0u, 0u, 0u, 0u);
-    if (c < nc) raw[it] = *(reinterpret_cast<const uint4*>(a.x + t * a.x_ld) + c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) raw[it][i] = 0u;
+    if (c < np) load_piece(a.x + t * a.x_ld + kPiece * c, a.wide_x != 0, raw[it]);
   }
   float rs = 1.f;
   if constexpr (NORM) {
     float ss = 0.f;
     if (a.residual) {
-      uint4 res[ITER];
+      uint32_t res[ITER][8];
 #pragma unroll
       for (int it = 0; it < ITER; ++it) {
         const int c = it * blockDim.x + threadIdx.x;
-        res[it] = make_uint4(0u, 0u, 0u, 0u);
-        if (c < nc) res[it] = *(reinterpret_cast<const uint4*>(a.residual + t * a.r_ld) + c);
-      }
 #pragma unroll
-      for (int it = 0; it < ITER; ++it) {
-        float v[8], r[8];
-        unpack8(raw[it], v);
-        unpack8(res[it], r);
-        raw[it] = make_uint4(pack_bf16(v[0] + r[0], v[1] + r[1]), pack_bf16(v[2] + r[2], v[3] + r[3]),
-                             pack_bf16(v[4] + r[4], v[5] + r[5]), pack_bf16(v[6] + r[6], v[7] + r[7]));
+        for (int i = 0; i < 8; ++i) res[it][i] = 0u;
+        if (c < np) load_piece(a.residual + t * a.r_ld + kPiece * c, a.wide_r != 0, res[it]);
       }
+      // bf16 + bf16 rounded once to bf16, which is what is stored and what is normalised
+#pragma unroll
+      for (int it = 0; it < ITER; ++it)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const __nv_bfloat162 sum = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&raw[it][i]),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&res[it][i]));
+          raw[it][i] = *reinterpret_cast<const uint32_t*>(&sum);
+        }
     }
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
       const int c = it * blockDim.x + threadIdx.x;
-      if (a.sum && c < nc) *(reinterpret_cast<uint4*>(a.sum + t * a.r_ld) + c) = raw[it];
-      float v[8];
-      unpack8(raw[it], v);
+      if (a.sum && c < np) store_piece(a.sum + t * a.r_ld + kPiece * c, a.wide_r != 0, raw[it]);
+      float v[16];
+      unpack(raw[it], v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+      for (int i = 0; i < 16; ++i) ss = fmaf(v[i], v[i], ss);
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
 #pragma unroll
@@ -102,139 +145,147 @@ mx_rows_kernel(const MxRowsLaunch a) {
 #pragma unroll
   for (int it = 0; it < ITER; ++it) {
     const int c = it * blockDim.x + threadIdx.x;
-    float v[8];
-    unpack8(raw[it], v);
+    float v[16];
+    unpack(raw[it], v);
     if constexpr (NORM) {
-      if (c < nc) {
-        float g[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(a.gain) + c), g);
+      // sum * gain is exact in fp32 (8 bits by 8), so y = (sum * gain) * rs has one rounding
+      if (c < np) {
+        uint32_t gw[8];
+        load_piece(a.gain + kPiece * c, a.wide_gain != 0, gw);
+        float g[16];
+        unpack(gw, g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * rs * g[i];
+        for (int i = 0; i < 16; ++i) v[i] *= g[i];
       }
+      if constexpr (FMT == MOE_MX_BF16 || FMT == MOE_MX_NVFP4)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] *= rs;
     }
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    GroupScale sc{};
+    uint32_t w[8];
+    uint32_t scale = 0;
     if constexpr (FMT == MOE_MX_BF16) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+      for (int i = 0; i < 8; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     } else {
-      uint32_t m = 0;
+      float m = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      if constexpr (Mx<FMT>::group == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      sc = group_scale<FMT>(m, factor);
-      uint32_t cw[2];
-      codes8<FMT>(v, sc, cw);
-      w[0] = cw[0];
-      w[1] = cw[1];
+      for (int i = 0; i < 16; ++i) m = abs_max(m, v[i]);
+      if constexpr (Mx<FMT>::group == 32) m = abs_max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      // MX: rounding is monotone and the divisor a power of two, so the largest y is the
+      // largest product times rs, and y / 2^k = product * (rs 2^-k) to the bit
+      const bool late = NORM && FMT != MOE_MX_NVFP4;
+      const GroupScale sc = group_scale<FMT>(late ? m * rs : m, factor);
+      float mul = late ? rs * sc.mul : sc.mul;
+      if (late && !(mul < 3e38f)) {  // a group near zero: 2^126 times rs is past fp32
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] *= rs;
+        mul = sc.mul;
+      }
+      codes_of<FMT, 16>(v, sc, mul, w);
+      scale = sc.byte;
     }
-    if (c >= nc) continue;
-    for (int j0 = 0; j0 < a.k; j0 += 8) {
-      int32_t at[8];
+    if (c >= np) continue;
+    if (a.k == 1) {
+      store_codes<FMT>(a, a.positions ? __ldg(a.positions + t) : t, c, w, scale);
+    } else {
+      for (int j0 = 0; j0 < a.k; j0 += 4) {
+        int32_t at[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        at[j] = j0 + j >= a.k ? -1 : a.positions ? __ldg(a.positions + t * a.k + j0 + j) : static_cast<int32_t>(t);
+        for (int j = 0; j < 4; ++j) at[j] = j0 + j < a.k ? __ldg(a.positions + t * a.k + j0 + j) : -1;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (at[j] < 0 || at[j] >= a.out_rows) continue;
-        uint8_t* row = a.codes + at[j] * code_pitch<FMT>(d);
-        if constexpr (FMT == MOE_MX_BF16) {
-          reinterpret_cast<uint4*>(row)[c] = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-          if constexpr (FMT == MOE_MX_MXFP8) reinterpret_cast<uint2*>(row)[c] = make_uint2(w[0], w[1]);
-          else reinterpret_cast<uint32_t*>(row)[c] = w[0];
-          constexpr int kLanes = Mx<FMT>::group / 8;
-          if (c % kLanes == 0) a.scales[at[j] * scale_pitch<FMT>(d) + c / kLanes] = static_cast<uint8_t>(sc.byte);
-        }
+        for (int j = 0; j < 4; ++j) store_codes<FMT>(a, at[j], c, w, scale);
       }
     }
   }
 }
 
+bool aligned32(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 32 == 0 && ld % 16 == 0; }
+
 template <int FMT, bool NORM>
-cudaError_t launch_rows(const MxRowsLaunch& a, cudaStream_t s) {
-  const int nc = a.d / 8;
+cudaError_t launch_rows(MxRowsLaunch a, cudaStream_t s) {
+  const int np = a.d / kPiece;
   // Few rows: as many threads as the row has pieces, for the shortest way through one row.  More rows
   // than SMs: 256 threads with several pieces each, so that an SM holds more rows in different phases.
   const int most = a.n > 2 * device_sms() ? kRowsSplitThreads : kRowsMaxThreads;
   int iters = 1;
-  while (iters * most < nc) iters *= 2;
-  const int threads = ((nc + iters - 1) / iters + 31) / 32 * 32;
+  while (iters * most < np) iters *= 2;
+  const int threads = ((np + iters - 1) / iters + 31) / 32 * 32;
+  a.wide_x = aligned32(a.x, a.x_ld);
+  a.wide_r = aligned32(a.residual, a.r_ld) && aligned32(a.sum, a.r_ld);
+  a.wide_gain = aligned32(a.gain, 0);
+  a.wide_out = aligned32(a.codes, 0);
   auto kern = iters == 1   ? mx_rows_kernel<FMT, NORM, 1>
               : iters == 2 ? mx_rows_kernel<FMT, NORM, 2>
-              : iters == 4 ? mx_rows_kernel<FMT, NORM, 4>
-                           : mx_rows_kernel<FMT, NORM, 8>;
+                           : mx_rows_kernel<FMT, NORM, 4>;
   return launch_maybe_overlapped(kern, static_cast<int>(a.n), threads, 0, s, true, a);
 }
 
-// A CTA covers 1024 pieces of eight columns, of as many rows as fit or of one row's
-// part, four pieces a thread: their loads are all under way before the first is used.
+// A CTA covers 1024 pieces, of as many rows as fit or of one row's part, four a
+// thread: their loads are all under way before the first is used.
 constexpr int kDeqPieces = 1024;
 
+// magic: ceil(2^32 / np) for rows of np < 1024 pieces (i / np = umulhi(i, magic) for i < 1024).
 template <int FMT>
 __global__ void __launch_bounds__(256)
 mx_dequantise_kernel(int64_t rows, int32_t d, const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                     const float* __restrict__ global_p, uint16_t* __restrict__ out, int64_t out_ld) {
+                     const float* __restrict__ global_p, uint16_t* __restrict__ out, int64_t out_ld, uint32_t magic,
+                     int32_t segs, int32_t rpb, int32_t wide) {
   pdl_launch_dependents();
   pdl_wait();
-  const int nc = d / 8;
-  const int segs = (nc + kDeqPieces - 1) / kDeqPieces, rpb = nc < kDeqPieces ? kDeqPieces / nc : 1;
+  const int np = d / kPiece;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / segs) * rpb;
   const int c0 = static_cast<int>(blockIdx.x % segs) * kDeqPieces;
   const float global = FMT == MOE_MX_NVFP4 && global_p ? __ldg(global_p) : 1.f;
-  int64_t r[4];
-  int c[4];
-  uint4 w[4];
+  constexpr int kWords = FMT == MOE_MX_BF16 ? 8 : FMT == MOE_MX_MXFP8 ? 4 : 2;
+  int r[4], c[4];
+  uint32_t w[4][kWords];
   uint32_t sb[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int i = 256 * u + threadIdx.x;
-    const int rl = nc < kDeqPieces ? i / nc : 0;
-    c[u] = nc < kDeqPieces ? i - rl * nc : c0 + i;
-    r[u] = rl < rpb && c[u] < nc && row0 + rl < rows ? row0 + rl : -1;
+    const int rl = np < kDeqPieces ? static_cast<int>(__umulhi(i, magic)) : 0;
+    c[u] = np < kDeqPieces ? i - rl * np : c0 + i;
+    r[u] = rl < rpb && c[u] < np && row0 + rl < rows ? rl : -1;
     if (r[u] >= 0) {
-      const uint8_t* row = codes + r[u] * code_pitch<FMT>(d);
+      const uint8_t* row = codes + (row0 + rl) * code_pitch<FMT>(d);
       if constexpr (FMT == MOE_MX_BF16) {
-        w[u] = __ldg(reinterpret_cast<const uint4*>(row) + c[u]);
+        load_piece(reinterpret_cast<const uint16_t*>(row) + kPiece * c[u], false, w[u]);
+      } else if constexpr (FMT == MOE_MX_MXFP8) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(row) + c[u]);
+        w[u][0] = q.x, w[u][1] = q.y, w[u][2] = q.z, w[u][3] = q.w;
       } else {
-        if constexpr (FMT == MOE_MX_MXFP8) {
-          const uint2 q = __ldg(reinterpret_cast<const uint2*>(row) + c[u]);
-          w[u].x = q.x;
-          w[u].y = q.y;
-        } else {
-          w[u].x = __ldg(reinterpret_cast<const uint32_t*>(row) + c[u]);
-        }
-        sb[u] = __ldg(scales + r[u] * scale_pitch<FMT>(d) + c[u] / (Mx<FMT>::group / 8));
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(row) + c[u]);
+        w[u][0] = q.x, w[u][1] = q.y;
       }
+      if constexpr (FMT != MOE_MX_BF16)
+        sb[u] = __ldg(scales + (row0 + rl) * scale_pitch<FMT>(d) + c[u] / (Mx<FMT>::group / kPiece));
     }
   }
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     if (r[u] < 0) continue;
-    uint4 o = w[u];
-    if constexpr (FMT != MOE_MX_BF16) {
+    uint32_t o[8];
+    if constexpr (FMT == MOE_MX_BF16) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = w[u][i];
+    } else {
       float sc;
       if constexpr (FMT == MOE_MX_NVFP4) sc = e4m3_value(sb[u]) * global;
       else if (sb[u] == 255u) sc = __uint_as_float(0x7fc00000u);
       else sc = sb[u] == 0u ? 0x1p-127f : __uint_as_float(sb[u] << 23);
-      float v[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 8; ++j) {
         __half2 h;
-        if constexpr (FMT == MOE_MX_MXFP8) {
-          const uint32_t pair = ((j < 2 ? w[u].x : w[u].y) >> (16 * (j & 1))) & 0xffffu;
-          h = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair), __NV_E4M3));
-        } else {
-          h = __half2(__nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>((w[u].x >> (8 * j)) & 0xffu),
-                                                 __NV_E2M1));
-        }
-        v[2 * j] = __low2float(h) * sc;
-        v[2 * j + 1] = __high2float(h) * sc;
+        if constexpr (FMT == MOE_MX_MXFP8)
+          h = __half2(__nv_cvt_fp8x2_to_halfraw2(
+              static_cast<__nv_fp8x2_storage_t>((w[u][j >> 1] >> (16 * (j & 1))) & 0xffffu), __NV_E4M3));
+        else
+          h = __half2(__nv_cvt_fp4x2_to_halfraw2(
+              static_cast<__nv_fp4x2_storage_t>((w[u][j >> 2] >> (8 * (j & 3))) & 0xffu), __NV_E2M1));
+        o[j] = pack_bf16(__low2float(h) * sc, __high2float(h) * sc);
       }
-      o = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     }
-    *(reinterpret_cast<uint4*>(out + r[u] * out_ld) + c[u]) = o;
+    store_piece(out + (row0 + r[u]) * out_ld + kPiece * c[u], wide != 0, o);
   }
 }
 
@@ -295,8 +346,9 @@ cudaError_t launch_mx_rows(int32_t fmt, const MxRowsLaunch& a, cudaStream_t s) {
 
 cudaError_t launch_mx_dequantise(int32_t fmt, int64_t rows, int32_t d, const uint8_t* codes, const uint8_t* scales,
                                  const float* global, uint16_t* out, int64_t out_ld, cudaStream_t s) {
-  const int nc = d / 8;
-  const int64_t segs = (nc + kDeqPieces - 1) / kDeqPieces, rpb = nc < kDeqPieces ? kDeqPieces / nc : 1;
+  const int np = d / kPiece;
+  const int segs = (np + kDeqPieces - 1) / kDeqPieces, rpb = np < kDeqPieces ? kDeqPieces / np : 1;
+  const uint32_t magic = np > 1 ? static_cast<uint32_t>(((1ull << 32) + np - 1) / np) : 0u;
   const int64_t blocks = (rows + rpb - 1) / rpb * segs;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   auto kern = fmt == MOE_MX_BF16    ? mx_dequantise_kernel<MOE_MX_BF16>
@@ -304,7 +356,7 @@ cudaError_t launch_mx_dequantise(int32_t fmt, int64_t rows, int32_t d, const uin
               : fmt == MOE_MX_MXFP4 ? mx_dequantise_kernel<MOE_MX_MXFP4>
                                     : mx_dequantise_kernel<MOE_MX_NVFP4>;
   return launch_maybe_overlapped(kern, static_cast<int>(blocks), 256, 0, s, true, rows, d, codes, scales, global, out,
-                                 out_ld);
+                                 out_ld, magic, segs, rpb, static_cast<int>(aligned32(out, out_ld)));
 }
 
 cudaError_t launch_mx_pack(const moe_mx_weights* w, const uint8_t* codes, const uint8_t* scales,

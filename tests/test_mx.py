@@ -189,6 +189,19 @@ def test_add_rmsnorm_zero_and_non_finite_rows():
     assert (v[1, 32:] == 0).all()
 
 
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4", "nvfp4"])
+def test_add_rmsnorm_groups_near_zero(fmt):
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    x[0, 64:] = bf16(gen(1), 192)               # zero groups beside others
+    x[1] = 1e-30 * bf16(gen(2), 256)            # rs = 1000: all of it eps
+    x[2, :32] = 2e-39                            # subnormal
+    x[3, 5] = 1e-38
+    x[3, 200] = -3.0
+    rows, _ = mx.mx_add_rmsnorm(x.cuda(), None, torch.ones(256, dtype=torch.bfloat16).cuda(), 1e-6, mx.MX_FORMATS[fmt])
+    v = x.double()
+    check_codes(rows, v / torch.sqrt((v * v).mean(1, keepdim=True) + 1e-6), fmt, rel=40 * 2.0**-24, absolute=1e-44)
+
+
 # ---------------------------------------------------------------- packed weights
 
 @pytest.mark.parametrize("fmt", plain.FORMATS)
