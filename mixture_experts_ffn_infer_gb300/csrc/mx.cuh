@@ -188,6 +188,7 @@ struct MxProductLaunch {
   // the offsets and weights were complete before the kernel in front began: they are read, and
   // weights streamed, while that one still runs
   bool early;
+  const moe_mx_weights* next;  // swiglu: the product that follows on the same rows, or null
 };
 cudaError_t launch_mx_product(const MxProductLaunch& a, cudaStream_t s);
 

@@ -323,6 +323,7 @@ moe_status moe_mx_layer_forward(const moe_mx_weights* gu, const moe_mx_weights* 
   g.h_scales = ws_at<uint8_t>(ws, L.h_scales);
   g.err = err;
   g.num_sms = device_sms();
+  g.next = dn;
   g.early = true;  // the routing plan was complete before the rows' kernel began
   if (g.num_sms <= 0 || launch_mx_product(g, s) != cudaSuccess) return MOE_ERR_CUDA;
 

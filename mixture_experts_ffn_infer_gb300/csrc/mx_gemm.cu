@@ -13,11 +13,13 @@
 //    half of what its bytes take from HBM.
 //  * A chunk is 128 bytes of codes along K: one bulk copy brings the packed weight
 //    block with its scales (33 to 36 KB), one TMA box the tile's rows.  Four stages.
-//  * Weight scales go from shared to tensor memory by tcgen05.cp (the packed order is
-//    the one it wants).  Row scales start at any row, so no copy shape fits them:
-//    warps 4-7 read them from global memory, each for its own 32-lane quarter (the
-//    tensor core wants them in all four), and store them with tcgen05.st, four chunks
-//    in flight.  Each stage has its own scale columns, so a stage's barrier covers them.
+//  * Scales go from shared to tensor memory by tcgen05.cp.  The packed weights hold
+//    theirs in the order it wants; a tile's row scales start at any row, so warps 4-7
+//    read them from global memory, 32 rows each and four chunks ahead, and lay them out
+//    in the stage.  (With each warp storing all 128 rows to its own quarter of tensor
+//    memory the same loads ran four times, and bounded a dense product: NVFP4 8192 x
+//    7168 x 7168 203 us against 164 us without them.)  Each stage has its own scale
+//    columns, so a stage's barriers cover them.
 //  * One accumulator of 256 columns beside the scales (bf16: two, no scales).  The
 //    epilogue empties it into registers, 128 columns a thread, and releases it before
 //    it computes, so the next unit's products wait for the read alone.
@@ -44,8 +46,8 @@ constexpr int kChunkTiles = 8;
 constexpr int kABytes = kTile * 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kWarpWeights = 0, kWarpIssue = 1, kWarpRows = 2, kWarpScales = 4, kWarpEpi = 8;
-constexpr int kRegsLow = 56, kRegsScales = 104, kRegsEpi = 176;
-static_assert(128 * (kRegsLow + kRegsScales + 2 * kRegsEpi) <= 65536, "register split");
+constexpr int kRegsLow = 56, kRegsEpi = 200;
+static_assert(256 * (kRegsLow + kRegsEpi) <= 65536, "register split");
 
 constexpr int kOutBf16 = 0, kOutF16 = 1, kOutSwiglu = 2;
 
@@ -53,14 +55,16 @@ template <int FMT>
 struct Cfg {
   static constexpr int kWords = Mx<FMT>::words;
   static constexpr int kWBytes = kMxCodeBlock + 1024 * kWords;
-  static constexpr int kStage = kWBytes + kABytes;
+  static constexpr int kSBytes = (512 * kWords + 1023) / 1024 * 1024;  // row scales, after the rows
+  static constexpr int kStage = kWBytes + kABytes + kSBytes;
   static constexpr int kAcc = FMT == MOE_MX_BF16 ? 2 : 1;
   static constexpr uint32_t kScaleCols = 12 * kWords;  // 4 words columns of row scales, 8 of weight scales
   static constexpr int kNumBars = 2 * kStages + 2 * kAcc + 1;
   static constexpr int kBarOff = kStages * kStage;
-  static constexpr int kPlanOff = kBarOff + kNumBars * 8 + 16;  // tile prefix, row starts
-  static constexpr int kTurnOff = (kPlanOff + 2 * (kMaxExperts + 1) * 4 + 64 * 4 + 15) / 16 * 16;  // 1 KB an epilogue warp
-  static constexpr int kSmem = 1024 + kTurnOff + 8 * 1024;
+  static constexpr int kPlanOff = kBarOff + kNumBars * 8 + 16;  // tile prefix, warp sums
+  static constexpr int kTurnOff = (kPlanOff + (kMaxExperts + 1) * 4 + 32 * 4 + 15) / 16 * 16;
+  static constexpr int kTurn = 512;  // an epilogue warp's
+  static constexpr int kSmem = 1024 + kTurnOff + 8 * kTurn;
   static_assert(kStage % 1024 == 0, "operand tiles stay 1024-byte aligned");
   static_assert(kSmem <= 232448, "shared memory per CTA");
   static_assert(256 * kAcc + kStages * kScaleCols <= kTmemCols, "tensor memory");
@@ -87,6 +91,8 @@ struct Args {
   int64_t h_row_bytes, h_pitch;
   uint32_t* err;
   int32_t early;
+  const uint8_t* next_packed;  // the product that follows on the same rows (may be null)
+  int32_t next_upt, next_chunks, next_units;  // its units that run first
 };
 
 // Rows' maps with boxes of 16, 32, 64 and 128 rows: a tile's copy brings its own
@@ -175,21 +181,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
-template <int COLS>
-__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[COLS]) {
-  if constexpr (COLS == 16) {
-    tmem_st16(taddr, r);
-  } else if constexpr (COLS == 8) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-  } else {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3])
-                 : "memory");
-  }
-}
-
 __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity))
@@ -206,7 +197,7 @@ struct Unit {
 // Unit number x.  Expert e's units are consecutive, T tiles x upt block rows: its
 // tiles in chunks of eight, block row after block row within a chunk, tile after
 // tile within a block row.
-__device__ __forceinline__ Unit unit_of(const int32_t* first_tile, const int32_t* row_at, int experts, int upt, int x) {
+__device__ __forceinline__ Unit unit_of(const int32_t* first_tile, const int32_t* offsets, int experts, int upt, int x) {
   const int t = x / upt;
   int lo = 0, hi = experts;  // first_tile[lo] <= t < first_tile[hi]
   while (hi - lo > 1) {
@@ -221,8 +212,8 @@ __device__ __forceinline__ Unit unit_of(const int32_t* first_tile, const int32_t
   Unit un;
   un.e = lo;
   un.u = in / nc;
-  un.row0 = row_at[lo] + tile * kTile;
-  un.nv = min(kTile, row_at[lo + 1] - un.row0);
+  un.row0 = __ldg(offsets + lo) + tile * kTile;
+  un.nv = min(kTile, __ldg(offsets + lo + 1) - un.row0);
   return un;
 }
 
@@ -242,8 +233,7 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + C::kNumBars * 8);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   int32_t* first_tile = reinterpret_cast<int32_t*>(smem + C::kPlanOff);
-  int32_t* row_at = first_tile + kMaxExperts + 1;
-  int32_t* warp_sum = row_at + kMaxExperts + 1;
+  int32_t* warp_sum = first_tile + kMaxExperts + 1;
 
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -277,8 +267,6 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
         const int lo = __ldg(a.offsets + e), hi = __ldg(a.offsets + e + 1);
         bad |= lo < 0 || hi < lo || hi > a.rows;
         n[j] = bad ? 0 : (hi - lo + kTile - 1) / kTile;
-        row_at[e] = lo;
-        if (e == a.experts - 1) row_at[e + 1] = hi;
       }
     }
     const int mine = n[0] + n[1];
@@ -290,8 +278,7 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
     }
     if (lane == 31) warp_sum[warp] = incl;
     bad = __syncthreads_or(bad);
-    int base = 0;
-    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    const int base = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0);
     const int excl = base + incl - mine;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -310,7 +297,7 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
   const int upt = a.upt, chunks = a.chunks;
   const int total = first_tile[a.experts] * upt;
   const int stride = gridDim.x;
-  auto unit_at = [&](int x) { return unit_of(first_tile, row_at, a.experts, upt, x); };
+  auto unit_at = [&](int x) { return unit_of(first_tile, a.offsets, a.experts, upt, x); };
 
   if (warp < kWarpScales) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
@@ -334,6 +321,17 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
         }
         if (!ok)
           for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) wait_drain(full(i % kStages), (i / kStages) & 1);
+        // HBM would idle from this CTA's last copy to the next product's first: bring that one's first
+        // blocks into L2 (152 units' first six blocks, 33 MB at most).
+        if (OUT == kOutSwiglu && ok && a.next_packed) {
+          const int next_total = min(first_tile[a.experts] * a.next_upt, a.next_units);
+          for (int x = blockIdx.x; x < next_total; x += stride) {
+            const Unit un = unit_of(first_tile, a.offsets, a.experts, a.next_upt, x);
+            const uint8_t* src = a.next_packed + (static_cast<int64_t>(un.e) * a.next_upt + un.u) * a.next_chunks * C::kWBytes;
+            for (int c = 0; c < min(a.next_chunks, 6); ++c)
+              bulk_prefetch_l2(src + static_cast<int64_t>(c) * C::kWBytes, C::kWBytes);
+          }
+        }
       }
       __syncwarp();
     } else if (warp == kWarpRows) {
@@ -378,9 +376,11 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
             const uint32_t w = sbase + s * C::kStage;
             const uint32_t sa = tmem + 256u * C::kAcc + s * C::kScaleCols, sb = sa + 4u * C::kWords;
             if constexpr (FMT != MOE_MX_BF16) {
-              const uint64_t sd = desc_scales(w + kMxCodeBlock);
+              const uint64_t wd = desc_scales(w + kMxCodeBlock), rd = desc_scales(w + C::kWBytes + kABytes);
 #pragma unroll
-              for (int i = 0; i < 2 * C::kWords; ++i) tmem_copy_scales(sb + 4 * i, desc_advance(sd, 512 * i));
+              for (int i = 0; i < 2 * C::kWords; ++i) tmem_copy_scales(sb + 4 * i, desc_advance(wd, 512 * i));
+#pragma unroll
+              for (int i = 0; i < C::kWords; ++i) tmem_copy_scales(sa + 4 * i, desc_advance(rd, 512 * i));
             }
             const uint64_t ad = desc_kmajor_sw128(w + C::kWBytes), bd = desc_kmajor_sw128(w);
 #pragma unroll
@@ -396,51 +396,43 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
       __syncwarp();
     }
   } else if (warp < kWarpEpi) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsScales));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
     if constexpr (FMT != MOE_MX_BF16) {
       pdl_wait();
       constexpr int W = C::kWords;
-      const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t cols = tmem + quarter + 256u * C::kAcc;
+      const int row = 32 * (warp & 3) + lane;  // this thread's row of the tile
+      // word i of row r at 512 i + 16 (r % 32) + 4 (r / 32), as in the packed weights
+      const uint32_t at = sbase + C::kWBytes + kABytes + 16 * lane + 4 * (warp & 3);
       // what is loaded runs four chunks ahead of what is stored
       int lx = blockIdx.x, lc = 0;
-      Unit un{};
-      uint32_t buf[4][4 * W];
-      auto load = [&](uint32_t (&r)[4 * W]) {
+      const uint8_t* src = nullptr;
+      uint32_t buf[kStages][W];
+      auto load = [&](uint32_t (&w)[W]) {
         if (lx >= total) return;
-        if (lc == 0) un = unit_at(lx);
-        const int left = a.groups - lc * 4 * W;  // scales of this chunk that exist
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t w[W];
-#pragma unroll
-          for (int i = 0; i < W; ++i) w[i] = 0;
-          if (32 * b + lane < un.nv) {
-            const uint8_t* p = a.x_scales + (static_cast<int64_t>(un.row0) + 32 * b + lane) * a.x_pitch + lc * 4 * W;
-            if constexpr (W == 4) {
-              const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
-              w[0] = q.x;
-              w[1] = q.y;
-              w[2] = q.z;
-              w[3] = q.w;
-            } else if constexpr (W == 2) {
-              const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
-              w[0] = q.x;
-              w[1] = q.y;
-            } else {
-              w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < W; ++i) r[4 * i + b] = w[i];
+        if (lc == 0) {
+          const Unit un = unit_at(lx);
+          src = row < un.nv ? a.x_scales + (static_cast<int64_t>(un.row0) + row) * a.x_pitch : nullptr;
         }
-        if (left < 4 * W) {  // the row's last chunk: bytes past its scales are padding
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+        if (src) {
+          const uint8_t* p = src + lc * 4 * W;
+          if constexpr (W == 4) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+          } else if constexpr (W == 2) {
+            const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+            w[0] = q.x, w[1] = q.y;
+          } else {
+            w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+          }
+        }
+        const int left = a.groups - lc * 4 * W;  // scales of this chunk that exist
+        if (left < 4 * W) {                      // the last chunk: bytes past them are padding
 #pragma unroll
           for (int i = 0; i < W; ++i) {
             const int k = left - 4 * i;
-            const uint32_t mask = k >= 4 ? 0xffffffffu : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) r[4 * i + b] &= mask;
+            w[i] &= k >= 4 ? 0xffffffffu : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
           }
         }
         if (++lc == chunks) {
@@ -452,18 +444,17 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
       const int64_t iters = mine * chunks;
       bool ok = true;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) load(buf[j]);
-      for (int64_t it = 0; ok && it < iters; it += 4) {
+      for (int j = 0; j < kStages; ++j) load(buf[j]);
+      for (int64_t it = 0; ok && it < iters; it += kStages) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kStages; ++j) {
           if (ok && it + j < iters) {
-            // stage j: kStages == 4
-            ok = __all_sync(0xffffffffu, wait_bounded(empty(j), ((it / 4) & 1) ^ 1, abort_flag, a.err));
+            ok = __all_sync(0xffffffffu, wait_bounded(empty(j), ((it / kStages) & 1) ^ 1, abort_flag, a.err));
             if (ok) {
-              tc_fence_after();
-              tmem_st_cols<4 * W>(cols + j * C::kScaleCols, buf[j]);
-              tmem_st_wait();
-              tc_fence_before();
+#pragma unroll
+              for (int i = 0; i < W; ++i)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + j * C::kStage + 512 * i), "r"(buf[j][i]) : "memory");
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copies to tensor memory read it
               __syncwarp();
               if (lane == 0) mbar_arrive(full(j));
               load(buf[j]);
@@ -511,7 +502,6 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty(ab));
       };
-      const bool any = __any_sync(0xffffffffu, me.to >= 0);
       Mine next;
       if constexpr (OUT == kOutSwiglu) {
         // 32 features at a time (the code of one pass is 10 KB: its first run on an SM costs as much as its work)
@@ -604,26 +594,32 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
         } else {
           // Rows that are not aligned, or the last block row: 16 columns at a time, turned through
           // shared memory so that eight lanes write the 16 columns of one row.
-          uint8_t* turn = smem + C::kTurnOff + (warp - kWarpEpi) * 1024;
+          uint8_t* turn = smem + C::kTurnOff + (warp - kWarpEpi) * C::kTurn;
           const uint32_t rows_on = __ballot_sync(0xffffffffu, me.to >= 0);
-          const int last = 32 - __clz(rows_on);  // rows up to the last that is written
 #pragma unroll 1
           for (int v = 0; v < 8; ++v) {
             uint32_t p[16], w[8];
             tmem_ld16(tcol + 128 * (v >> 2) + 16 * (v & 3), p);
             tmem_ld_wait();
             const int at = 256 * me.u + 128 * (v >> 2) + 64 * hf + 16 * (v & 3);
-            if (any && at < a.n_out) {
+            if (at >= a.n_out) continue;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) w[i] = pack2(p[2 * i], p[2 * i + 1]);
+            for (int i = 0; i < 8; ++i) w[i] = pack2(p[2 * i], p[2 * i + 1]);
+            const int col = at + 2 * (lane & 7);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {  // 16 rows at a time
+              const uint32_t on = rows_on >> (16 * half) & 0xffffu;
+              if (on == 0) continue;
               __syncwarp();
-              reinterpret_cast<uint4*>(turn)[2 * lane] = make_uint4(w[0], w[1], w[2], w[3]);
-              reinterpret_cast<uint4*>(turn)[2 * lane + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+              if (lane >> 4 == half) {
+                reinterpret_cast<uint4*>(turn)[2 * (lane & 15)] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(turn)[2 * (lane & 15) + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
               __syncwarp();
-              const int col = at + 2 * (lane & 7);
+              const int last = 32 - __clz(on);  // rows up to the last that is written
               for (int r0 = 0; r0 < last; r0 += 4) {
                 const int r = r0 + (lane >> 3);
-                const int to = __shfl_sync(0xffffffffu, me.to, r);
+                const int to = __shfl_sync(0xffffffffu, me.to, 16 * half + r);
                 if (to < 0) continue;
                 const uint32_t two = *reinterpret_cast<const uint32_t*>(turn + 32 * r + 4 * (lane & 7));
                 uint16_t* at_row = o + static_cast<int64_t>(to) * a.out_ld;
@@ -665,7 +661,7 @@ cudaError_t launch(const MxProductLaunch& g, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     regs.store(fa.numRegs, std::memory_order_relaxed);
   }
-  if (regs.load(std::memory_order_relaxed) * kThreads < 128 * (kRegsLow + kRegsScales + 2 * kRegsEpi))
+  if (regs.load(std::memory_order_relaxed) * kThreads < 256 * (kRegsLow + kRegsEpi))
     return cudaErrorInvalidConfiguration;
   const moe_mx_weights* w = g.w;
   Args a{};
@@ -695,6 +691,12 @@ cudaError_t launch(const MxProductLaunch& g, cudaStream_t s) {
   a.h_pitch = static_cast<int64_t>(moe_mx_scale_pitch(FMT, w->n_out));
   a.err = g.err;
   a.early = g.early ? 1 : 0;
+  if (g.next) {
+    a.next_packed = static_cast<const uint8_t*>(g.next->packed);
+    a.next_upt = static_cast<int32_t>(mx_unit_rows(g.next));
+    a.next_chunks = static_cast<int32_t>(mx_chunks(g.next));
+    a.next_units = g.num_sms;
+  }
   RowMaps maps;
   for (int i = 0; i < 4; ++i)
     if (!encode_rows_map(&maps.box[i], g.x_codes, moe_mx_code_bytes(FMT, w->k), g.rows, 16u << i))
