@@ -74,9 +74,8 @@ struct GroupFactor {
   float g, six, inv;
 };
 template <int FMT>
-__device__ __forceinline__ GroupFactor group_factor(const float* global) {
+__device__ __forceinline__ GroupFactor group_factor(float g) {
   if constexpr (FMT != MOE_MX_NVFP4) return GroupFactor{1.f, 6.f, 0.f};
-  const float g = global ? __ldg(global) : 1.f;
   return GroupFactor{g, 6.0f * g, __frcp_rn(6.0f * g)};
 }
 

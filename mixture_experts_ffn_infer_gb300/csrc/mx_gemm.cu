@@ -43,6 +43,7 @@ constexpr int kStages = 4;
 constexpr int kTile = 128;
 constexpr int kMaxExperts = 1024;
 constexpr int kChunkTiles = 8;
+constexpr int kEarlyChunks = 8;  // 152 x 8 x 36 KB: 45 MB of the 129 MB L2, 6.6 us of HBM time
 constexpr int kABytes = kTile * 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kWarpWeights = 0, kWarpIssue = 1, kWarpRows = 2, kWarpScales = 4, kWarpEpi = 8;
@@ -317,6 +318,10 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
             }
             mbar_arrive_expect_tx(full(s), C::kWBytes);
             bulk_load(sbase + s * C::kStage, src + static_cast<int64_t>(c) * C::kWBytes, C::kWBytes, full(s), pol);
+            // The rows are not there yet: keep HBM busy beyond the stages that the copies fill.
+            if (a.early && it == kStages - 1)
+              for (int f = c + 1; f < min(chunks, c + 1 + kEarlyChunks); ++f)
+                bulk_prefetch_l2(src + static_cast<int64_t>(f) * C::kWBytes, C::kWBytes);
           }
         }
         if (!ok)
@@ -505,7 +510,7 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
       Mine next;
       if constexpr (OUT == kOutSwiglu) {
         // 32 features at a time (the code of one pass is 10 KB: its first run on an SM costs as much as its work)
-        const GroupFactor hf_factor = group_factor<FMT>(a.h_global);
+        const GroupFactor hf_factor = group_factor<FMT>(a.h_global ? __ldg(a.h_global) : 1.f);
         uint8_t* hc = a.h_codes + static_cast<int64_t>(me.row) * a.h_row_bytes;
         uint8_t* hs = a.h_scales + static_cast<int64_t>(me.row) * a.h_pitch;
 #pragma unroll 1

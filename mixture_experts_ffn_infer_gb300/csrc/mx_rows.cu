@@ -98,6 +98,20 @@ mx_rows_kernel(const MxRowsLaunch a) {
     for (int i = 0; i < 8; ++i) raw[it][i] = 0u;
     if (c < np) load_piece(a.x + t * a.x_ld + kPiece * c, a.wide_x != 0, raw[it]);
   }
+  // A row in one pass is a matter of latency: all that it reads is under way before anything waits (behind
+  // it, the next kernel's weights may already queue for HBM).
+  constexpr bool kEarly = ITER == 1;
+  uint32_t gain_early[8] = {};
+  int32_t at_early[8];
+  const int cols_early = min(static_cast<int>(threadIdx.x), np - 1);
+  if constexpr (kEarly) {
+    if constexpr (NORM) load_piece(a.gain + kPiece * cols_early, a.wide_gain != 0, gain_early);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      at_early[j] = j >= a.k ? -1 : a.positions ? __ldg(a.positions + t * a.k + j) : static_cast<int32_t>(t);
+  }
+  const float* gp = FMT == MOE_MX_NVFP4 ? a.global : nullptr;
+  const float global_early = gp ? __ldg(gp) : 1.f;
   float rs = 1.f;
   if constexpr (NORM) {
     float ss = 0.f;
@@ -141,7 +155,7 @@ mx_rows_kernel(const MxRowsLaunch a) {
     }
     rs = rsqrtf(ss / static_cast<float>(d) + a.eps);
   }
-  const GroupFactor factor = group_factor<FMT>(a.global);
+  const GroupFactor factor = group_factor<FMT>(global_early);
 #pragma unroll
   for (int it = 0; it < ITER; ++it) {
     const int c = it * blockDim.x + threadIdx.x;
@@ -151,7 +165,12 @@ mx_rows_kernel(const MxRowsLaunch a) {
       // sum * gain is exact in fp32 (8 bits by 8), so y = (sum * gain) * rs has one rounding
       if (c < np) {
         uint32_t gw[8];
-        load_piece(a.gain + kPiece * c, a.wide_gain != 0, gw);
+        if constexpr (kEarly) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) gw[i] = gain_early[i];
+        } else {
+          load_piece(a.gain + kPiece * c, a.wide_gain != 0, gw);
+        }
         float g[16];
         unpack(gw, g);
 #pragma unroll
@@ -185,7 +204,11 @@ mx_rows_kernel(const MxRowsLaunch a) {
       scale = sc.byte;
     }
     if (c >= np) continue;
-    if (a.k == 1) {
+    if constexpr (kEarly) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) store_codes<FMT>(a, at_early[j], c, w, scale);
+      for (int j = 8; j < a.k; ++j) store_codes<FMT>(a, __ldg(a.positions + t * a.k + j), c, w, scale);
+    } else if (a.k == 1) {
       store_codes<FMT>(a, a.positions ? __ldg(a.positions + t) : t, c, w, scale);
     } else {
       for (int j0 = 0; j0 < a.k; j0 += 4) {
