@@ -63,33 +63,94 @@ def _on(stream, fn, *args, **kw):
 
 class MxRows:
     """Rows of `cols` columns in a microscaled format: uint8 codes [rows, .] and scales [rows, pitch] (None for
-    bf16), and NVFP4's fp32 factor [1] (None = 1)."""
+    bf16), and NVFP4's fp32 factor [1] (None = 1).
 
-    __slots__ = ("fmt", "cols", "codes", "scales", "global_scale")
+    Rows that a call here allocates keep codes and scales in one buffer and make the two tensors when they are asked
+    for; what is needed of them otherwise is where they are."""
+
+    __slots__ = ("fmt", "cols", "global_scale", "_rows", "_dev", "_codes", "_scales", "_buf", "_addr")
 
     def __init__(self, fmt, cols, codes, scales=None, global_scale=None):
         self.fmt = fmt
         self.cols = cols
-        self.codes = codes
-        self.scales = scales
         self.global_scale = global_scale
+        self._codes = codes
+        self._scales = scales
+        self._buf = None
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._views()
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._codes is None:
+            self._views()
+        return self._scales
 
     @property
     def rows(self):
-        return self.codes.shape[0]
+        return self._rows if self._buf is not None else self._codes.shape[0]
 
-    def _check(self, dev):
-        codes, scales = self.codes, self.scales
+    def _views(self):
+        n = self._rows
+        cb, pitch = _width(self.fmt, self.cols)
+        self._codes = self._buf[:n * cb].view(n, cb)
+        self._scales = self._buf[n * cb + 255 & -256:][:n * pitch].view(n, pitch) if pitch else None
+
+    def _check(self, dev=None):
+        """(rows, device index, address of the codes, address of the scales), once they are what they have to be."""
+        if self._buf is not None:             # as allocated below
+            if dev is not None and dev != self._dev:
+                raise ValueError(f"rows: expected on device {dev}")
+            return self._addr
+        codes, scales = self._codes, self._scales
         n = codes.shape[0]
+        if dev is None:
+            dev = codes.get_device()
         cb, pitch = _width(self.fmt, self.cols)
         _want(codes, "codes", _U8, (n, cb), dev)
         if pitch:
             if scales is None:
                 raise ValueError("scales: missing")
             _want(scales, "scales", _U8, (n, pitch), dev)
-        if self.global_scale is not None:
-            _want_values(self.global_scale, "global_scale", dev)
-        return n
+        return n, dev, codes.data_ptr(), scales.data_ptr() if pitch else None
+
+    def _factor(self, dev):
+        """Address of NVFP4's factor."""
+        g = self.global_scale
+        if g is None:
+            return None
+        _want_values(g, "global_scale", dev)
+        return g.data_ptr()
+
+
+def _new_rows(fmt, n, cols, device, dev, global_scale):
+    if not 0 <= fmt <= 3 or cols <= 0 or cols & 31:
+        raise MoeError(2, "moe_mx_code_bytes")
+    r = MxRows(fmt, cols, None, None, global_scale)
+    at = n * (cols * _BITS[fmt] >> 3)
+    if fmt:
+        scales = at + 255 & -256
+        r._buf = buf = _empty(scales + n * (cols // _GROUP[fmt] + 15 & -16), dtype=_U8, device=device)
+        base = buf.data_ptr()
+        r._addr = n, dev, base, base + scales
+    else:
+        r._buf = buf = _empty(at, dtype=_U8, device=device)
+        r._addr = n, dev, buf.data_ptr(), None
+    r._rows = n
+    r._dev = dev
+    return r
+
+
+def mx_rows(fmt, rows, cols, device="cuda", global_scale=None) -> MxRows:
+    """Uninitialised rows."""
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return _new_rows(fmt, rows, cols, device, device.index if device.type == "cuda" else -1, global_scale)
 
 
 class MxWeights:
@@ -129,28 +190,28 @@ class MxWeights:
         return got[0]
 
 
-def mx_rows(fmt, rows, cols, device="cuda", global_scale=None) -> MxRows:
-    """Uninitialised rows."""
-    cb, pitch = _width(fmt, cols)
-    return MxRows(fmt, cols, _empty((rows, cb), dtype=_U8, device=device),
-                  _empty((rows, pitch), dtype=_U8, device=device) if pitch else None, global_scale)
-
-
 def _out_rows(fmt, n, d, positions, out_rows, global_scale, out, device, dev):
-    """(k, rows, the rows to write) of a call that writes n tokens' rows."""
+    """(k, address of positions, address of the factor, rows, addresses of codes and scales, the rows to write)."""
     if global_scale is not None:
         _want_values(global_scale, "global_scale", dev)
-    k = 1
+        g = global_scale.data_ptr()
+    else:
+        g = None
     if positions is not None:
         k = positions.shape[1] if positions.dim() == 2 else 0
         _want(positions, "positions", _I32, (n, k), dev)
+        at = positions.data_ptr()
+    else:
+        k, at = 1, None
     if out is None:
-        m = n * k if out_rows is None else out_rows
-        return k, m, mx_rows(fmt, m, d, device, global_scale)
-    if out.fmt != fmt or out.cols != d:
-        raise ValueError("out: of another format or width")
-    out.global_scale = global_scale
-    return k, out._check(dev), out
+        out = _new_rows(fmt, n * k if out_rows is None else out_rows, d, device, dev, global_scale)
+        m, _, codes, scales = out._addr
+    else:
+        if out.fmt != fmt or out.cols != d:
+            raise ValueError("out: of another format or width")
+        m, _, codes, scales = out._check(dev)
+        out.global_scale = global_scale
+    return k, at, g, m, codes, scales, out
 
 
 def mx_quantise(x, fmt, positions=None, out_rows=None, global_scale=None, out=None, stream=None) -> MxRows:
@@ -162,12 +223,8 @@ def mx_quantise(x, fmt, positions=None, out_rows=None, global_scale=None, out=No
     n, d = shape
     dev = x.get_device()
     ld = _row_stride(x, "x", shape, dev)
-    k, m, out = _out_rows(fmt, n, d, positions, out_rows, global_scale, out, x.device, dev)
-    scales = out.scales
-    st = load_library().moe_mx_quantise(
-        fmt, n, k, d, x.data_ptr(), ld, None if positions is None else positions.data_ptr(),
-        None if global_scale is None else global_scale.data_ptr(), m, out.codes.data_ptr(),
-        None if scales is None else scales.data_ptr(), _raw_stream(dev))
+    k, at, g, m, codes, scales, out = _out_rows(fmt, n, d, positions, out_rows, global_scale, out, x.device, dev)
+    st = load_library().moe_mx_quantise(fmt, n, k, d, x.data_ptr(), ld, at, g, m, codes, scales, _raw_stream(dev))
     if st:
         raise MoeError(st, "moe_mx_quantise")
     return out
@@ -183,7 +240,10 @@ def mx_add_rmsnorm(x, residual, gain, eps, fmt, positions=None, out_rows=None, g
     n, d = shape
     dev, device = x.get_device(), x.device
     ld = _row_stride(x, "x", shape, dev)
-    r_ld = 0 if residual is None else _row_stride(residual, "residual", shape, dev)
+    if residual is None:
+        r_ld = res = None
+    else:
+        r_ld, res = _row_stride(residual, "residual", shape, dev), residual.data_ptr()
     _want(gain, "gain", _BF16, (d,), dev)
     if sum_out is None:
         r_ld = r_ld or d
@@ -194,13 +254,9 @@ def mx_add_rmsnorm(x, residual, gain, eps, fmt, positions=None, out_rows=None, g
         if r_ld and s_ld != r_ld and n > 1:
             raise ValueError("sum_out: its row stride differs from residual's")
         r_ld = r_ld or s_ld
-    k, m, out = _out_rows(fmt, n, d, positions, out_rows, global_scale, out, device, dev)
-    scales = out.scales
-    st = load_library().moe_mx_add_rmsnorm(
-        fmt, n, k, d, x.data_ptr(), ld, None if residual is None else residual.data_ptr(), r_ld, gain.data_ptr(), eps,
-        None if positions is None else positions.data_ptr(),
-        None if global_scale is None else global_scale.data_ptr(), m, sum_out.data_ptr(), out.codes.data_ptr(),
-        None if scales is None else scales.data_ptr(), _raw_stream(dev))
+    k, at, g, m, codes, scales, out = _out_rows(fmt, n, d, positions, out_rows, global_scale, out, device, dev)
+    st = load_library().moe_mx_add_rmsnorm(fmt, n, k, d, x.data_ptr(), ld, res, r_ld, gain.data_ptr(), eps, at, g, m,
+                                           sum_out.data_ptr(), codes, scales, _raw_stream(dev))
     if st:
         raise MoeError(st, "moe_mx_add_rmsnorm")
     return out, sum_out
@@ -210,16 +266,14 @@ def mx_dequantise(r: MxRows, out=None, stream=None):
     """bf16 values of rows."""
     if stream is not None:
         return _on(stream, mx_dequantise, r, out)
-    codes, scales, g = r.codes, r.scales, r.global_scale
-    dev = codes.get_device()
-    n, d = r._check(dev), r.cols
-    ld = d
+    n, dev, codes, scales = r._check()
+    g = r._factor(dev)
+    d = ld = r.cols
     if out is None:
-        out = _empty((n, d), dtype=_BF16, device=codes.device)
+        out = _empty((n, d), dtype=_BF16, device=r._buf.device if r._codes is None else r._codes.device)
     else:
         ld = _row_stride(out, "out", (n, d), dev)
-    st = load_library().moe_mx_dequantise(r.fmt, n, d, codes.data_ptr(), None if scales is None else scales.data_ptr(),
-                                          None if g is None else g.data_ptr(), out.data_ptr(), ld, _raw_stream(dev))
+    st = load_library().moe_mx_dequantise(r.fmt, n, d, codes, scales, g, out.data_ptr(), ld, _raw_stream(dev))
     if st:
         raise MoeError(st, "moe_mx_dequantise")
     return out
@@ -229,21 +283,21 @@ def mx_pack(rows: MxRows, num_experts, up=None, alpha=None, alpha_up=None, strea
     """Packed weights from rows [num_experts * n_out] of a format (up: the SwiGLU pair's second matrix)."""
     if stream is not None:
         return _on(stream, mx_pack, rows, num_experts, up, alpha, alpha_up)
-    dev = rows.codes.get_device()
-    n = rows._check(dev)
+    n, dev, codes, scales = rows._check()
     if num_experts < 1 or n % num_experts != 0:
         raise ValueError("rows: not a multiple of num_experts")
-    if up is not None and ((up.fmt, up.cols) != (rows.fmt, rows.cols) or up._check(dev) != n):
-        raise ValueError("up: not like the first matrix")
+    codes_up = scales_up = None
+    if up is not None:
+        if (up.fmt, up.cols, up.rows) != (rows.fmt, rows.cols, n):
+            raise ValueError("up: not like the first matrix")
+        _, _, codes_up, scales_up = up._check(dev)
     w = MxWeights(rows.fmt, num_experts, n // num_experts, rows.cols, None, alpha, alpha_up, up is not None)
     nbytes = moe_mx_packed_bytes(w.struct())
     if nbytes == 0:
         raise MoeError(2, "moe_mx_packed_bytes")
     w.packed = _empty(nbytes, dtype=_U8, device=rows.codes.device)
-    st = load_library().moe_mx_pack_weights(
-        w.checked(dev), *(None if t is None else t.data_ptr()
-                          for t in (rows.codes, rows.scales, up and up.codes, up and up.scales, w.packed)),
-        _raw_stream(dev))
+    st = load_library().moe_mx_pack_weights(w.checked(dev), codes, scales, codes_up, scales_up, w.packed.data_ptr(),
+                                            _raw_stream(dev))
     if st:
         raise MoeError(st, "moe_mx_pack_weights")
     return w
@@ -255,18 +309,18 @@ def mx_workspace(device="cuda"):
 
 
 def _operands(x: MxRows, w: MxWeights, offsets, ws):
-    """(device index, rows, the weights' struct, workspace) of checked operands."""
-    dev = x.codes.get_device()
-    n = x._check(dev)
+    """(rows, device index, addresses of codes, scales and factor, the weights' struct, workspace), checked."""
+    n, dev, codes, scales = x._check()
+    g = x._factor(dev)
     st = w.checked(dev)
     if x.fmt != w.fmt or x.cols != w.k:
         raise ValueError("x: of another format or width than the weights")
     _want(offsets, "offsets", _I32, (w.num_experts + 1,), dev)
     if ws is None:
-        ws = mx_workspace(x.codes.device)
+        ws = mx_workspace(offsets.device)
     elif ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"ws: expected contiguous bytes on device {dev}")
-    return dev, n, st, ws
+    return n, dev, codes, scales, g, st, ws
 
 
 def mx_grouped_product(x: MxRows, w: MxWeights, offsets, out=None, out_pos=None, row_weight=None, ws=None,
@@ -275,12 +329,12 @@ def mx_grouped_product(x: MxRows, w: MxWeights, offsets, out=None, out_pos=None,
     p = out_pos (int32 [rows], default r)."""
     if stream is not None:
         return _on(stream, mx_grouped_product, x, w, offsets, out, out_pos, row_weight, ws, out_type)
-    dev, n, struct, ws = _operands(x, w, offsets, ws)
+    n, dev, codes, scales, g, struct, ws = _operands(x, w, offsets, ws)
     dtype = _F16 if out_type == MOE_MX_OUT_F16 else _BF16
     cols = ld = w.n_out
     out_rows = n
     if out is None:
-        out = _empty((n, cols), dtype=dtype, device=x.codes.device)
+        out = _empty((n, cols), dtype=dtype, device=offsets.device)
     else:
         if out.dtype is not dtype or out.dim() != 2 or out.shape[1] != cols or out.get_device() != dev or (
                 cols > 1 and out.stride(1) != 1):
@@ -288,16 +342,16 @@ def mx_grouped_product(x: MxRows, w: MxWeights, offsets, out=None, out_pos=None,
         out_rows, ld = out.shape[0], out.stride(0)
         if out_rows < 2 and ld < cols:
             ld = cols
+    to = weight = None
     if out_pos is not None:
         _want(out_pos, "out_pos", _I32, (n,), dev)
+        to = out_pos.data_ptr()
     if row_weight is not None:
         _want_values(row_weight, "row_weight", dev, out_rows)
-    scales, g = x.scales, x.global_scale
-    st = load_library().moe_mx_grouped_product(
-        struct, n, x.codes.data_ptr(), None if scales is None else scales.data_ptr(),
-        None if g is None else g.data_ptr(), offsets.data_ptr(), out.data_ptr(), out_type, out_rows, ld,
-        None if out_pos is None else out_pos.data_ptr(), None if row_weight is None else row_weight.data_ptr(),
-        ws.data_ptr(), ws.nbytes, _raw_stream(dev))
+        weight = row_weight.data_ptr()
+    st = load_library().moe_mx_grouped_product(struct, n, codes, scales, g, offsets.data_ptr(), out.data_ptr(),
+                                               out_type, out_rows, ld, to, weight, ws.data_ptr(), ws.nbytes,
+                                               _raw_stream(dev))
     if st:
         raise MoeError(st, "moe_mx_grouped_product")
     return out
@@ -307,13 +361,12 @@ def mx_grouped_swiglu(x: MxRows, w: MxWeights, offsets, h_global=None, out=None,
     """Rows of silu(x Wg_e^T) * (x Wu_e^T) in the format of x."""
     if stream is not None:
         return _on(stream, mx_grouped_swiglu, x, w, offsets, h_global, out, ws)
-    dev, n, struct, ws = _operands(x, w, offsets, ws)
-    _, m, out = _out_rows(w.fmt, n, w.n_out, None, None, h_global, out, x.codes.device, dev)
+    n, dev, codes, scales, g, struct, ws = _operands(x, w, offsets, ws)
+    _, _, hg, m, h_codes, h_scales, out = _out_rows(w.fmt, n, w.n_out, None, None, h_global, out, offsets.device, dev)
     if m != n:
         raise ValueError("out: of another number of rows")
-    ptr = [None if t is None else t.data_ptr()
-           for t in (x.codes, x.scales, x.global_scale, offsets, h_global, out.codes, out.scales, ws)]
-    st = load_library().moe_mx_grouped_swiglu(struct, n, *ptr, ws.nbytes, _raw_stream(dev))
+    st = load_library().moe_mx_grouped_swiglu(struct, n, codes, scales, g, offsets.data_ptr(), hg, h_codes, h_scales,
+                                              ws.data_ptr(), ws.nbytes, _raw_stream(dev))
     if st:
         raise MoeError(st, "moe_mx_grouped_swiglu")
     return out
