@@ -157,6 +157,9 @@ struct MxRowsLaunch {
   uint16_t* sum;
   uint8_t* codes;
   uint8_t* scales;
+  // x, residual, gain and global were complete before the kernel in front began (positions are that one's):
+  // they are read while it still runs
+  int32_t late;
   int32_t wide_x, wide_r, wide_gain, wide_out;  // set by the launcher: rows on 32-byte boundaries
 };
 cudaError_t launch_mx_rows(int32_t fmt, const MxRowsLaunch& a, cudaStream_t s);

@@ -309,6 +309,7 @@ moe_status moe_mx_layer_forward(const moe_mx_weights* gu, const moe_mx_weights* 
   a.sum = static_cast<uint16_t*>(sum);
   a.codes = ws_at<uint8_t>(ws, L.x_codes);
   a.scales = ws_at<uint8_t>(ws, L.x_scales);
+  a.late = 1;
   if (launch_mx_rows(f, a, s) != cudaSuccess) return MOE_ERR_CUDA;
 
   MxProductLaunch g{};

@@ -86,8 +86,12 @@ template <int FMT, bool NORM, int ITER>
 __global__ void __launch_bounds__(ITER == 1 ? kRowsMaxThreads : kRowsSplitThreads)
 mx_rows_kernel(const MxRowsLaunch a) {
   __shared__ float part[32];
-  pdl_launch_dependents();
-  pdl_wait();
+  // A dependent kernel may read what the kernel in front of this one wrote without waiting
+  // (MxProductLaunch::early), so it is let in only after this wait.
+  if (!a.late) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
   const int64_t t = blockIdx.x;
   const int d = a.d, np = d / kPiece;
   uint32_t raw[ITER][8];
@@ -102,14 +106,15 @@ mx_rows_kernel(const MxRowsLaunch a) {
   // it, the next kernel's weights may already queue for HBM).
   constexpr bool kEarly = ITER == 1;
   uint32_t gain_early[8] = {};
-  int32_t at_early[8];
   const int cols_early = min(static_cast<int>(threadIdx.x), np - 1);
-  if constexpr (kEarly) {
-    if constexpr (NORM) load_piece(a.gain + kPiece * cols_early, a.wide_gain != 0, gain_early);
+  if constexpr (kEarly && NORM) load_piece(a.gain + kPiece * cols_early, a.wide_gain != 0, gain_early);
+  int32_t at_early[8];
+  auto load_positions = [&]() {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      at_early[j] = j >= a.k ? -1 : a.positions ? __ldg(a.positions + t * a.k + j) : static_cast<int32_t>(t);
-  }
+      at_early[j] = j >= a.k ? -1 : a.positions ? __ldcg(a.positions + t * a.k + j) : static_cast<int32_t>(t);
+  };
+  if (kEarly && !a.late) load_positions();
   const float* gp = FMT == MOE_MX_NVFP4 ? a.global : nullptr;
   const float global_early = gp ? __ldg(gp) : 1.f;
   float rs = 1.f;
@@ -156,6 +161,11 @@ mx_rows_kernel(const MxRowsLaunch a) {
     rs = rsqrtf(ss / static_cast<float>(d) + a.eps);
   }
   const GroupFactor factor = group_factor<FMT>(global_early);
+  if (a.late) {  // the positions are the kernel's in front, which may still run until here
+    pdl_wait();
+    pdl_launch_dependents();
+    if (kEarly) load_positions();
+  }
 #pragma unroll
   for (int it = 0; it < ITER; ++it) {
     const int c = it * blockDim.x + threadIdx.x;
@@ -207,14 +217,14 @@ mx_rows_kernel(const MxRowsLaunch a) {
     if constexpr (kEarly) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) store_codes<FMT>(a, at_early[j], c, w, scale);
-      for (int j = 8; j < a.k; ++j) store_codes<FMT>(a, __ldg(a.positions + t * a.k + j), c, w, scale);
+      for (int j = 8; j < a.k; ++j) store_codes<FMT>(a, __ldcg(a.positions + t * a.k + j), c, w, scale);
     } else if (a.k == 1) {
-      store_codes<FMT>(a, a.positions ? __ldg(a.positions + t) : t, c, w, scale);
+      store_codes<FMT>(a, a.positions ? __ldcg(a.positions + t) : t, c, w, scale);
     } else {
       for (int j0 = 0; j0 < a.k; j0 += 4) {
         int32_t at[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) at[j] = j0 + j < a.k ? __ldg(a.positions + t * a.k + j0 + j) : -1;
+        for (int j = 0; j < 4; ++j) at[j] = j0 + j < a.k ? __ldcg(a.positions + t * a.k + j0 + j) : -1;
 #pragma unroll
         for (int j = 0; j < 4; ++j) store_codes<FMT>(a, at[j], c, w, scale);
       }
@@ -253,8 +263,8 @@ __global__ void __launch_bounds__(256)
 mx_dequantise_kernel(int64_t rows, int32_t d, const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                      const float* __restrict__ global_p, uint16_t* __restrict__ out, int64_t out_ld, uint32_t magic,
                      int32_t segs, int32_t rpb, int32_t wide) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   const int np = d / kPiece;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / segs) * rpb;
   const int c0 = static_cast<int>(blockIdx.x % segs) * kDeqPieces;

@@ -472,6 +472,35 @@ def test_layer_graph_and_other_stream():
     assert torch.equal(out, again) and not torch.equal(out, want)
 
 
+@pytest.mark.parametrize("n", [1, 20, 3000])   # the routing plan in one kernel, and in several
+def test_layer_graph_with_nothing_left_in_the_workspace(n):
+    # each replay starts from a cleared workspace and other routing: a kernel that read the plan, or the rows, before
+    # they are written would give something else
+    c = layer_case("mxfp8", n, 256, 8, 4, 128, 21)
+    x, res, gain, ids, w = (c[p].cuda() for p in ("x", "res", "gain", "ids", "w"))
+    ws = torch.zeros(1 << 25, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    args = (x, res, gain, 1e-6, ids, w, c["gate_up"], c["down"])
+    mx.mx_layer_forward(*args, ws=ws, stream=s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        ws.zero_()
+        outs = [mx.mx_layer_forward(*args, ws=ws)[1] for _ in range(3)]
+    for k in range(4):
+        ids.copy_(torch.rand(n, 8, generator=gen(k)).topk(4, 1).indices.to(torch.int32))
+        x.copy_(bf16(gen(50 + k), n, 256))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        fresh = torch.zeros(1 << 25, dtype=torch.uint8, device="cuda")
+        _, want = mx.mx_layer_forward(*args, ws=fresh)
+        torch.cuda.synchronize()
+        for out in outs:
+            assert torch.equal(out, want)
+
+
 def test_rows_of_nothing():
     w = mx.mx_pack(make("mxfp4", 2, 64, 64, 1)[0], 2)
     x = mx.mx_rows(mx.MOE_MX_MXFP4, 0, 64)
