@@ -105,19 +105,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Codes of N consecutive columns, all of one group, into N / 8 (e2m1) or N / 4 (e4m3) words.
-// mul: s.mul, or for the MX formats s.mul times any factor that v still lacks.
+// Codes of N quotients into N / 8 (e2m1) or N / 4 (e4m3) words; all zero with `none` (a zero
+// divisor, or a group that is not finite).
 template <int FMT, int N>
-__device__ __forceinline__ void codes_of(const float* v, const GroupScale& s, float mul, uint32_t* w) {
-  auto scaled = [&](int i) { return FMT == MOE_MX_NVFP4 ? quotient(v[i], s.div, mul, 8.f) : v[i] * mul; };
-  const bool none = s.mul == 0.f;  // a zero divisor, or a group that is not finite
+__device__ __forceinline__ void pack_codes(const float* t, bool none, uint32_t* w) {
   if constexpr (FMT == MOE_MX_MXFP8) {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const uint32_t lo =
-          __nv_cvt_float2_to_fp8x2(make_float2(scaled(4 * i), scaled(4 * i + 1)), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi =
-          __nv_cvt_float2_to_fp8x2(make_float2(scaled(4 * i + 2), scaled(4 * i + 3)), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * i], t[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * i + 2], t[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
       w[i] = none ? 0u : lo | (hi << 16);
     }
   } else {
@@ -126,12 +122,26 @@ __device__ __forceinline__ void codes_of(const float* v, const GroupScale& s, fl
       uint32_t word = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        word |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(
-                    make_float2(scaled(8 * i + 2 * j), scaled(8 * i + 2 * j + 1)), __NV_E2M1, cudaRoundNearest))
+        word |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(t[8 * i + 2 * j], t[8 * i + 2 * j + 1]),
+                                                               __NV_E2M1, cudaRoundNearest))
                 << (8 * j);
       w[i] = none ? 0u : word;
     }
   }
+}
+
+template <int FMT>
+__device__ __forceinline__ float over_scale(float v, const GroupScale& s) {
+  return FMT == MOE_MX_NVFP4 ? quotient(v, s.div, s.mul, 8.f) : v * s.mul;
+}
+
+// Codes of N consecutive columns, all of one group.
+template <int FMT, int N>
+__device__ __forceinline__ void codes_of(const float* v, const GroupScale& s, uint32_t* w) {
+  float t[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) t[i] = over_scale<FMT>(v[i], s);
+  pack_codes<FMT, N>(t, s.mul == 0.f, w);
 }
 
 // The larger magnitude, NaN if either is: as bits it is above every finite value's.

@@ -547,7 +547,7 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
                 for (int i = 0; i < G; ++i) m = abs_max(m, h[G * g + i]);
                 const GroupScale sc = group_scale<FMT>(m, hf_factor);
                 sbytes |= sc.byte << (8 * g);
-                codes_of<FMT, G>(h + G * g, sc, sc.mul, out + (FMT == MOE_MX_MXFP8 ? 8 : G / 8) * g);
+                codes_of<FMT, G>(h + G * g, sc, out + (FMT == MOE_MX_MXFP8 ? 8 : G / 8) * g);
               }
               if constexpr (FMT == MOE_MX_MXFP8) {
                 *reinterpret_cast<uint4*>(hc + at) = make_uint4(out[0], out[1], out[2], out[3]);

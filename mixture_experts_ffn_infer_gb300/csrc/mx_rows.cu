@@ -79,13 +79,93 @@ __device__ __forceinline__ void store_codes(const MxRowsLaunch& a, int64_t pos, 
   }
 }
 
+// ---------------------------------------------------------------- the norm's last bits
+// A code of 2 to 4 bits turns a difference in y's last bit into a step of a quarter where y
+// lies on a rounding border.  So the norm's factor is carried as a sum of two floats, and 16
+// columns with a quotient within 2^-21 of a border are done again in double (about one in
+// 10^4): the codes are those of the exact y.  Against 64 bits, 8192 x 7168 to NVFP4 then has 0
+// to 2 codes off instead of 50 to 70.
+
+struct Pair {
+  float hi, lo;
+};
+// a + b with what the rounded sum leaves out (D. Knuth's two-sum).
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = a + b, bb = s - a;
+  return Pair{s, (a - (s - bb)) + (b - bb)};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  Pair s = two_sum(a.hi, b.hi);
+  s.lo += a.lo + b.lo;
+  return s;
+}
+__device__ __forceinline__ Pair warp_sum_pair(Pair v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v = add(v, Pair{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+  return v;
+}
+// 1 / sqrt(ss / d + eps): rsqrtf and one Newton step r + r (1 - m r^2) / 2 kept as a pair, its
+// residual from the exact parts of m r.
+__device__ __forceinline__ Pair rsqrt_mean(Pair ss, float d, float eps) {
+  const float q = ss.hi / d;
+  Pair m = two_sum(q, eps);
+  m.lo += (fmaf(-q, d, ss.hi) + ss.lo) / d;
+  const float r = rsqrtf(m.hi);
+  const float h = m.hi * r, low = fmaf(m.lo, r, fmaf(m.hi, r, -h));
+  const float lo = 0.5f * r * fmaf(-low, r, fmaf(-h, r, 1.f));
+  const float hi = r + lo;
+  const float rest = lo - (hi - r);
+  return rest == rest ? Pair{hi, rest} : Pair{r, 0.f};  // zero, infinity, NaN: as rsqrtf says
+}
+
+// Every border of e4m3 and e2m1 (and every power-of-two step of a scale) has at most four
+// leading bits, so near one the other bits are all zeros or all ones.
+__device__ __forceinline__ bool near_border(float t) {
+  return ((__float_as_uint(t) + 2u) & 0x7ffffu) <= 4u && t != 0.f;
+}
+// x rounded to odd: any narrower rounding of the result is that of x.
+__device__ __forceinline__ float to_odd(double x) {
+  const float f = __double2float_rz(x);
+  return static_cast<double>(f) == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
+// Codes of 16 columns and the byte of their group's scale, from p = sum * gain (exact), the
+// group's largest |p| and the norm's factor.
+template <int FMT>
+__device__ __noinline__ uint32_t exact_codes(const float* p, float top_p, Pair rs, GroupFactor f, uint32_t* w) {
+  const double factor = static_cast<double>(rs.hi) + rs.lo, top = top_p * factor;
+  uint32_t byte;
+  double inv = 0.;
+  if constexpr (FMT == MOE_MX_NVFP4) {
+    byte = __nv_cvt_float_to_fp8(to_odd(top / f.six), __NV_SATFINITE, __NV_E4M3);
+    const float div = e4m3_value(byte) * f.g;
+    if (div > 0.f) inv = 1. / div;
+  } else {
+    constexpr double kMax = FMT == MOE_MX_MXFP8 ? 448. : 6.;
+    auto power = [](int k127) { return __longlong_as_double(static_cast<long long>(k127 - 127 + 1023) << 52); };
+    int k127 = static_cast<int>(group_scale<FMT>(static_cast<float>(top), f).byte);
+    if (top > kMax * power(k127)) ++k127;
+    else if (k127 > 1 && top <= kMax * power(k127 - 1)) --k127;
+    byte = static_cast<uint32_t>(k127);
+    inv = 1. / power(k127);
+  }
+  float t[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) t[i] = to_odd(p[i] * factor * inv);
+  pack_codes<FMT, 16>(t, inv == 0., w);
+  return byte;
+}
+
 // ITER passes of blockDim.x pieces cover the row, held as the bf16 pairs they are
 // read as (the stored sum is bf16 too).  The sum of squares is taken per thread in
 // column order, then by shuffles, then over the warps.
 template <int FMT, bool NORM, int ITER>
-__global__ void __launch_bounds__(ITER == 1 ? kRowsMaxThreads : kRowsSplitThreads)
+// (two passes: five CTAs an SM with a few spilled words are faster than four without, 355 us against 369 for
+// 32,768 rows of 7168 to MXFP8 and back)
+__global__ void __launch_bounds__(ITER == 1 ? kRowsMaxThreads : kRowsSplitThreads, ITER == 1 ? 1 : ITER == 2 ? 5 : 2)
 mx_rows_kernel(const MxRowsLaunch a) {
-  __shared__ float part[32];
+  __shared__ Pair part[32];
   // A dependent kernel may read what the kernel in front of this one wrote without waiting
   // (MxProductLaunch::early), so it is let in only after this wait.
   if (!a.late) {
@@ -117,9 +197,9 @@ mx_rows_kernel(const MxRowsLaunch a) {
   if (kEarly && !a.late) load_positions();
   const float* gp = FMT == MOE_MX_NVFP4 ? a.global : nullptr;
   const float global_early = gp ? __ldg(gp) : 1.f;
-  float rs = 1.f;
+  Pair rs{1.f, 0.f};
   if constexpr (NORM) {
-    float ss = 0.f;
+    float sq[4] = {0.f, 0.f, 0.f, 0.f};
     if (a.residual) {
       uint32_t res[ITER][8];
 #pragma unroll
@@ -146,19 +226,17 @@ mx_rows_kernel(const MxRowsLaunch a) {
       float v[16];
       unpack(raw[it], v);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) ss = fmaf(v[i], v[i], ss);
+      for (int i = 0; i < 16; ++i) sq[i & 3] = fmaf(v[i], v[i], sq[i & 3]);
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    // a thread's sum of a few squares is plain fp32 (the threads' roundings average out)
+    Pair ss = warp_sum_pair(Pair{(sq[0] + sq[1]) + (sq[2] + sq[3]), 0.f});
     if (warps > 1) {
       if (lane == 0) part[warp] = ss;
       __syncthreads();
-      ss = lane < warps ? part[lane] : 0.f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      ss = warp_sum_pair(lane < warps ? part[lane] : Pair{0.f, 0.f});
     }
-    rs = rsqrtf(ss / static_cast<float>(d) + a.eps);
+    rs = rsqrt_mean(ss, static_cast<float>(d), a.eps);
   }
   const GroupFactor factor = group_factor<FMT>(global_early);
   if (a.late) {  // the positions are the kernel's in front, which may still run until here
@@ -186,32 +264,50 @@ mx_rows_kernel(const MxRowsLaunch a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] *= g[i];
       }
-      if constexpr (FMT == MOE_MX_BF16 || FMT == MOE_MX_NVFP4)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] *= rs;
     }
     uint32_t w[8];
     uint32_t scale = 0;
     if constexpr (FMT == MOE_MX_BF16) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+      for (int i = 0; i < 8; ++i)
+        w[i] = NORM ? pack_bf16(v[2 * i] * rs.hi, v[2 * i + 1] * rs.hi) : pack_bf16(v[2 * i], v[2 * i + 1]);
     } else {
       float m = 0.f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) m = abs_max(m, v[i]);
       if constexpr (Mx<FMT>::group == 32) m = abs_max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      // MX: rounding is monotone and the divisor a power of two, so the largest y is the
-      // largest product times rs, and y / 2^k = product * (rs 2^-k) to the bit
-      const bool late = NORM && FMT != MOE_MX_NVFP4;
-      const GroupScale sc = group_scale<FMT>(late ? m * rs : m, factor);
-      float mul = late ? rs * sc.mul : sc.mul;
-      if (late && !(mul < 3e38f)) {  // a group near zero: 2^126 times rs is past fp32
+      if constexpr (!NORM) {
+        const GroupScale sc = group_scale<FMT>(m, factor);
+        codes_of<FMT, 16>(v, sc, w);
+        scale = sc.byte;
+      } else {
+        // rounding is monotone, so the largest y is the largest product times rs
+        const float top = m * rs.hi;
+        const GroupScale sc = group_scale<FMT>(top, factor);
+        // The codes of quotients a little above and a little below the true ones (rs and the reciprocal are
+        // within 2^-22 together): where they agree they are the true quotients' codes.
+        const float mul = rs.hi * sc.mul;
+        const bool none = sc.mul == 0.f || m == 0.f;
+        uint32_t below[8];
+        float t[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] *= rs;
-        mul = sc.mul;
+        for (int i = 0; i < 16; ++i) t[i] = v[i] * (mul * (1.f + 0x1p-21f));
+        pack_codes<FMT, 16>(t, none, w);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t[i] = v[i] * (mul * (1.f - 0x1p-21f));
+        pack_codes<FMT, 16>(t, none, below);
+        scale = sc.byte;
+        const float edge = FMT == MOE_MX_NVFP4 ? quotient(top, factor.six, factor.inv, 1024.f) : top;
+        bool again = near_border(edge) || !(mul < 3e38f);  // (near zero, 2^126 times rs is past fp32)
+#pragma unroll
+        for (int i = 0; i < (FMT == MOE_MX_MXFP8 ? 4 : 2); ++i) again |= w[i] != below[i];
+        if (again && !none) {
+          float p[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) p[i] = v[i];
+          scale = exact_codes<FMT>(p, m, rs, factor, w);
+        }
       }
-      codes_of<FMT, 16>(v, sc, mul, w);
-      scale = sc.byte;
     }
     if (c >= np) continue;
     if constexpr (kEarly) {

@@ -166,6 +166,22 @@ def test_add_rmsnorm(fmt, n, d, residual):
     check_codes(rows, exact, fmt, rel=40 * 2.0**-24)
 
 
+@pytest.mark.parametrize("fmt,g", [("mxfp8", 1.0), ("mxfp4", 1.0), ("nvfp4", 2.0**-8)])
+def test_add_rmsnorm_codes_of_the_exact_values(fmt, g):
+    # With the factor as a pair and border cases in double, y's relative error is that of the threads' fp32 sums of 16
+    # squares (four chains): roundings of 2^-25 at random that average over 448 threads to below 2^-27, half of it in
+    # the root.  A code differs only with its quotient that near a border, at most 8 borders a binade: 2^-25 of the codes.
+    gg = gen(77)
+    n, d = 512, 7168
+    x, r, gain = bf16(gg, n, d), bf16(gg, n, d), (1 + bf16(gg, d, std=0.1)).to(torch.bfloat16)
+    rows, total = mx.mx_add_rmsnorm(x.cuda(), r.cuda(), gain.cuda(), 1e-6, mx.MX_FORMATS[fmt],
+                                    global_scale=dev_scalar(g) if fmt == "nvfp4" else None)
+    v = total.cpu().double()
+    codes, scales = plain.encode(v / torch.sqrt((v * v).mean(1, keepdim=True) + 1e-6) * gain.double(), fmt, g)
+    off = (rows.codes.cpu() != codes).sum().item() + 16 * (rows.scales.cpu()[:, :scales.shape[1]] != scales).sum().item()
+    assert off <= 32                            # 3.7 million codes: a fraction of one on average, or one group's scale
+
+
 def test_add_rmsnorm_in_place_and_strided():
     g = gen(8)
     d = 256
