@@ -517,6 +517,92 @@ def test_layer_graph_with_nothing_left_in_the_workspace(n):
             assert torch.equal(out, want)
 
 
+def test_layer_inputs_written_right_before_the_call():
+    # weights, rows and routing overwritten by the kernels in front of the call: nothing may be read ahead of them
+    c, o = layer_case("mxfp4", 40, 256, 8, 4, 128, 31), layer_case("mxfp4", 40, 256, 8, 4, 128, 41)
+    _, want = run_layer(o, "mxfp4")
+    names = ("x", "res", "gain", "ids", "w")
+    a, b = [[t[p].cuda() for p in names] for t in (c, o)]
+    ws = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    call = lambda: mx.mx_layer_forward(a[0], a[1], a[2], 1e-6, a[3], a[4], c["gate_up"], c["down"], ws=ws)[1]
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        for t, u in zip(a, b):
+            t.copy_(u)
+        c["gate_up"].packed.copy_(o["gate_up"].packed)
+        c["down"].packed.copy_(o["down"].packed)
+        out = call()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+class Guarded:
+    """Device buffers with 4 KB of a fixed pattern on either side of each."""
+
+    def __init__(self):
+        self.all = []
+
+    def bytes(self, *shape):
+        n = 1
+        for v in shape:
+            n *= v
+        buf = torch.full((8192 + (n + 255) // 256 * 256,), 0xC3, dtype=torch.uint8, device="cuda")
+        self.all.append((buf, n))
+        return buf[4096:4096 + n].view(*shape)
+
+    def like(self, dtype, *shape):
+        size = torch.empty(0, dtype=dtype).element_size()
+        return self.bytes(*shape[:-1], shape[-1] * size).view(dtype)
+
+    def rows(self, fmt, n, cols):
+        pitch = mx.moe_mx_scale_pitch(fmt, cols)
+        return mx.MxRows(fmt, cols, self.bytes(n, mx.moe_mx_code_bytes(fmt, cols)), self.bytes(n, pitch) if pitch else None)
+
+    def check(self):
+        torch.cuda.synchronize()
+        for buf, n in self.all:
+            assert (buf[:4096] == 0xC3).all() and (buf[4096 + n:] == 0xC3).all()
+
+
+@pytest.mark.parametrize("fmt", plain.FORMATS)
+def test_nothing_is_written_beside_the_outputs(fmt):
+    F, g = mx.MX_FORMATS[fmt], gen(6)
+    n, k, d, f, E = 45, 2, 256, 160, 3
+    m = Guarded()
+    x, res, gain = bf16(g, n, d).cuda(), bf16(g, n, d).cuda(), torch.ones(d, dtype=torch.bfloat16).cuda()
+    pos = torch.randperm(n * k, generator=g).to(torch.int32).reshape(n, k).cuda()
+    q = m.rows(F, n * k, d)
+    mx.mx_quantise(x, F, positions=pos, out=q)
+    mx.mx_add_rmsnorm(x, res, gain, 1e-6, F, positions=pos, out=q, sum_out=m.like(torch.bfloat16, n, d))
+    mx.mx_dequantise(q, out=m.like(torch.bfloat16, n * k, d))
+    gu = [rows_of(torch.randn(E * f, d, generator=g, dtype=torch.float64), fmt)[0] for _ in range(2)]
+    dn = rows_of(torch.randn(E * d, f, generator=g, dtype=torch.float64), fmt)[0]
+    w1, w2 = mx.mx_pack(gu[0], E, up=gu[1]), mx.mx_pack(dn, E)
+    for w, parts in ((w1, gu), (w2, [dn])):
+        packed = m.bytes(w.packed.numel())
+        mx.moe_mx_pack_weights(w.struct(), parts[0].codes, parts[0].scales, parts[-1].codes, parts[-1].scales, packed)
+        assert torch.equal(packed, w.packed)
+    off = offsets_of([40, 0, 50]).cuda()
+    h, ws = m.rows(F, n * k, f), m.bytes(256)
+    ws.zero_()
+    mx.mx_grouped_swiglu(q, w1, off, out=h, ws=ws)
+    mx.mx_grouped_product(h, w2, off, out=m.like(torch.bfloat16, n * k, d), ws=ws)
+    assert mx.moe_get_error(ws) == mx.MOE_OK
+    size = mx.moe_mx_layer_workspace_size(w1.struct(), w2.struct(), k, n)
+    ids = torch.rand(n, E, generator=g).topk(k, 1).indices.to(torch.int32).cuda()
+    wt = torch.rand(n, k, generator=g).cuda()
+    total, out, lws = m.like(torch.bfloat16, n, d), m.like(torch.bfloat16, n, d), m.bytes(size)
+    mx.moe_mx_layer_forward(w1.struct(), w2.struct(), k, n, x, res, gain, 1e-6, ids, wt, None, None, total, out, lws)
+    assert mx.moe_get_error(lws) == mx.MOE_OK
+    m.check()
+
+
 def test_rows_of_nothing():
     w = mx.mx_pack(make("mxfp4", 2, 64, 64, 1)[0], 2)
     x = mx.mx_rows(mx.MOE_MX_MXFP4, 0, 64)
