@@ -5,6 +5,10 @@ arch=compute_103a,code=sm_103a``), in parallel, then linked into one shared
 library with a static CUDA runtime.  The driver API is reached through
 ``cudaGetDriverEntryPointByVersion``, so loading the library needs no GPU.
 
+Beside it goes ``_mx_torch``, the Python module of the microscaled-format calls
+on torch tensors (``csrc/mx_torch.cpp``): host code, compiled with g++ against
+torch's headers and linked to the library.
+
     python -m mixture_experts_ffn_infer_gb300.build [--force] [--verbose]
 """
 
@@ -16,6 +20,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -23,6 +28,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_ffn.so")
+BINDING = os.path.join(HERE, "_mx_torch" + sysconfig.get_config_var("EXT_SUFFIX"))
+BINDING_SRC = os.path.join(CSRC, "mx_torch.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
@@ -42,14 +49,45 @@ def sources():
 
 def _deps():
     return sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
-        os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [os.path.abspath(__file__)]
+        os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [BINDING_SRC, os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _torch_paths():
+    """(include directories, library directory) of the installed torch."""
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    inc = os.path.join(root, "include")
+    return [inc, os.path.join(inc, "torch", "csrc", "api", "include")], os.path.join(root, "lib")
+
+
+def compile_binding() -> str:
+    inc, _ = _torch_paths()
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    obj = os.path.join(BUILD, "mx_torch.o")
+    cmd = ["g++", "-std=c++20", "-O2", "-fPIC", "-fvisibility=hidden", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=1", "-I", INCLUDE,
+           *[f"-isystem{p}" for p in (*inc, sysconfig.get_paths()["include"], cuda)], "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def link_binding(obj: str) -> None:
+    _, lib = _torch_paths()
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-Wl,--no-as-needed", LIB, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -68,18 +106,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj, r.stdout + r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        binding = ex.submit(compile_binding)  # the longest: first
         results = list(ex.map(compile_one, sources()))
+        binding = binding.result()
     if verbose:
         for _, log in results:
             if log.strip():
                 print(log, file=sys.stderr)
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *[o for o, _ in results], "-lpthread", "-ldl",
+    cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "-soname=libmoe_ffn.so", "-o", tmp, *[o for o, _ in results], "-lpthread", "-ldl",
            "-lrt"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    link_binding(binding)
     return LIB
 
 

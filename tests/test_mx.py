@@ -603,6 +603,29 @@ def test_nothing_is_written_beside_the_outputs(fmt):
     m.check()
 
 
+def test_calls_hold_no_references():
+    import sys
+    x = torch.randn(4, 64, device="cuda").to(torch.bfloat16)
+    gain, pos, g = torch.ones(64, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 1, dtype=torch.int32, device="cuda"), dev_scalar(1.0)
+    w = mx.mx_pack(make("nvfp4", 1, 64, 64, 1)[0], 1, alpha=dev_scalar(2.0))
+    off = offsets_of([4]).cuda()
+    held = [x, gain, pos, g, w, w.packed, w.alpha, off]
+    before = None
+    for i in range(60):
+        rows, total = mx.mx_add_rmsnorm(x, x, gain, 1e-6, 3, positions=pos, global_scale=g)
+        out = mx.mx_quantise(x, 3, global_scale=g, out=rows)
+        assert out is rows
+        y = mx.mx_grouped_product(rows, w, off)
+        mx.mx_dequantise(rows, out=total)
+        with pytest.raises(ValueError):
+            mx.mx_grouped_product(rows, w, off.long())
+        counts = [sys.getrefcount(o) for o in (*held, rows, rows.codes, total, y, None, mx.MxRows)]
+        if i == 5:
+            before = torch.cuda.memory_allocated(), counts
+    assert torch.cuda.memory_allocated() == before[0]
+    assert all(abs(a - b) < 10 for a, b in zip(counts, before[1]))
+
+
 def test_rows_of_nothing():
     w = mx.mx_pack(make("mxfp4", 2, 64, 64, 1)[0], 2)
     x = mx.mx_rows(mx.MOE_MX_MXFP4, 0, 64)

@@ -179,6 +179,20 @@ def test_host_tensors_are_refused(lib):
             call()
 
 
+def test_call_signatures(lib):
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for call in (lambda: mx.mx_quantise(), lambda: mx.mx_quantise(x), lambda: mx.mx_quantise(x, 1, fmt=1),
+                 lambda: mx.mx_quantise(x, 1, nothing=1), lambda: mx.mx_dequantise(1, 2, 3, 4), lambda: mx.mx_quantise(x, "a")):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: mx.mx_quantise(None, 1), lambda: mx.mx_quantise([1], 1), lambda: mx.mx_dequantise(None),
+                 lambda: mx.mx_grouped_product(mx.mx_rows(1, 4, 64, "cpu"), None, x)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(AttributeError):
+        mx.mx_dequantise(x)
+
+
 def test_header_is_c99(tmp_path):
     src = tmp_path / "a.c"
     src.write_text('#include "moe_mx.h"\nint main(void) { moe_mx_weights w = {MOE_MX_NVFP4, 1, 256, 256, 0, 0, 0, 0};\n'
