@@ -81,10 +81,10 @@ __device__ __forceinline__ void store_codes(const MxRowsLaunch& a, int64_t pos, 
 
 // ---------------------------------------------------------------- the norm's last bits
 // A code of 2 to 4 bits turns a difference in y's last bit into a step of a quarter where y
-// lies on a rounding border.  So the norm's factor is carried as a sum of two floats, and 16
-// columns with a quotient within 2^-21 of a border are done again in double (about one in
-// 10^4): the codes are those of the exact y.  Against 64 bits, 8192 x 7168 to NVFP4 then has 0
-// to 2 codes off instead of 50 to 70.
+// lies on a rounding border.  So the norm's factor is carried as a sum of two floats, the
+// scales come from exact products with it, and 16 columns with a quotient near a border are
+// done again with exact products: the codes are those of the exact y.  Against 64 bits, 8192 x
+// 7168 to NVFP4 then has 0 to 2 codes off instead of 50 to 70.
 
 struct Pair {
   float hi, lo;
@@ -119,42 +119,19 @@ __device__ __forceinline__ Pair rsqrt_mean(Pair ss, float d, float eps) {
   return rest == rest ? Pair{hi, rest} : Pair{r, 0.f};  // zero, infinity, NaN: as rsqrtf says
 }
 
-// Every border of e4m3 and e2m1 (and every power-of-two step of a scale) has at most four
-// leading bits, so near one the other bits are all zeros or all ones.
-__device__ __forceinline__ bool near_border(float t) {
-  return ((__float_as_uint(t) + 2u) & 0x7ffffu) <= 4u && t != 0.f;
+// p * r rounded to odd (the last bit set where the product is not exact): any narrower
+// rounding of the result is that of the product.
+__device__ __forceinline__ float odd_product(float p, Pair r) {
+  const float t = p * r.hi;
+  const float e = fmaf(p, r.lo, fmaf(p, r.hi, -t));
+  const float s = t + e, rest = e - (s - t);
+  const uint32_t b = __float_as_uint(s);
+  return rest == 0.f || (b & 1u) ? s : __uint_as_float((rest < 0.f) != (s < 0.f) ? b - 1u : b + 1u);
 }
-// x rounded to odd: any narrower rounding of the result is that of x.
-__device__ __forceinline__ float to_odd(double x) {
-  const float f = __double2float_rz(x);
-  return static_cast<double>(f) == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
-}
-
-// Codes of 16 columns and the byte of their group's scale, from p = sum * gain (exact), the
-// group's largest |p| and the norm's factor.
-template <int FMT>
-__device__ __noinline__ uint32_t exact_codes(const float* p, float top_p, Pair rs, GroupFactor f, uint32_t* w) {
-  const double factor = static_cast<double>(rs.hi) + rs.lo, top = top_p * factor;
-  uint32_t byte;
-  double inv = 0.;
-  if constexpr (FMT == MOE_MX_NVFP4) {
-    byte = __nv_cvt_float_to_fp8(to_odd(top / f.six), __NV_SATFINITE, __NV_E4M3);
-    const float div = e4m3_value(byte) * f.g;
-    if (div > 0.f) inv = 1. / div;
-  } else {
-    constexpr double kMax = FMT == MOE_MX_MXFP8 ? 448. : 6.;
-    auto power = [](int k127) { return __longlong_as_double(static_cast<long long>(k127 - 127 + 1023) << 52); };
-    int k127 = static_cast<int>(group_scale<FMT>(static_cast<float>(top), f).byte);
-    if (top > kMax * power(k127)) ++k127;
-    else if (k127 > 1 && top <= kMax * power(k127 - 1)) --k127;
-    byte = static_cast<uint32_t>(k127);
-    inv = 1. / power(k127);
-  }
-  float t[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) t[i] = to_odd(p[i] * factor * inv);
-  pack_codes<FMT, 16>(t, inv == 0., w);
-  return byte;
+// r / b as a pair, inv = 1 / b rounded.
+__device__ __forceinline__ Pair over(Pair r, float b, float inv) {
+  const float hi = quotient(r.hi, b, inv, 3e38f);
+  return Pair{hi, (fmaf(-hi, b, r.hi) + r.lo) * inv};
 }
 
 // ITER passes of blockDim.x pieces cover the row, held as the bf16 pairs they are
@@ -239,6 +216,7 @@ mx_rows_kernel(const MxRowsLaunch a) {
     rs = rsqrt_mean(ss, static_cast<float>(d), a.eps);
   }
   const GroupFactor factor = group_factor<FMT>(global_early);
+  const Pair rs_six = NORM && FMT == MOE_MX_NVFP4 ? over(rs, factor.six, factor.inv) : Pair{0.f, 0.f};
   if (a.late) {  // the positions are the kernel's in front, which may still run until here
     pdl_wait();
     pdl_launch_dependents();
@@ -281,31 +259,38 @@ mx_rows_kernel(const MxRowsLaunch a) {
         codes_of<FMT, 16>(v, sc, w);
         scale = sc.byte;
       } else {
-        // rounding is monotone, so the largest y is the largest product times rs
-        const float top = m * rs.hi;
-        const GroupScale sc = group_scale<FMT>(top, factor);
-        // The codes of quotients a little above and a little below the true ones (rs and the reciprocal are
-        // within 2^-22 together): where they agree they are the true quotients' codes.
+        // the group's scale is that of its largest y, the largest product times rs
+        const bool bad = !(m * rs.hi < __uint_as_float(0x7f800000u));
+        GroupScale sc{};
+        if constexpr (FMT == MOE_MX_NVFP4) {
+          sc.byte = bad ? 0x7fu : __nv_cvt_float_to_fp8(odd_product(m, rs_six), __NV_SATFINITE, __NV_E4M3);
+          sc.div = e4m3_value(sc.byte) * factor.g;
+          sc.mul = !bad && sc.div > 0.f ? __frcp_rn(sc.div) : 0.f;
+        } else {
+          sc = group_scale<FMT>(bad ? __uint_as_float(0x7f800000u) : odd_product(m, rs), factor);
+        }
+        scale = sc.byte;
+        // The codes of quotients a little above and a little below the true ones (what rounds between v and t is
+        // within five units, three for MX): where they agree they are the true quotients' codes.
+        constexpr float kOff = FMT == MOE_MX_NVFP4 ? 0x1p-21f : 0x1p-22f;
         const float mul = rs.hi * sc.mul;
         const bool none = sc.mul == 0.f || m == 0.f;
         uint32_t below[8];
         float t[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) t[i] = v[i] * (mul * (1.f + 0x1p-21f));
+        for (int i = 0; i < 16; ++i) t[i] = v[i] * (mul * (1.f + kOff));
         pack_codes<FMT, 16>(t, none, w);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) t[i] = v[i] * (mul * (1.f - 0x1p-21f));
+        for (int i = 0; i < 16; ++i) t[i] = v[i] * (mul * (1.f - kOff));
         pack_codes<FMT, 16>(t, none, below);
-        scale = sc.byte;
-        const float edge = FMT == MOE_MX_NVFP4 ? quotient(top, factor.six, factor.inv, 1024.f) : top;
-        bool again = near_border(edge) || !(mul < 3e38f);  // (near zero, 2^126 times rs is past fp32)
+        bool again = !(mul < 3e38f);  // (near zero, 2^126 times rs is past fp32)
 #pragma unroll
         for (int i = 0; i < (FMT == MOE_MX_MXFP8 ? 4 : 2); ++i) again |= w[i] != below[i];
         if (again && !none) {
-          float p[16];
+          const Pair by = FMT == MOE_MX_NVFP4 ? over(rs, sc.div, sc.mul) : rs;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) p[i] = v[i];
-          scale = exact_codes<FMT>(p, m, rs, factor, w);
+          for (int i = 0; i < 16; ++i) t[i] = odd_product(v[i], by) * (FMT == MOE_MX_NVFP4 ? 1.f : sc.mul);
+          pack_codes<FMT, 16>(t, false, w);
         }
       }
     }
