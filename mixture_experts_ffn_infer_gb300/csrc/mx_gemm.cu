@@ -574,7 +574,11 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
             return pack_bf16(y0, y1);
           }
         };
-        if (a.out_vec && 256 * (me.u + 1) <= a.n_out) {
+        const uint32_t rows_on = __ballot_sync(0xffffffffu, me.to >= 0);
+        if (rows_on == 0) {
+          release();
+          next = mine_of(x + stride);
+        } else if (a.out_vec) {
           uint32_t p[2][64];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -584,23 +588,63 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
           tmem_ld_wait();
           release();
           next = mine_of(x + stride);
-          if (me.to >= 0) {
-            uint16_t* to = o + static_cast<int64_t>(me.to) * a.out_ld + 256 * me.u + 64 * hf;
+          // Four lanes exchange their rows' four 32-byte pieces, so that a store covers whole 128-byte
+          // lines of eight rows instead of a piece of each of 32 (which the load/store unit takes one
+          // line at a time).
+          const int j = lane & 3;
+          uint16_t* to[4];
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+          for (int i = 0; i < 4; ++i) {
+            const int r = __shfl_sync(0xffffffffu, me.to, (lane & ~3) + i);
+            to[i] = r >= 0 ? o + static_cast<int64_t>(r) * a.out_ld : nullptr;
+          }
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            uint32_t w[4][8];
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[v][i] = pack2(p[m][16 * v + 2 * i], p[m][16 * v + 2 * i + 1]);
+#pragma unroll
+            for (int step = 1; step <= 2; step *= 2) {
+              const bool up = (lane & step) != 0;
 #pragma unroll
               for (int v = 0; v < 4; ++v) {
-                uint32_t w[8];
+                if (v & step) continue;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = pack2(p[m][16 * v + 2 * i], p[m][16 * v + 2 * i + 1]);
-                stg256(to + 128 * m + 16 * v, w);
+                for (int i = 0; i < 8; ++i) {
+                  const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[v][i] : w[v + step][i], step);
+                  if (up) w[v][i] = got;
+                  else w[v + step][i] = got;
+                }
               }
+            }
+            const int at = 256 * me.u + 128 * m + 64 * hf + 16 * j;  // w[i]: these 16 columns of the i-th row
+            if (at + 16 <= a.n_out) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (to[i]) stg256(to[i] + at, w[i]);
+            } else if (at < a.n_out) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (!to[i]) continue;
+#pragma unroll
+                for (int c = 0; c < 15; ++c)
+                  if (at + c < a.n_out) to[i][at + c] = static_cast<uint16_t>(w[i][c >> 1] >> (16 * (c & 1)));
+              }
+            }
           }
         } else {
-          // Rows that are not aligned, or the last block row: 16 columns at a time, turned through
-          // shared memory so that eight lanes write the 16 columns of one row.
+          // Rows that are not aligned: 16 columns of 16 rows at a time, turned through shared memory so
+          // that eight lanes write the 16 columns of one row.  What a lane writes is always of the same
+          // eight rows.
           uint8_t* turn = smem + C::kTurnOff + (warp - kWarpEpi) * C::kTurn;
-          const uint32_t rows_on = __ballot_sync(0xffffffffu, me.to >= 0);
+          uint16_t* to[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = __shfl_sync(0xffffffffu, me.to, 4 * i + (lane >> 3));
+            to[i] = r >= 0 ? o + r * a.out_ld + 2 * (lane & 7) : nullptr;
+          }
 #pragma unroll 1
           for (int v = 0; v < 8; ++v) {
             uint32_t p[16], w[8];
@@ -610,26 +654,25 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
             if (at >= a.n_out) continue;
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = pack2(p[2 * i], p[2 * i + 1]);
-            const int col = at + 2 * (lane & 7);
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {  // 16 rows at a time
-              const uint32_t on = rows_on >> (16 * half) & 0xffffu;
-              if (on == 0) continue;
+            const int left = a.n_out - at - 2 * (lane & 7);  // columns from this lane's first on
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if ((rows_on >> (16 * half) & 0xffffu) == 0) continue;
               __syncwarp();
               if (lane >> 4 == half) {
                 reinterpret_cast<uint4*>(turn)[2 * (lane & 15)] = make_uint4(w[0], w[1], w[2], w[3]);
                 reinterpret_cast<uint4*>(turn)[2 * (lane & 15) + 1] = make_uint4(w[4], w[5], w[6], w[7]);
               }
               __syncwarp();
-              const int last = 32 - __clz(on);  // rows up to the last that is written
-              for (int r0 = 0; r0 < last; r0 += 4) {
-                const int r = r0 + (lane >> 3);
-                const int to = __shfl_sync(0xffffffffu, me.to, 16 * half + r);
-                if (to < 0) continue;
-                const uint32_t two = *reinterpret_cast<const uint32_t*>(turn + 32 * r + 4 * (lane & 7));
-                uint16_t* at_row = o + static_cast<int64_t>(to) * a.out_ld;
-                if (col < a.n_out) at_row[col] = static_cast<uint16_t>(two);
-                if (col + 1 < a.n_out) at_row[col + 1] = static_cast<uint16_t>(two >> 16);
+              uint32_t two[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                two[i] = *reinterpret_cast<const uint32_t*>(turn + 32 * (4 * i + (lane >> 3)) + 4 * (lane & 7));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint16_t* q = to[4 * half + i];
+                if (q && left > 0) q[at] = static_cast<uint16_t>(two[i]);
+                if (q && left > 1) q[at + 1] = static_cast<uint16_t>(two[i] >> 16);
               }
             }
           }
