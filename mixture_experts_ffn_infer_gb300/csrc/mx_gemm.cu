@@ -28,6 +28,12 @@
 //
 // Warps (512 threads, one CTA per SM, persistent over units):
 //   0 weight copies   1 MMA issue   2 row copies   3 idle   4-7 row scales   8-15 epilogue
+// Few units with a long K leave most SMs idle, and each of the others bound by the latency
+// of its own four stages.  Then a cluster of 2, 4 or 8 CTAs takes one unit, each a part of
+// K; every CTA finishes a slice of the columns, for which the others write their partial
+// sums into its stage memory (added in the CTAs' order, so the result does not depend on
+// which is first).
+//
 // Within an expert up to eight tiles run a weight block one after another, so that
 // they take place at the same time and share it through L2.  Every wait is bounded
 // (common.cuh); after one gives up all roles drain and the kernel ends.
@@ -43,12 +49,18 @@ constexpr int kStages = 4;
 constexpr int kTile = 128;
 constexpr int kMaxExperts = 1024;
 constexpr int kChunkTiles = 8;
+constexpr int kSplitChunks = 6;
 constexpr int kEarlyChunks = 8;  // 152 x 8 x 36 KB: 45 MB of the 129 MB L2, 6.6 us of HBM time
 constexpr int kABytes = kTile * 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kWarpWeights = 0, kWarpIssue = 1, kWarpRows = 2, kWarpScales = 4, kWarpEpi = 8;
-constexpr int kRegsLow = 56, kRegsEpi = 200;
-static_assert(256 * (kRegsLow + kRegsEpi) <= 65536, "register split");
+// Registers a thread after the split: the epilogue's two warpgroups hold 128 accumulators (rows out, with
+// their pieces) or 64 and the features made of them (SwiGLU).
+template <int OUT>
+struct Regs {
+  static constexpr int low = OUT == 2 ? 80 : 56, epi = 256 - low;
+};
+constexpr int kRegsLaunch = 256 * 256;  // of the block: two warpgroups of each
 
 constexpr int kOutBf16 = 0, kOutF16 = 1, kOutSwiglu = 2;
 
@@ -60,12 +72,13 @@ struct Cfg {
   static constexpr int kStage = kWBytes + kABytes + kSBytes;
   static constexpr int kAcc = FMT == MOE_MX_BF16 ? 2 : 1;
   static constexpr uint32_t kScaleCols = 12 * kWords;  // 4 words columns of row scales, 8 of weight scales
-  static constexpr int kNumBars = 2 * kStages + 2 * kAcc + 1;
+  static constexpr int kNumBars = 2 * kStages + 2 * kAcc + 3;
   static constexpr int kBarOff = kStages * kStage;
   static constexpr int kPlanOff = kBarOff + kNumBars * 8 + 16;  // tile prefix, warp sums
   static constexpr int kTurnOff = (kPlanOff + (kMaxExperts + 1) * 4 + 32 * 4 + 15) / 16 * 16;
   static constexpr int kTurn = 512;  // an epilogue warp's
   static constexpr int kSmem = 1024 + kTurnOff + 8 * kTurn;
+  static_assert(kStages * kStage >= kTile * 256 * 4, "the other CTAs' partial sums");
   static_assert(kStage % 1024 == 0, "operand tiles stay 1024-byte aligned");
   static_assert(kSmem <= 232448, "shared memory per CTA");
   static_assert(256 * kAcc + kStages * kScaleCols <= kTmemCols, "tensor memory");
@@ -76,6 +89,7 @@ struct Args {
   const float* alpha;
   const float* alpha_up;
   int32_t experts, n_out, upt, chunks, groups;  // upt: packed block rows; groups: scales of a row
+  int32_t split;                                // CTAs (a cluster) of a unit
   int32_t rows;
   const uint8_t* x_scales;
   int64_t x_pitch;
@@ -182,6 +196,44 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
+// ---------------------------------------------------------------- clusters
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address in CTA `rank` of the cluster of what is at `addr` here.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void peer_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void peer_store(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// wait_bounded for what other CTAs of the cluster wrote before they arrived.
+__device__ __forceinline__ bool wait_peers(uint32_t bar, volatile uint32_t* abort_flag, uint32_t* err) {
+  const long long t0 = clock64();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar)
+        : "memory");
+    if (ok) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      *abort_flag = 1u;
+      atomicOr(err, DEV_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity))
@@ -218,7 +270,173 @@ __device__ __forceinline__ Unit unit_of(const int32_t* first_tile, const int32_t
   return un;
 }
 
+// 32 features of h from column `at` on, in the format, to their row's codes and scales (where `on`).
+template <int FMT>
+__device__ __forceinline__ void store_h(bool on, uint8_t* hc, uint8_t* hs, int at, const float (&h)[32],
+                                        const GroupFactor& hf_factor) {
+  if constexpr (FMT == MOE_MX_BF16) {
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack_bf16(h[2 * i], h[2 * i + 1]);
+    if (!on) return;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      *reinterpret_cast<uint4*>(hc + 2 * at + 16 * v) = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+  } else {
+    constexpr int G = Mx<FMT>::group;
+    uint32_t out[8];
+    uint32_t sbytes = 0;
+#pragma unroll
+    for (int g = 0; g < 32 / G; ++g) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < G; ++i) m = abs_max(m, h[G * g + i]);
+      const GroupScale sc = group_scale<FMT>(m, hf_factor);
+      sbytes |= sc.byte << (8 * g);
+      codes_of<FMT, G>(h + G * g, sc, out + (FMT == MOE_MX_MXFP8 ? 8 : G / 8) * g);
+    }
+    if (!on) return;
+    if constexpr (FMT == MOE_MX_MXFP8) {
+      *reinterpret_cast<uint4*>(hc + at) = make_uint4(out[0], out[1], out[2], out[3]);
+      *reinterpret_cast<uint4*>(hc + at + 16) = make_uint4(out[4], out[5], out[6], out[7]);
+    } else {
+      *reinterpret_cast<uint4*>(hc + at / 2) = make_uint4(out[0], out[1], out[2], out[3]);
+    }
+    if constexpr (G == 16) *reinterpret_cast<uint16_t*>(hs + at / 16) = static_cast<uint16_t>(sbytes);
+    else hs[at / 32] = static_cast<uint8_t>(sbytes);
+  }
+}
+
+// The epilogue of a cluster's unit: column c of a 128-column half is CTA c / width's.  What the
+// others own of this thread's row goes to them; what they have of this CTA's columns is added
+// to its own.
 template <int FMT, int OUT>
+__device__ __forceinline__ void finish_split(const Args& a, uint32_t sbase, uint32_t tcol, int rank, int hf, int tok,
+                                             bool speaker, int u, int row, int to, float f0, float f1,
+                                             uint32_t ready_bar, uint32_t parts_bar, volatile uint32_t* abort_flag) {
+  // (split is a power of two: its divisions as shifts; as divisions they took most of the epilogue)
+  const int lane = threadIdx.x & 31, split = a.split, log_width = 7 - (31 - __clz(split)), width = 1 << log_width;
+  const int half_split = split >> 1, my_half = rank * width >= 64;
+  const bool rows_on = __any_sync(0xffffffffu, to >= 0);
+  // this CTA's stages are free: the others may write to them
+  if (speaker && lane < split && lane != rank) peer_arrive(peer_addr(ready_bar, lane));
+  if (!__all_sync(0xffffffffu, wait_peers(ready_bar, abort_flag, a.err))) return;
+  // where CTA s's partial sums of columns col + 4 i .. of half m of this row are: float4s, rows innermost
+  auto part_at = [&](int s, int m, int col, int i) {
+    const uint32_t at = ((2 * s + m) << (log_width - 2)) + ((col & (width - 1)) >> 2) + i;
+    return sbase + 16u * (at * kTile + tok);
+  };
+  if (rows_on) {
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      const int col = 64 * hf + 16 * k, owner = col >> log_width;
+      if (owner == rank) continue;
+      uint32_t p[2][16];
+      tmem_ld16(tcol + 16 * k, p[0]);
+      tmem_ld16(tcol + 128 + 16 * k, p[1]);
+      tmem_ld_wait();
+      if (to >= 0)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const uint32_t dst = peer_addr(part_at(rank, m, col, 0), owner);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            peer_store(dst + 16 * kTile * i, p[m][4 * i], p[m][4 * i + 1], p[m][4 * i + 2], p[m][4 * i + 3]);
+        }
+    }
+  }
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  __syncwarp();
+  if (lane < half_split && half_split * hf + lane != rank) peer_arrive(peer_addr(parts_bar, half_split * hf + lane));
+  if (my_half != hf || !__all_sync(0xffffffffu, wait_peers(parts_bar, abort_flag, a.err)) || !rows_on) return;
+
+  // 16 columns of both halves, summed in the CTAs' order
+  auto summed = [&](int col, float* x0, float* x1) {
+    uint32_t p[2][16];
+    tmem_ld16(tcol + col - 64 * hf, p[0]);
+    tmem_ld16(tcol + 128 + col - 64 * hf, p[1]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x0[i] = x1[i] = 0.f;
+#pragma unroll 1
+    for (int s = 0; s < split; ++s) {
+      uint4 v[2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // (the CTA's own place holds nothing that is used)
+          v[m][i] = lds128(part_at(s, m, col, i));
+      if (s == rank) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[m][i] = make_uint4(p[m][4 * i], p[m][4 * i + 1], p[m][4 * i + 2], p[m][4 * i + 3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x0[4 * i] += __uint_as_float(v[0][i].x);
+        x0[4 * i + 1] += __uint_as_float(v[0][i].y);
+        x0[4 * i + 2] += __uint_as_float(v[0][i].z);
+        x0[4 * i + 3] += __uint_as_float(v[0][i].w);
+        x1[4 * i] += __uint_as_float(v[1][i].x);
+        x1[4 * i + 1] += __uint_as_float(v[1][i].y);
+        x1[4 * i + 2] += __uint_as_float(v[1][i].z);
+        x1[4 * i + 3] += __uint_as_float(v[1][i].w);
+      }
+    }
+  };
+  const int first = width * rank;
+  if constexpr (OUT == kOutSwiglu) {
+    const GroupFactor hf_factor = group_factor<FMT>(a.h_global ? __ldg(a.h_global) : 1.f);
+    uint8_t* hc = a.h_codes + static_cast<int64_t>(row) * a.h_row_bytes;
+    uint8_t* hs = a.h_scales + static_cast<int64_t>(row) * a.h_pitch;
+#pragma unroll 1
+    for (int col = first; col < first + width; col += 32) {
+      const int at = 128 * u + col;
+      float g[32], up[32];
+      summed(col, g, up);
+      summed(col + 16, g + 16, up + 16);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) g[i] = silu(g[i] * f0) * (up[i] * f1);
+      store_h<FMT>(to >= 0 && at < a.n_out, hc, hs, at, g, hf_factor);
+    }
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(max(to, 0)) * a.out_ld;
+    float top = 0.f;  // largest magnitude, for f16's range
+#pragma unroll 1
+    for (int col = first; col < first + width; col += 16) {
+      float x[2][16];
+      summed(col, x[0], x[1]);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int at = 256 * u + 128 * m + col;
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float y0 = x[m][2 * i] * f0, y1 = x[m][2 * i + 1] * f0;
+          if constexpr (OUT == kOutF16) {
+            top = fmaxf(top, fmaxf(fabsf(y0), fabsf(y1)));
+            const __half2 h2 = __floats2half2_rn(y0, y1);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h2);
+          } else {
+            w[i] = pack_bf16(y0, y1);
+          }
+        }
+        if (a.out_vec && at + 16 <= a.n_out) {
+          if (to >= 0) stg256(o + at, w);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (to >= 0 && at + c < a.n_out) o[at + c] = static_cast<uint16_t>(w[c >> 1] >> (16 * (c & 1)));
+        }
+      }
+    }
+    if (OUT == kOutF16 && __any_sync(0xffffffffu, to >= 0 && top >= 65520.f) && lane == 0) atomicOr(a.err, DEV_ERR_RANGE);
+  }
+}
+
+template <int FMT, int OUT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
   using C = Cfg<FMT>;
@@ -231,6 +449,8 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
   auto acc_full = [&](int i) { return bar0 + 8u * (2 * kStages + i); };
   auto acc_empty = [&](int i) { return bar0 + 8u * (2 * kStages + C::kAcc + i); };
   const uint32_t drain_bar = bar0 + 8u * (C::kNumBars - 1);
+  const uint32_t ready_bar = bar0 + 8u * (C::kNumBars - 2);  // the peers' stages are free
+  const uint32_t parts_bar = bar0 + 8u * (C::kNumBars - 3);  // the peers' partial sums are here
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + C::kNumBars * 8);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   int32_t* first_tile = reinterpret_cast<int32_t*>(smem + C::kPlanOff);
@@ -248,6 +468,8 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
       mbar_init(acc_empty(i), 8);
     }
     mbar_init(drain_bar, 1);
+    mbar_init(ready_bar, SPLIT ? a.split - 1 : 1);
+    mbar_init(parts_bar, SPLIT ? 4 * (a.split - 1) : 1);  // four warps of each peer
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -295,22 +517,27 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (SPLIT) cluster_sync();  // the peers' barriers are initialised
   const int upt = a.upt, chunks = a.chunks;
   const int total = first_tile[a.experts] * upt;
+  // This CTA's units (one at most with a cluster to each), and its part of their chunks.
   const int stride = gridDim.x;
+  const int split = SPLIT ? a.split : 1;
+  const int rank = SPLIT ? static_cast<int>(blockIdx.x) % split : 0, first = static_cast<int>(blockIdx.x) / split;
+  const int c0 = SPLIT ? chunks * rank / split : 0, c1 = SPLIT ? chunks * (rank + 1) / split : chunks;
   auto unit_at = [&](int x) { return unit_of(first_tile, a.offsets, a.experts, upt, x); };
 
   if (warp < kWarpScales) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<OUT>::low));
     if (warp == kWarpWeights) {
       if (lane == 0) {
         const uint64_t pol = policy_evict_first();
         uint32_t it = 0;
         bool ok = true;
-        for (int x = blockIdx.x; ok && x < total; x += stride) {
+        for (int x = first; ok && x < total; x += stride) {
           const Unit un = unit_at(x);
           const uint8_t* src = a.packed + (static_cast<int64_t>(un.e) * upt + un.u) * chunks * C::kWBytes;
-          for (int c = 0; c < chunks; ++c, ++it) {
+          for (int c = c0; c < c1; ++c, ++it) {
             const int s = it % kStages;
             if (!wait_bounded(empty(s), ((it / kStages) & 1) ^ 1, abort_flag, a.err)) {
               ok = false;
@@ -320,7 +547,7 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
             bulk_load(sbase + s * C::kStage, src + static_cast<int64_t>(c) * C::kWBytes, C::kWBytes, full(s), pol);
             // The rows are not there yet: keep HBM busy beyond the stages that the copies fill.
             if (a.early && it == kStages - 1)
-              for (int f = c + 1; f < min(chunks, c + 1 + kEarlyChunks); ++f)
+              for (int f = c + 1; f < min(c1, c + 1 + kEarlyChunks); ++f)
                 bulk_prefetch_l2(src + static_cast<int64_t>(f) * C::kWBytes, C::kWBytes);
           }
         }
@@ -345,11 +572,11 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
         const uint64_t pol = policy_evict_last();
         uint32_t it = 0;
         bool ok = true;
-        for (int x = blockIdx.x; ok && x < total; x += stride) {
+        for (int x = first; ok && x < total; x += stride) {
           const Unit un = unit_at(x);
           const int b = un.nv <= 16 ? 0 : un.nv <= 32 ? 1 : un.nv <= 64 ? 2 : 3;
           const uint32_t bytes = (16u << b) * 128u;
-          for (int c = 0; c < chunks; ++c, ++it) {
+          for (int c = c0; c < c1; ++c, ++it) {
             const int s = it % kStages;
             if (!wait_bounded(empty(s), ((it / kStages) & 1) ^ 1, abort_flag, a.err)) {
               ok = false;
@@ -367,11 +594,11 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
       if (elect_one()) {
         uint32_t it = 0, ui = 0;
         bool ok = true;
-        for (int x = blockIdx.x; ok && x < total; x += stride, ++ui) {
+        for (int x = first; ok && x < total; x += stride, ++ui) {
           const int ab = ui % C::kAcc;
           if (!wait_bounded(acc_empty(ab), ((ui / C::kAcc) & 1) ^ 1, abort_flag, a.err)) break;
           const uint32_t d = tmem + 256u * ab;
-          for (int c = 0; c < chunks; ++c, ++it) {
+          for (int c = c0; c < c1; ++c, ++it) {
             const int s = it % kStages;
             if (!wait_bounded(full(s), (it / kStages) & 1, abort_flag, a.err)) {
               ok = false;
@@ -390,7 +617,7 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
             const uint64_t ad = desc_kmajor_sw128(w + C::kWBytes), bd = desc_kmajor_sw128(w);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              issue_mma<FMT>(d, desc_advance(ad, 32 * kk), desc_advance(bd, 32 * kk), sa, sb, kk, c > 0 || kk > 0);
+              issue_mma<FMT>(d, desc_advance(ad, 32 * kk), desc_advance(bd, 32 * kk), sa, sb, kk, c > c0 || kk > 0);
             tc_commit(empty(s));
           }
           if (ok) tc_commit(acc_full(ab));
@@ -401,7 +628,7 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
       __syncwarp();
     }
   } else if (warp < kWarpEpi) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<OUT>::low));
     if constexpr (FMT != MOE_MX_BF16) {
       pdl_wait();
       constexpr int W = C::kWords;
@@ -409,12 +636,12 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
       // word i of row r at 512 i + 16 (r % 32) + 4 (r / 32), as in the packed weights
       const uint32_t at = sbase + C::kWBytes + kABytes + 16 * lane + 4 * (warp & 3);
       // what is loaded runs four chunks ahead of what is stored
-      int lx = blockIdx.x, lc = 0;
+      int lx = first, lc = c0;
       const uint8_t* src = nullptr;
       uint32_t buf[kStages][W];
       auto load = [&](uint32_t (&w)[W]) {
         if (lx >= total) return;
-        if (lc == 0) {
+        if (lc == c0) {
           const Unit un = unit_at(lx);
           src = row < un.nv ? a.x_scales + (static_cast<int64_t>(un.row0) + row) * a.x_pitch : nullptr;
         }
@@ -440,13 +667,13 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
             w[i] &= k >= 4 ? 0xffffffffu : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
           }
         }
-        if (++lc == chunks) {
-          lc = 0;
+        if (++lc == c1) {
+          lc = c0;
           lx += stride;
         }
       };
-      const int64_t mine = blockIdx.x < total ? (total - 1 - static_cast<int>(blockIdx.x)) / stride + 1 : 0;
-      const int64_t iters = mine * chunks;
+      const int64_t mine = first < total ? (total - 1 - first) / stride + 1 : 0;
+      const int64_t iters = mine * (c1 - c0);
       bool ok = true;
 #pragma unroll
       for (int j = 0; j < kStages; ++j) load(buf[j]);
@@ -469,7 +696,7 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<OUT>::epi));
     if (a.early) pdl_wait();
     const int q = warp & 3, hf = (warp - kWarpEpi) >> 2;
     const int tok = q * 32 + lane;
@@ -496,25 +723,32 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
       return m;
     };
     uint32_t ui = 0;
-    Mine me = mine_of(blockIdx.x);
-    for (int x = blockIdx.x; x < total; x += stride, ++ui) {
+    Mine me = mine_of(first);
+    for (int x = first; x < total; x += stride, ++ui) {
       const int ab = ui % C::kAcc;
       if (!__all_sync(0xffffffffu, wait_bounded(acc_full(ab), (ui / C::kAcc) & 1, abort_flag, a.err))) break;
       tc_fence_after();
+      const uint32_t rows_on = __ballot_sync(0xffffffffu, me.to >= 0);
       const uint32_t tcol = tmem + lane_base + 256u * ab + 64u * hf;
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty(ab));
       };
+      if constexpr (SPLIT) {
+        finish_split<FMT, OUT>(a, sbase, tcol, rank, hf, tok, warp == kWarpEpi, me.u, me.row, me.to, me.f0, me.f1, ready_bar,
+                               parts_bar, abort_flag);
+        break;  // a cluster has one unit
+      }
       Mine next;
       if constexpr (OUT == kOutSwiglu) {
         // 32 features at a time (the code of one pass is 10 KB: its first run on an SM costs as much as its work)
         const GroupFactor hf_factor = group_factor<FMT>(a.h_global ? __ldg(a.h_global) : 1.f);
         uint8_t* hc = a.h_codes + static_cast<int64_t>(me.row) * a.h_row_bytes;
         uint8_t* hs = a.h_scales + static_cast<int64_t>(me.row) * a.h_pitch;
+        if (rows_on == 0) release();
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < 2 && rows_on != 0; ++half) {
           const int at = 128 * me.u + 64 * hf + 32 * half;
           float h[32];
           {
@@ -529,36 +763,7 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) h[i] = silu(__uint_as_float(g[i]) * me.f0) * (__uint_as_float(u[i]) * me.f1);
           }
-          if (me.to >= 0 && at < a.n_out) {
-            if constexpr (FMT == MOE_MX_BF16) {
-#pragma unroll
-              for (int v = 0; v < 4; ++v)
-                *reinterpret_cast<uint4*>(hc + 2 * at + 16 * v) =
-                    make_uint4(pack_bf16(h[8 * v], h[8 * v + 1]), pack_bf16(h[8 * v + 2], h[8 * v + 3]),
-                               pack_bf16(h[8 * v + 4], h[8 * v + 5]), pack_bf16(h[8 * v + 6], h[8 * v + 7]));
-            } else {
-              constexpr int G = Mx<FMT>::group;
-              uint32_t out[8];
-              uint32_t sbytes = 0;
-#pragma unroll
-              for (int g = 0; g < 32 / G; ++g) {
-                float m = 0.f;
-#pragma unroll
-                for (int i = 0; i < G; ++i) m = abs_max(m, h[G * g + i]);
-                const GroupScale sc = group_scale<FMT>(m, hf_factor);
-                sbytes |= sc.byte << (8 * g);
-                codes_of<FMT, G>(h + G * g, sc, out + (FMT == MOE_MX_MXFP8 ? 8 : G / 8) * g);
-              }
-              if constexpr (FMT == MOE_MX_MXFP8) {
-                *reinterpret_cast<uint4*>(hc + at) = make_uint4(out[0], out[1], out[2], out[3]);
-                *reinterpret_cast<uint4*>(hc + at + 16) = make_uint4(out[4], out[5], out[6], out[7]);
-              } else {
-                *reinterpret_cast<uint4*>(hc + at / 2) = make_uint4(out[0], out[1], out[2], out[3]);
-              }
-              if constexpr (G == 16) *reinterpret_cast<uint16_t*>(hs + at / 16) = static_cast<uint16_t>(sbytes);
-              else hs[at / 32] = static_cast<uint8_t>(sbytes);
-            }
-          }
+          store_h<FMT>(me.to >= 0 && at < a.n_out, hc, hs, at, h, hf_factor);
         }
         next = mine_of(x + stride);
       } else {
@@ -574,7 +779,6 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
             return pack_bf16(y0, y1);
           }
         };
-        const uint32_t rows_on = __ballot_sync(0xffffffffu, me.to >= 0);
         if (rows_on == 0) {
           release();
           next = mine_of(x + stride);
@@ -688,16 +892,17 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
     }
   }
   __syncthreads();
+  if constexpr (SPLIT) cluster_sync();  // no CTA's memory goes while another may still write to it
   if (warp == kWarpIssue) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
 }
 
-template <int FMT, int OUT>
-cudaError_t launch(const MxProductLaunch& g, cudaStream_t s) {
+template <int FMT, int OUT, bool SPLIT>
+cudaError_t launch(const MxProductLaunch& g, int64_t units, int split, cudaStream_t s) {
   using C = Cfg<FMT>;
-  auto kern = mx_product_kernel<FMT, OUT>;
+  auto kern = mx_product_kernel<FMT, OUT, SPLIT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   // An increase of the register split that cannot be met never returns: launch only if the kernel's own
@@ -709,7 +914,7 @@ cudaError_t launch(const MxProductLaunch& g, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     regs.store(fa.numRegs, std::memory_order_relaxed);
   }
-  if (regs.load(std::memory_order_relaxed) * kThreads < 256 * (kRegsLow + kRegsEpi))
+  if (regs.load(std::memory_order_relaxed) * kThreads < kRegsLaunch)
     return cudaErrorInvalidConfiguration;
   const moe_mx_weights* w = g.w;
   Args a{};
@@ -749,19 +954,41 @@ cudaError_t launch(const MxProductLaunch& g, cudaStream_t s) {
   for (int i = 0; i < 4; ++i)
     if (!encode_rows_map(&maps.box[i], g.x_codes, moe_mx_code_bytes(FMT, w->k), g.rows, 16u << i))
       return cudaErrorInvalidValue;
-  // no more CTAs than units there can be: an expert's last tile may be short
-  const int64_t tiles = static_cast<int64_t>(g.rows) / kTile + (g.rows < w->num_experts ? g.rows : w->num_experts);
-  const int64_t units = tiles * a.upt;
-  const int grid = static_cast<int>(units < g.num_sms ? units : g.num_sms);
-  return launch_maybe_overlapped(kern, grid, kThreads, C::kSmem, s, true, maps, a);
+  a.split = split;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(SPLIT ? units * split : units < g.num_sms ? units : g.num_sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, maps, a);
 }
 
 }  // namespace
 
+template <int FMT, int OUT>
+static cudaError_t launch_out(const MxProductLaunch& g, cudaStream_t s) {
+  // The most units there can be: an expert's last tile may be short.
+  const int64_t tiles = static_cast<int64_t>(g.rows) / kTile + (g.rows < g.w->num_experts ? g.rows : g.w->num_experts);
+  const int64_t units = tiles * mx_unit_rows(g.w), chunks = mx_chunks(g.w);
+  // A cluster to each unit where all of them fit and each CTA keeps kSplitChunks chunks (SwiGLU: up to
+  // four, so that a slice holds whole groups).
+  for (int n = OUT == kOutSwiglu ? 4 : 8; n > 1; n /= 2)
+    if (units * n <= g.num_sms && chunks >= kSplitChunks * n) return launch<FMT, OUT, true>(g, units, n, s);
+  return launch<FMT, OUT, false>(g, units, 1, s);
+}
+
 template <int FMT>
 static cudaError_t launch_format(const MxProductLaunch& g, cudaStream_t s) {
-  if (g.w->swiglu) return launch<FMT, kOutSwiglu>(g, s);
-  return g.out_f16 ? launch<FMT, kOutF16>(g, s) : launch<FMT, kOutBf16>(g, s);
+  if (g.w->swiglu) return launch_out<FMT, kOutSwiglu>(g, s);
+  return g.out_f16 ? launch_out<FMT, kOutF16>(g, s) : launch_out<FMT, kOutBf16>(g, s);
 }
 
 cudaError_t launch_mx_product(const MxProductLaunch& g, cudaStream_t s) {

@@ -274,6 +274,9 @@ CASES = [  # counts per expert, n_out, k
     ([300, 0, 64], 257, 1056),
     ([33] * 9, 512, 1024),
     ([1300], 300, 288),           # eleven tiles of one expert: two chunks
+    ([3], 300, 3104),             # few units, long rows: clusters of two, four and eight by format
+    ([100, 0, 1], 257, 6176),
+    ([1], 96, 7168),
 ]
 
 
@@ -356,7 +359,8 @@ def test_grouped_product_bad_offsets(bad):
 
 
 @pytest.mark.parametrize("fmt", plain.FORMATS)
-@pytest.mark.parametrize("counts,f,k", [([1], 32, 32), ([3, 0, 50], 160, 288), ([130, 7], 256, 1024)])
+@pytest.mark.parametrize("counts,f,k", [([1], 32, 32), ([3, 0, 50], 160, 288), ([130, 7], 256, 1024), ([20], 160, 3104),
+                                        ([1, 0, 2], 96, 7168)])
 def test_grouped_swiglu(fmt, counts, f, k):
     E, R = len(counts), sum(counts)
     x, xv = rows_of(torch.randn(R, k, generator=gen(7), dtype=torch.float64), fmt, 0.002)
