@@ -89,6 +89,7 @@ struct Args {
   const float* alpha;
   const float* alpha_up;
   int32_t experts, n_out, upt, chunks, groups;  // upt: packed block rows; groups: scales of a row
+  uint64_t upt_inv, next_upt_inv;
   int32_t split;                                // CTAs (a cluster) of a unit
   int32_t rows;
   const uint8_t* x_scales;
@@ -250,8 +251,10 @@ struct Unit {
 // Unit number x.  Expert e's units are consecutive, T tiles x upt block rows: its
 // tiles in chunks of eight, block row after block row within a chunk, tile after
 // tile within a block row.
-__device__ __forceinline__ Unit unit_of(const int32_t* first_tile, const int32_t* offsets, int experts, int upt, int x) {
-  const int t = x / upt;
+// (upt_inv: ceil(2^64 / upt), by which a 32-bit quotient is one multiplication; every role waits for this.)
+__device__ __forceinline__ Unit unit_of(const int32_t* first_tile, const int32_t* offsets, int experts, int upt,
+                                        uint64_t upt_inv, int x) {
+  const int t = upt == 1 ? x : static_cast<int>(__umul64hi(static_cast<uint64_t>(x), upt_inv));
   int lo = 0, hi = experts;  // first_tile[lo] <= t < first_tile[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -259,12 +262,12 @@ __device__ __forceinline__ Unit unit_of(const int32_t* first_tile, const int32_t
     else hi = mid;
   }
   const int l = x - first_tile[lo] * upt, tiles = first_tile[lo + 1] - first_tile[lo];
-  const int chunk = l / (kChunkTiles * upt), in = l - chunk * kChunkTiles * upt;
+  const int chunk = tiles <= kChunkTiles ? 0 : l / (kChunkTiles * upt), in = l - chunk * kChunkTiles * upt;
   const int nc = min(kChunkTiles, tiles - chunk * kChunkTiles);
-  const int tile = chunk * kChunkTiles + in % nc;
+  const int u = nc == 1 ? in : in / nc, tile = chunk * kChunkTiles + in - u * nc;
   Unit un;
   un.e = lo;
-  un.u = in / nc;
+  un.u = u;
   un.row0 = __ldg(offsets + lo) + tile * kTile;
   un.nv = min(kTile, __ldg(offsets + lo + 1) - un.row0);
   return un;
@@ -525,7 +528,7 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
   const int split = SPLIT ? a.split : 1;
   const int rank = SPLIT ? static_cast<int>(blockIdx.x) % split : 0, first = static_cast<int>(blockIdx.x) / split;
   const int c0 = SPLIT ? chunks * rank / split : 0, c1 = SPLIT ? chunks * (rank + 1) / split : chunks;
-  auto unit_at = [&](int x) { return unit_of(first_tile, a.offsets, a.experts, upt, x); };
+  auto unit_at = [&](int x) { return unit_of(first_tile, a.offsets, a.experts, upt, a.upt_inv, x); };
 
   if (warp < kWarpScales) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<OUT>::low));
@@ -558,7 +561,7 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
         if (OUT == kOutSwiglu && ok && a.next_packed) {
           const int next_total = min(first_tile[a.experts] * a.next_upt, a.next_units);
           for (int x = blockIdx.x; x < next_total; x += stride) {
-            const Unit un = unit_of(first_tile, a.offsets, a.experts, a.next_upt, x);
+            const Unit un = unit_of(first_tile, a.offsets, a.experts, a.next_upt, a.next_upt_inv, x);
             const uint8_t* src = a.next_packed + (static_cast<int64_t>(un.e) * a.next_upt + un.u) * a.next_chunks * C::kWBytes;
             for (int c = 0; c < min(a.next_chunks, 6); ++c)
               bulk_prefetch_l2(src + static_cast<int64_t>(c) * C::kWBytes, C::kWBytes);
@@ -923,7 +926,9 @@ cudaError_t launch(const MxProductLaunch& g, int64_t units, int split, cudaStrea
   a.alpha_up = w->alpha_up;
   a.experts = w->num_experts;
   a.n_out = w->n_out;
+  auto inverse = [](int64_t d) { return d > 1 ? ~0ull / static_cast<uint64_t>(d) + 1 : 0ull; };  // ceil(2^64 / d)
   a.upt = static_cast<int32_t>(mx_unit_rows(w));
+  a.upt_inv = inverse(a.upt);
   a.chunks = static_cast<int32_t>(mx_chunks(w));
   a.groups = Mx<FMT>::group ? w->k / (Mx<FMT>::group ? Mx<FMT>::group : 1) : 0;
   a.rows = g.rows;
@@ -947,6 +952,7 @@ cudaError_t launch(const MxProductLaunch& g, int64_t units, int split, cudaStrea
   if (g.next) {
     a.next_packed = static_cast<const uint8_t*>(g.next->packed);
     a.next_upt = static_cast<int32_t>(mx_unit_rows(g.next));
+    a.next_upt_inv = inverse(a.next_upt);
     a.next_chunks = static_cast<int32_t>(mx_chunks(g.next));
     a.next_units = g.num_sms;
   }
@@ -973,6 +979,31 @@ cudaError_t launch(const MxProductLaunch& g, int64_t units, int split, cudaStrea
 
 }  // namespace
 
+// How many clusters of n CTAs run at once (looked up until it is known; 0 where it cannot be).
+template <int FMT, int OUT>
+static int max_clusters(int n) {
+  using C = Cfg<FMT>;
+  static std::atomic<int> known[9];  // one more than the number
+  const int k = known[n].load(std::memory_order_relaxed);
+  if (k > 0) return k - 1;
+  auto kern = mx_product_kernel<FMT, OUT, true>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(n));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(n);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess) return 0;
+  known[n].store(clusters + 1, std::memory_order_relaxed);
+  return clusters;
+}
+
 template <int FMT, int OUT>
 static cudaError_t launch_out(const MxProductLaunch& g, cudaStream_t s) {
   // The most units there can be: an expert's last tile may be short.
@@ -980,8 +1011,10 @@ static cudaError_t launch_out(const MxProductLaunch& g, cudaStream_t s) {
   const int64_t units = tiles * mx_unit_rows(g.w), chunks = mx_chunks(g.w);
   // A cluster to each unit where all of them fit and each CTA keeps kSplitChunks chunks (SwiGLU: up to
   // four, so that a slice holds whole groups).
+  // (A cluster of eight leaves SMs of its processing cluster over: 15 or so fit at once, not 19.)
   for (int n = OUT == kOutSwiglu ? 4 : 8; n > 1; n /= 2)
-    if (units * n <= g.num_sms && chunks >= kSplitChunks * n) return launch<FMT, OUT, true>(g, units, n, s);
+    if (units * n <= g.num_sms && chunks >= kSplitChunks * n && units <= max_clusters<FMT, OUT>(n))
+      return launch<FMT, OUT, true>(g, units, n, s);
   return launch<FMT, OUT, false>(g, units, 1, s);
 }
 
