@@ -138,8 +138,8 @@ __device__ __forceinline__ Pair over(Pair r, float b, float inv) {
 // read as (the stored sum is bf16 too).  The sum of squares is taken per thread in
 // column order, then by shuffles, then over the warps.
 template <int FMT, bool NORM, int ITER>
-// (two passes: five CTAs an SM with a few spilled words are faster than four without, 355 us against 369 for
-// 32,768 rows of 7168 to MXFP8 and back)
+// (Two passes: five CTAs an SM with a few spilled words were faster than four without, 355 us against 369 for
+// 32,768 rows of 7168 to MXFP8 and back; 345 us since.)
 __global__ void __launch_bounds__(ITER == 1 ? kRowsMaxThreads : kRowsSplitThreads, ITER == 1 ? 1 : ITER == 2 ? 5 : 2)
 mx_rows_kernel(const MxRowsLaunch a) {
   __shared__ Pair part[32];
