@@ -79,12 +79,11 @@ __device__ __forceinline__ void store_codes(const MxRowsLaunch& a, int64_t pos, 
   }
 }
 
-// ---------------------------------------------------------------- the norm's last bits
+// ---------------------------------------------------------------- the sum of squares
 // A code of 2 to 4 bits turns a difference in y's last bit into a step of a quarter where y
-// lies on a rounding border.  So the norm's factor is carried as a sum of two floats, the
-// scales come from exact products with it, and 16 columns with a quotient near a border are
-// done again with exact products: the codes are those of the exact y.  Against 64 bits, 8192 x
-// 7168 to NVFP4 then has 0 to 2 codes off instead of 50 to 70.
+// lies on a rounding border, and the norm's factor moves a whole row's.  So the row's sum is
+// carried over lanes and warps as a sum of two floats: whatever the order, it is the same to
+// the last bit (but for the threads' own few squares).
 
 struct Pair {
   float hi, lo;
@@ -105,35 +104,6 @@ __device__ __forceinline__ Pair warp_sum_pair(Pair v) {
     v = add(v, Pair{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
   return v;
 }
-// 1 / sqrt(ss / d + eps): rsqrtf and one Newton step r + r (1 - m r^2) / 2 kept as a pair, its
-// residual from the exact parts of m r.
-__device__ __forceinline__ Pair rsqrt_mean(Pair ss, float d, float eps) {
-  const float q = ss.hi / d;
-  Pair m = two_sum(q, eps);
-  m.lo += (fmaf(-q, d, ss.hi) + ss.lo) / d;
-  const float r = rsqrtf(m.hi);
-  const float h = m.hi * r, low = fmaf(m.lo, r, fmaf(m.hi, r, -h));
-  const float lo = 0.5f * r * fmaf(-low, r, fmaf(-h, r, 1.f));
-  const float hi = r + lo;
-  const float rest = lo - (hi - r);
-  return rest == rest ? Pair{hi, rest} : Pair{r, 0.f};  // zero, infinity, NaN: as rsqrtf says
-}
-
-// p * r rounded to odd (the last bit set where the product is not exact): any narrower
-// rounding of the result is that of the product.
-__device__ __forceinline__ float odd_product(float p, Pair r) {
-  const float t = p * r.hi;
-  const float e = fmaf(p, r.lo, fmaf(p, r.hi, -t));
-  const float s = t + e, rest = e - (s - t);
-  const uint32_t b = __float_as_uint(s);
-  return rest == 0.f || (b & 1u) ? s : __uint_as_float((rest < 0.f) != (s < 0.f) ? b - 1u : b + 1u);
-}
-// r / b as a pair, inv = 1 / b rounded.
-__device__ __forceinline__ Pair over(Pair r, float b, float inv) {
-  const float hi = quotient(r.hi, b, inv, 3e38f);
-  return Pair{hi, (fmaf(-hi, b, r.hi) + r.lo) * inv};
-}
-
 // ITER passes of blockDim.x pieces cover the row, held as the bf16 pairs they are
 // read as (the stored sum is bf16 too).  The sum of squares is taken per thread in
 // column order, then by shuffles, then over the warps.
@@ -174,7 +144,7 @@ mx_rows_kernel(const MxRowsLaunch a) {
   if (kEarly && !a.late) load_positions();
   const float* gp = FMT == MOE_MX_NVFP4 ? a.global : nullptr;
   const float global_early = gp ? __ldg(gp) : 1.f;
-  Pair rs{1.f, 0.f};
+  float rs = 1.f;
   if constexpr (NORM) {
     float sq[4] = {0.f, 0.f, 0.f, 0.f};
     if (a.residual) {
@@ -213,10 +183,10 @@ mx_rows_kernel(const MxRowsLaunch a) {
       __syncthreads();
       ss = warp_sum_pair(lane < warps ? part[lane] : Pair{0.f, 0.f});
     }
-    rs = rsqrt_mean(ss, static_cast<float>(d), a.eps);
+    const float sum = ss.hi + ss.lo;  // (an infinite sum's low part is NaN)
+    rs = rsqrtf((sum == sum ? sum : ss.hi) / static_cast<float>(d) + a.eps);
   }
   const GroupFactor factor = group_factor<FMT>(global_early);
-  const Pair rs_six = NORM && FMT == MOE_MX_NVFP4 ? over(rs, factor.six, factor.inv) : Pair{0.f, 0.f};
   if (a.late) {  // the positions are the kernel's in front, which may still run until here
     pdl_wait();
     pdl_launch_dependents();
@@ -228,7 +198,6 @@ mx_rows_kernel(const MxRowsLaunch a) {
     float v[16];
     unpack(raw[it], v);
     if constexpr (NORM) {
-      // sum * gain is exact in fp32 (8 bits by 8), so y = (sum * gain) * rs has one rounding
       if (c < np) {
         uint32_t gw[8];
         if constexpr (kEarly) {
@@ -240,59 +209,22 @@ mx_rows_kernel(const MxRowsLaunch a) {
         float g[16];
         unpack(gw, g);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] *= g[i];
+        for (int i = 0; i < 16; ++i) v[i] = v[i] * rs * g[i];
       }
     }
     uint32_t w[8];
     uint32_t scale = 0;
     if constexpr (FMT == MOE_MX_BF16) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        w[i] = NORM ? pack_bf16(v[2 * i] * rs.hi, v[2 * i + 1] * rs.hi) : pack_bf16(v[2 * i], v[2 * i + 1]);
+      for (int i = 0; i < 8; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     } else {
       float m = 0.f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) m = abs_max(m, v[i]);
       if constexpr (Mx<FMT>::group == 32) m = abs_max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      if constexpr (!NORM) {
-        const GroupScale sc = group_scale<FMT>(m, factor);
-        codes_of<FMT, 16>(v, sc, w);
-        scale = sc.byte;
-      } else {
-        // the group's scale is that of its largest y, the largest product times rs
-        const bool bad = !(m * rs.hi < __uint_as_float(0x7f800000u));
-        GroupScale sc{};
-        if constexpr (FMT == MOE_MX_NVFP4) {
-          sc.byte = bad ? 0x7fu : __nv_cvt_float_to_fp8(odd_product(m, rs_six), __NV_SATFINITE, __NV_E4M3);
-          sc.div = e4m3_value(sc.byte) * factor.g;
-          sc.mul = !bad && sc.div > 0.f ? __frcp_rn(sc.div) : 0.f;
-        } else {
-          sc = group_scale<FMT>(bad ? __uint_as_float(0x7f800000u) : odd_product(m, rs), factor);
-        }
-        scale = sc.byte;
-        // The codes of quotients a little above and a little below the true ones (what rounds between v and t is
-        // within five units, three for MX): where they agree they are the true quotients' codes.
-        constexpr float kOff = FMT == MOE_MX_NVFP4 ? 0x1p-21f : 0x1p-22f;
-        const float mul = rs.hi * sc.mul;
-        const bool none = sc.mul == 0.f || m == 0.f;
-        uint32_t below[8];
-        float t[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) t[i] = v[i] * (mul * (1.f + kOff));
-        pack_codes<FMT, 16>(t, none, w);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) t[i] = v[i] * (mul * (1.f - kOff));
-        pack_codes<FMT, 16>(t, none, below);
-        bool again = !(mul < 3e38f);  // (near zero, 2^126 times rs is past fp32)
-#pragma unroll
-        for (int i = 0; i < (FMT == MOE_MX_MXFP8 ? 4 : 2); ++i) again |= w[i] != below[i];
-        if (again && !none) {
-          const Pair by = FMT == MOE_MX_NVFP4 ? over(rs, sc.div, sc.mul) : rs;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) t[i] = odd_product(v[i], by) * (FMT == MOE_MX_NVFP4 ? 1.f : sc.mul);
-          pack_codes<FMT, 16>(t, false, w);
-        }
-      }
+      const GroupScale sc = group_scale<FMT>(m, factor);
+      codes_of<FMT, 16>(v, sc, w);
+      scale = sc.byte;
     }
     if (c >= np) continue;
     if constexpr (kEarly) {

@@ -167,10 +167,10 @@ def test_add_rmsnorm(fmt, n, d, residual):
 
 
 @pytest.mark.parametrize("fmt,g", [("mxfp8", 1.0), ("mxfp4", 1.0), ("nvfp4", 2.0**-8)])
-def test_add_rmsnorm_codes_of_the_exact_values(fmt, g):
-    # With the factor as a pair and border cases in double, y's relative error is that of the threads' fp32 sums of 16
-    # squares (four chains): roundings of 2^-25 at random that average over 448 threads to below 2^-27, half of it in
-    # the root.  A code differs only with its quotient that near a border, at most 8 borders a binade: 2^-25 of the codes.
+def test_add_rmsnorm_few_codes_off_the_exact_values(fmt, g):
+    # y is off by four fp32 roundings (the sum, rsqrtf's two units, two products): 2^-22 at most.  A code differs only
+    # with its quotient that near a border, at most 8 borders a binade: 2^-18 of the codes, 14 of 3.7 million, and a
+    # group's scale as often, for which its 16 or 32 codes may follow.
     gg = gen(77)
     n, d = 512, 7168
     x, r, gain = bf16(gg, n, d), bf16(gg, n, d), (1 + bf16(gg, d, std=0.1)).to(torch.bfloat16)
@@ -178,8 +178,11 @@ def test_add_rmsnorm_codes_of_the_exact_values(fmt, g):
                                     global_scale=dev_scalar(g) if fmt == "nvfp4" else None)
     v = total.cpu().double()
     codes, scales = plain.encode(v / torch.sqrt((v * v).mean(1, keepdim=True) + 1e-6) * gain.double(), fmt, g)
-    off = (rows.codes.cpu() != codes).sum().item() + 16 * (rows.scales.cpu()[:, :scales.shape[1]] != scales).sum().item()
-    assert off <= 32                            # 3.7 million codes: a fraction of one on average, or one group's scale
+    groups = rows.scales.cpu()[:, :scales.shape[1]] != scales
+    assert groups.sum().item() <= 14
+    off = rows.codes.cpu() != codes
+    off &= ~groups.repeat_interleave(off.shape[1] // groups.shape[1], 1)
+    assert off.sum().item() <= 42               # three times the mean
 
 
 def test_add_rmsnorm_in_place_and_strided():
