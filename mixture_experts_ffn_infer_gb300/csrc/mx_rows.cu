@@ -107,7 +107,7 @@ __device__ __forceinline__ Pair warp_sum_pair(Pair v) {
 // ITER passes of blockDim.x pieces cover the row, held as the bf16 pairs they are
 // read as (the stored sum is bf16 too).  The sum of squares is taken per thread in
 // column order, then by shuffles, then over the warps.
-template <int FMT, bool NORM, int ITER>
+template <int FMT, bool NORM, int ITER, bool WARP>
 // (Two passes: five CTAs an SM with a few spilled words were faster than four without, 355 us against 369 for
 // 32,768 rows of 7168 to MXFP8 and back; 345 us since.)
 __global__ void __launch_bounds__(ITER == 1 ? kRowsMaxThreads : kRowsSplitThreads, ITER == 1 ? 1 : ITER == 2 ? 5 : 2)
@@ -119,12 +119,15 @@ mx_rows_kernel(const MxRowsLaunch a) {
     pdl_wait();
     pdl_launch_dependents();
   }
-  const int64_t t = blockIdx.x;
+  // the row, and this thread's place among those that share it
+  const int width = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t t = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5) : blockIdx.x;
+  if (WARP && t >= a.n) return;
   const int d = a.d, np = d / kPiece;
   uint32_t raw[ITER][8];
 #pragma unroll
   for (int it = 0; it < ITER; ++it) {
-    const int c = it * blockDim.x + threadIdx.x;
+    const int c = it * width + tid;
 #pragma unroll
     for (int i = 0; i < 8; ++i) raw[it][i] = 0u;
     if (c < np) load_piece(a.x + t * a.x_ld + kPiece * c, a.wide_x != 0, raw[it]);
@@ -133,7 +136,7 @@ mx_rows_kernel(const MxRowsLaunch a) {
   // it, the next kernel's weights may already queue for HBM).
   constexpr bool kEarly = ITER == 1;
   uint32_t gain_early[8] = {};
-  const int cols_early = min(static_cast<int>(threadIdx.x), np - 1);
+  const int cols_early = min(tid, np - 1);
   if constexpr (kEarly && NORM) load_piece(a.gain + kPiece * cols_early, a.wide_gain != 0, gain_early);
   int32_t at_early[8];
   auto load_positions = [&]() {
@@ -151,7 +154,7 @@ mx_rows_kernel(const MxRowsLaunch a) {
       uint32_t res[ITER][8];
 #pragma unroll
       for (int it = 0; it < ITER; ++it) {
-        const int c = it * blockDim.x + threadIdx.x;
+        const int c = it * width + tid;
 #pragma unroll
         for (int i = 0; i < 8; ++i) res[it][i] = 0u;
         if (c < np) load_piece(a.residual + t * a.r_ld + kPiece * c, a.wide_r != 0, res[it]);
@@ -168,17 +171,17 @@ mx_rows_kernel(const MxRowsLaunch a) {
     }
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
-      const int c = it * blockDim.x + threadIdx.x;
+      const int c = it * width + tid;
       if (a.sum && c < np) store_piece(a.sum + t * a.r_ld + kPiece * c, a.wide_r != 0, raw[it]);
       float v[16];
       unpack(raw[it], v);
 #pragma unroll
       for (int i = 0; i < 16; ++i) sq[i & 3] = fmaf(v[i], v[i], sq[i & 3]);
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = WARP ? 1 : blockDim.x >> 5;
     // a thread's sum of a few squares is plain fp32 (the threads' roundings average out)
     Pair ss = warp_sum_pair(Pair{(sq[0] + sq[1]) + (sq[2] + sq[3]), 0.f});
-    if (warps > 1) {
+    if (!WARP && warps > 1) {
       if (lane == 0) part[warp] = ss;
       __syncthreads();
       ss = warp_sum_pair(lane < warps ? part[lane] : Pair{0.f, 0.f});
@@ -194,7 +197,7 @@ mx_rows_kernel(const MxRowsLaunch a) {
   }
 #pragma unroll
   for (int it = 0; it < ITER; ++it) {
-    const int c = it * blockDim.x + threadIdx.x;
+    const int c = it * width + tid;
     float v[16];
     unpack(raw[it], v);
     if constexpr (NORM) {
@@ -250,20 +253,25 @@ bool aligned32(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p
 template <int FMT, bool NORM>
 cudaError_t launch_rows(MxRowsLaunch a, cudaStream_t s) {
   const int np = a.d / kPiece;
-  // Few rows: as many threads as the row has pieces, for the shortest way through one row.  More rows
-  // than SMs: 256 threads with several pieces each, so that an SM holds more rows in different phases.
-  const int most = a.n > 2 * device_sms() ? kRowsSplitThreads : kRowsMaxThreads;
+  // Few rows: as many threads as the row has pieces, for the shortest way through one row.  More rows than
+  // SMs: two pieces a thread, so that an SM holds more rows in different phases; and rows of up to 64 pieces
+  // one to a warp, eight to a CTA (a CTA each, the launch of the CTAs bounded them: 32,768 rows took 39 us
+  // whatever their width).
+  const bool many = a.n > 2 * device_sms(), by_warp = many && np <= 64;
   int iters = 1;
-  while (iters * most < np) iters *= 2;
-  const int threads = ((np + iters - 1) / iters + 31) / 32 * 32;
+  while (iters * (by_warp ? 32 : many ? kRowsSplitThreads : kRowsMaxThreads) < np) iters *= 2;
+  if (many && !by_warp && iters == 1) iters = 2;
+  const int threads = by_warp ? 256 : ((np + iters - 1) / iters + 31) / 32 * 32;
+  const int64_t grid = by_warp ? (a.n + 7) / 8 : a.n;
   a.wide_x = aligned32(a.x, a.x_ld);
   a.wide_r = aligned32(a.residual, a.r_ld) && aligned32(a.sum, a.r_ld);
   a.wide_gain = aligned32(a.gain, 0);
   a.wide_out = aligned32(a.codes, 0);
-  auto kern = iters == 1   ? mx_rows_kernel<FMT, NORM, 1>
-              : iters == 2 ? mx_rows_kernel<FMT, NORM, 2>
-                           : mx_rows_kernel<FMT, NORM, 4>;
-  return launch_maybe_overlapped(kern, static_cast<int>(a.n), threads, 0, s, true, a);
+  auto kern = by_warp      ? iters == 1 ? mx_rows_kernel<FMT, NORM, 1, true> : mx_rows_kernel<FMT, NORM, 2, true>
+              : iters == 1 ? mx_rows_kernel<FMT, NORM, 1, false>
+              : iters == 2 ? mx_rows_kernel<FMT, NORM, 2, false>
+                           : mx_rows_kernel<FMT, NORM, 4, false>;
+  return launch_maybe_overlapped(kern, static_cast<int>(grid), threads, 0, s, true, a);
 }
 
 // A CTA covers 1024 pieces, of as many rows as fit or of one row's part, four a
