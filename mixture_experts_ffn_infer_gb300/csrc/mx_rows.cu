@@ -5,7 +5,8 @@
 //
 // mx_rows_kernel       - [add the residual, RMS norm,] quantise, write to each
 //                        position of the token.  One CTA per token, or one
-//                        warp where many narrow rows come; a thread holds 16 consecutive columns at a time (32 bytes) in
+//                        warp where many narrow rows come; a thread holds
+//                        16 consecutive columns at a time (32 bytes) in
 //                        registers from the first read to the codes, so x is
 //                        read once, and a group is the thread's own columns
 //                        (16) or its and its neighbour's (32).  With eight

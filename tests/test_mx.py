@@ -166,6 +166,28 @@ def test_add_rmsnorm(fmt, n, d, residual):
     check_codes(rows, exact, fmt, rel=40 * 2.0**-24)
 
 
+@pytest.mark.parametrize("fmt", plain.FORMATS)
+@pytest.mark.parametrize("d", [32, 512, 544, 1024, 1056, 4128])
+def test_many_rows(fmt, d):
+    """More rows than SMs: a row to a warp up to 1024 columns (here with a last CTA of three), wider ones a CTA."""
+    g = gen(d)
+    n, k = 611, 9                               # positions past the eighth as well
+    x, r, gain = bf16(g, n, d), bf16(g, n, d), (1 + bf16(g, d, std=0.1)).to(torch.bfloat16)
+    F = mx.MX_FORMATS[fmt]
+    bits_equal(mx.mx_quantise(x.cuda(), F), *plain.encode(x.double(), fmt))
+    pos = torch.full((n, k), -1, dtype=torch.int32)
+    pos[:, 8] = torch.randperm(n, generator=g).to(torch.int32)
+    pos[:, 3] = pos[:, 8] + n
+    out = mx.mx_rows(F, 2 * n, d)
+    rows, total = mx.mx_add_rmsnorm(x.cuda(), r.cuda(), gain.cuda(), 1e-6, F, positions=pos.cuda(), out=out)
+    want = (x.float() + r.float()).to(torch.bfloat16)
+    assert torch.equal(total.cpu(), want)
+    v = want.double()
+    exact = torch.empty(2 * n, d, dtype=torch.float64)
+    exact[pos[:, 8].long()] = exact[pos[:, 3].long()] = v / torch.sqrt((v * v).mean(1, keepdim=True) + 1e-6) * gain.double()
+    check_codes(rows, exact, fmt, rel=40 * 2.0**-24)
+
+
 @pytest.mark.parametrize("fmt,g", [("mxfp8", 1.0), ("mxfp4", 1.0), ("nvfp4", 2.0**-8)])
 def test_add_rmsnorm_few_codes_off_the_exact_values(fmt, g):
     # y is off by four fp32 roundings (the sum, rsqrtf's two units, two products): 2^-22 at most.  A code differs only
