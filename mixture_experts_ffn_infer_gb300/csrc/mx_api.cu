@@ -12,6 +12,7 @@ constexpr int kMaxCols = 65536;
 constexpr int kMaxRowCols = 16384;  // moe_mx_quantise, moe_mx_add_rmsnorm: a row in one CTA's registers
 constexpr int kMaxPositions = 1024;
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 4096;
+constexpr int64_t kMaxUnits = (int64_t(1) << 31) - 4096;  // a CTA counts one round past them in 32 bits
 
 bool format_ok(int32_t f) { return f >= MOE_MX_BF16 && f <= MOE_MX_NVFP4; }
 bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -50,7 +51,7 @@ bool rows_args_ok(const MxRowsLaunch& a, int32_t format, bool norm) {
 moe_status product_check(const moe_mx_weights* w, int64_t rows) {
   if (!w || rows < 0) return MOE_ERR_INVALID_ARG;
   if (!weights_dims_ok(w) || rows > kMaxRows ||
-      (rows / 128 + w->num_experts) * mx_unit_rows(w) >= (int64_t(1) << 31))
+      (rows / 128 + w->num_experts) * mx_unit_rows(w) >= kMaxUnits)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

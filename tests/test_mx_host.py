@@ -108,6 +108,14 @@ def test_product_refusals(lib, kw, status):
     assert product(lib, **kw) == status
 
 
+def test_unit_count_stays_in_32_bits(lib):
+    # 128 block rows of 256; a CTA counts past the last unit by one round, for which 4096 numbers are kept
+    tiles = ((1 << 31) - 4096) // 128
+    call = lambda t: product(lib, w=W(E=1, n_out=32768), rows=128 * (t - 1), ld=32768, ws=None)
+    assert call(tiles - 1) == WORKSPACE         # accepted so far
+    assert call(tiles) == UNSUPPORTED
+
+
 def test_swiglu_refusals(lib):
     def call(w=W(swiglu=1), rows=8, xc=P, hc=P, hs=P, ws=P):
         return lib.moe_mx_grouped_swiglu(ctypes.byref(w), rows, xc, P, None, P, None, hc, hs, ws, 256, None)
