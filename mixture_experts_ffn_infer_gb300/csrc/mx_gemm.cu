@@ -30,7 +30,7 @@
 // Warps (512 threads, one CTA per SM, persistent over units):
 //   0 weight copies   1 MMA issue   2 row copies   3 idle   4-7 row scales   8-15 epilogue
 // Measured on one GB300: the down projection of 32,768 K2 rows over 384 experts (MXFP4) 520
-// us, 515 of them its bytes at the measured copy rate; dense 8192 x 7168 x 7168 NVFP4 5.0,
+// us, 517 of them its bytes at the measured copy rate; dense 8192 x 7168 x 7168 NVFP4 5.0,
 // MXFP4 5.4, MXFP8 3.0, bf16 1.7 PFLOP/s, bounded by the 50 to 55 KB that a chunk brings
 // from L2 (about 55 bytes a cycle and SM; bf16 by the MMAs).
 //
