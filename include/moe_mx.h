@@ -127,7 +127,7 @@ size_t moe_mx_packed_bytes(const moe_mx_weights *w);
 /* Products grouped by expert: rows expert_offsets[e] .. expert_offsets[e + 1] - 1 of x belong to expert e.
  *   out[p(r)] = row_weight[p(r)] * (global * alpha[e]) * x[r] W_e^T,   p(r) = out_pos[r]
  * accumulated in fp32 and rounded once.
- *   rows            rows of x, below 2^31
+ *   rows            rows of x, below 2^31; (rows / 128 + E) * ceil(n_out / 256) at most 2^31 - 4097
  *   x_codes, x_scales  rows of w->k columns in w->format;  x_global  x's factor (NULL = 1)
  *   expert_offsets  [E + 1] int32, ascending from >= 0 to <= rows; anything else computes nothing
  *                   and raises MOE_ERR_ROUTING.  Rows of no expert are left alone, empty experts cost nothing.
