@@ -29,8 +29,8 @@
 //
 // Warps (512 threads, one CTA per SM, persistent over units):
 //   0 weight copies   1 MMA issue   2 row copies   3 idle   4-7 row scales   8-15 epilogue
-// Measured on one GB300: the down projection of 32,768 K2 rows over 384 experts (MXFP4) 520
-// us, 517 of them its bytes at the measured copy rate; dense 8192 x 7168 x 7168 NVFP4 5.0,
+// Measured on one GB300: the down projection of 32,768 K2 rows over 384 experts (MXFP4) 489
+// us (its bytes at the rate of a plain copy: 517); dense 8192 x 7168 x 7168 NVFP4 5.0,
 // MXFP4 5.4, MXFP8 3.0, bf16 1.7 PFLOP/s, bounded by the 50 to 55 KB that a chunk brings
 // from L2 (about 55 bytes a cycle and SM; bf16 by the MMAs).
 //
@@ -58,6 +58,14 @@ constexpr int kMaxExperts = 1024;
 constexpr int kChunkTiles = 8;
 constexpr int kSplitChunks = 6;  // of a CTA, from which a cluster gains more than its exchange costs (about 2 us)
 constexpr int kEarlyChunks = 8;  // 152 x 8 x 36 KB: 45 MB of the 129 MB L2, 6.6 us of HBM time
+// The weights' lines are the first to leave L2 where little else moves, up to kStreamRows rows an expert on average,
+// or where one tile reads them and they are few enough for a part to stay for the next call (K2 layer, NVFP4, 1 token
+// 50.6 us, 56.5 with the normal policy; 16 experts x 7168 x 2048, 80 rows, 132 MB, 22.9 and 25.0).  Elsewhere further
+// tiles read them again, and outputs push lines that are to leave first out before all their readers came (down
+// product of 384 experts, 3.2 GB, 64 rows each 496 us with the normal policy, 520 without; layer of 256 tokens 1317
+// and 1347, of 4096 1600 and 1636; one bf16 expert x 6093 x 480, 25,414 rows, 128 and 144).
+constexpr int kStreamRows = 4;
+constexpr int64_t kStreamBytes = int64_t(512) << 20;
 constexpr int kABytes = kTile * 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kWarpWeights = 0, kWarpIssue = 1, kWarpRows = 2, kWarpScales = 4, kWarpEpi = 8;
@@ -114,6 +122,7 @@ struct Args {
   int64_t h_row_bytes, h_pitch;
   uint32_t* err;
   int32_t early;
+  int32_t stream;  // the weights' lines leave L2 first (kStreamRows)
   const uint8_t* next_packed;  // the product that follows on the same rows (may be null)
   int32_t next_upt, next_chunks, next_units;  // its units that run first
 };
@@ -541,7 +550,7 @@ mx_product_kernel(const __grid_constant__ RowMaps maps, const Args a) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<OUT>::low));
     if (warp == kWarpWeights) {
       if (lane == 0) {
-        const uint64_t pol = policy_evict_first();
+        const uint64_t pol = a.stream ? policy_evict_first() : policy_evict_normal();
         uint32_t it = 0;
         bool ok = true;
         for (int x = first; ok && x < total; x += stride) {
@@ -956,6 +965,9 @@ cudaError_t launch(const MxProductLaunch& g, int64_t units, int split, cudaStrea
   a.h_pitch = static_cast<int64_t>(moe_mx_scale_pitch(FMT, w->n_out));
   a.err = g.err;
   a.early = g.early ? 1 : 0;
+  const int64_t touched = static_cast<int64_t>(g.rows < w->num_experts ? g.rows : w->num_experts) * a.upt * a.chunks * C::kWBytes;
+  a.stream = g.rows <= static_cast<int64_t>(kStreamRows) * w->num_experts ||
+             (g.rows <= static_cast<int64_t>(kTile) * w->num_experts && touched <= kStreamBytes);
   if (g.next) {
     a.next_packed = static_cast<const uint8_t*>(g.next->packed);
     a.next_upt = static_cast<int32_t>(mx_unit_rows(g.next));
