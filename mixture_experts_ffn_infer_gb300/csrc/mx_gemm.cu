@@ -59,11 +59,13 @@ constexpr int kChunkTiles = 8;
 constexpr int kSplitChunks = 6;  // of a CTA, from which a cluster gains more than its exchange costs (about 2 us)
 constexpr int kEarlyChunks = 8;  // 152 x 8 x 36 KB: 45 MB of the 129 MB L2, 6.6 us of HBM time
 // The weights' lines are the first to leave L2 where little else moves, up to kStreamRows rows an expert on average,
-// or where one tile reads them and they are few enough for a part to stay for the next call (K2 layer, NVFP4, 1 token
-// 50.6 us, 56.5 with the normal policy; 16 experts x 7168 x 2048, 80 rows, 132 MB, 22.9 and 25.0).  Elsewhere further
-// tiles read them again, and outputs push lines that are to leave first out before all their readers came (down
-// product of 384 experts, 3.2 GB, 64 rows each 496 us with the normal policy, 520 without; layer of 256 tokens 1317
-// and 1347, of 4096 1600 and 1636; one bf16 expert x 6093 x 480, 25,414 rows, 128 and 144).
+// or where an expert's tiles run at the same time (kChunkTiles) and the weights are few enough for a part to stay for
+// the next call (K2 layer, NVFP4, 1 token 50.6 us, 56.5 with the normal policy; 16 experts x 7168 x 2048, 80 rows, 132
+// MB, 22.9 and 25.0; one bf16 expert x 4096 x 4096, 1000 rows, 27.4 and 29.6).  Elsewhere later tiles read them again,
+// or outputs push lines that are to leave first out before all their readers came (down product of 384 experts, 3.2
+// GB, 64 rows each 496 us with the normal policy, 520 without; layer of 256 tokens 1317 and 1347, of 4096 1616 and
+// 1655; one bf16 expert x 6093 x 480, 25,414 rows, 127 and 144; but 8 NVFP4 experts x 4096 x 4096, 16,384 rows, 122
+// and 120).
 constexpr int kStreamRows = 4;
 constexpr int64_t kStreamBytes = int64_t(512) << 20;
 constexpr int kABytes = kTile * 128;
@@ -967,7 +969,7 @@ cudaError_t launch(const MxProductLaunch& g, int64_t units, int split, cudaStrea
   a.early = g.early ? 1 : 0;
   const int64_t touched = static_cast<int64_t>(g.rows < w->num_experts ? g.rows : w->num_experts) * a.upt * a.chunks * C::kWBytes;
   a.stream = g.rows <= static_cast<int64_t>(kStreamRows) * w->num_experts ||
-             (g.rows <= static_cast<int64_t>(kTile) * w->num_experts && touched <= kStreamBytes);
+             (g.rows <= static_cast<int64_t>(kChunkTiles * kTile) * w->num_experts && touched <= kStreamBytes);
   if (g.next) {
     a.next_packed = static_cast<const uint8_t*>(g.next->packed);
     a.next_upt = static_cast<int32_t>(mx_unit_rows(g.next));
