@@ -145,12 +145,15 @@ const float* values(PyObject* o, const char* name, int64_t count, int dev) {
   return static_cast<const float*>(t.const_data_ptr());
 }
 
-// bf16 rows: the row stride in elements (that of a single row is not used, and torch may report any).
+// bf16 rows: the row stride in elements, d or more (that of a single row is not used, and torch may report any).
 int64_t row_stride(const at::Tensor& t, const char* name, int64_t n, int64_t d, int dev) {
   if (t.scalar_type() != at::kBFloat16 || t.dim() != 2 || t.size(0) != n || t.size(1) != d || t.get_device() != dev ||
       t.stride(1) != 1)
     refuse(name, "bf16 rows [" + std::to_string(n) + ", " + std::to_string(d) + "] on device " + std::to_string(dev), t);
-  return n > 1 ? t.stride(0) : std::max(t.stride(0), d);
+  if (n <= 1) return d;
+  // expanded rows, or a window that slides by less than a row
+  if (t.stride(0) < d) refuse(name, "rows of their own, not " + std::to_string(t.stride(0)) + " elements apart", t);
+  return t.stride(0);
 }
 
 void two_dims(const at::Tensor& t, const char* name) {
@@ -355,14 +358,14 @@ PyObject* mx_add_rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyO
     if (c.v[8]) {
       sum = tensor(c.v[8], "sum_out");
       const int64_t s_ld = row_stride(sum, "sum_out", n, d, dev);
-      if (r_ld && s_ld != r_ld && n > 1) throw Refused{"sum_out: its row stride differs from residual's"};
-      if (!r_ld) r_ld = s_ld;
+      if (res && s_ld != r_ld) throw Refused{"sum_out: its row stride differs from residual's"};
+      r_ld = s_ld;
     }
     Target t;
     target(&t, fmt, c.v[6] ? integer(c.v[6], "out_rows") : n * k, d, c.v[7], c.v[9], x, dev);
     const cudaStream_t s = stream_of(dev);
     if (!c.v[8]) {
-      if (!r_ld) r_ld = d;
+      if (!res) r_ld = d;
       sum = r_ld == d ? at::empty({n, d}, x.options()) : at::empty_strided({n, d}, {r_ld, 1}, x.options());
     }
     call("moe_mx_add_rmsnorm", [&] {

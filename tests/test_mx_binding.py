@@ -1,0 +1,41 @@
+"""What the Python binding of the microscaled-format calls decides from its tensors alone (no GPU needed: host and meta
+tensors are refused later than these are, by another message)."""
+
+import pytest
+import torch
+
+import mixture_experts_ffn_infer_gb300 as mx
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from mixture_experts_ffn_infer_gb300 import build
+    build.build()
+
+
+def bf16(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+# ---------------------------------------------------------------- rows that share memory
+
+@pytest.mark.parametrize("residual", [bf16(1, 64).expand(5, 64), bf16(5 * 32 + 32).as_strided((5, 64), (32, 1))])
+@pytest.mark.parametrize("sum_out", [None, bf16(5, 64), bf16(1, 64).expand(5, 64)])
+def test_a_residual_whose_rows_overlap_is_refused(residual, sum_out):
+    with pytest.raises(ValueError, match="residual: .*rows of their own"):
+        mx.mx_add_rmsnorm(bf16(5, 64), residual, bf16(64), 1e-6, 1, sum_out=sum_out)
+
+
+def test_other_rows_that_overlap_are_refused():
+    x, gain, shared = bf16(5, 64), bf16(64), bf16(1, 64).expand(5, 64)
+    with pytest.raises(ValueError, match="x: .*rows of their own"):
+        mx.mx_quantise(shared, 1)
+    with pytest.raises(ValueError, match="x: .*rows of their own"):
+        mx.mx_add_rmsnorm(shared, x, gain, 1e-6, 1)
+    with pytest.raises(ValueError, match="sum_out: .*rows of their own"):
+        mx.mx_add_rmsnorm(x, None, gain, 1e-6, 1, sum_out=shared)
+
+
+def test_the_row_strides_of_residual_and_sum_have_to_agree():
+    with pytest.raises(ValueError, match="row stride differs"):
+        mx.mx_add_rmsnorm(bf16(5, 64), bf16(5, 128)[:, :64], bf16(64), 1e-6, 1, sum_out=bf16(5, 64))
