@@ -261,11 +261,13 @@ struct Target {
   }
 };
 
-void target(Target* t, int64_t fmt, int64_t rows, int64_t cols, PyObject* global_scale, PyObject* out,
+// need: rows that have to be there (those of x, where no positions say which are written).
+void target(Target* t, int64_t fmt, int64_t rows, int64_t cols, int64_t need, PyObject* global_scale, PyObject* out,
             const at::Tensor& like, int dev) {
   if (out) {
     t->r = rows_of(out, &dev);
     if (t->r.fmt != fmt || t->r.cols != cols) throw Refused{"out: of another format or width"};
+    if (t->r.n < need) throw Refused{"out: fewer rows than x, and no positions"};
     if (PyObject_SetAttr(out, s_global_scale, global_scale ? global_scale : Py_None) < 0) throw PythonError{};
     Py_INCREF(out);
     t->object = out;
@@ -273,8 +275,9 @@ void target(Target* t, int64_t fmt, int64_t rows, int64_t cols, PyObject* global
   }
   int64_t cb, pitch;
   widths(fmt, cols, &cb, &pitch);
-  stream_of(dev);  // host tensors are refused before anything is allocated
   if (rows < 0) throw Refused{"out_rows: negative"};
+  if (rows < need) throw Refused{"out_rows: fewer rows than x, and no positions"};
+  stream_of(dev);  // host tensors are refused before anything is allocated
   t->r.fmt = static_cast<int32_t>(fmt);
   t->r.n = rows;
   t->r.cols = cols;
@@ -319,7 +322,7 @@ PyObject* mx_quantise(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObje
     const float* g = values(c.v[4], "global_scale", 1, dev);
     const c10::cuda::OptionalCUDAGuard on(dev < 0 ? std::nullopt : std::make_optional(x.device()));
     Target t;
-    target(&t, fmt, c.v[3] ? integer(c.v[3], "out_rows") : n * k, d, c.v[4], c.v[5], x, dev);
+    target(&t, fmt, c.v[3] ? integer(c.v[3], "out_rows") : n * k, d, c.v[2] ? 0 : n, c.v[4], c.v[5], x, dev);
     const cudaStream_t s = stream_of(dev);
     call("moe_mx_quantise", [&] {
       return moe_mx_quantise(t.r.fmt, n, static_cast<int32_t>(k), static_cast<int32_t>(d), x.const_data_ptr(), ld, pos, g,
@@ -362,7 +365,7 @@ PyObject* mx_add_rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyO
       r_ld = s_ld;
     }
     Target t;
-    target(&t, fmt, c.v[6] ? integer(c.v[6], "out_rows") : n * k, d, c.v[7], c.v[9], x, dev);
+    target(&t, fmt, c.v[6] ? integer(c.v[6], "out_rows") : n * k, d, c.v[5] ? 0 : n, c.v[7], c.v[9], x, dev);
     const cudaStream_t s = stream_of(dev);
     if (!c.v[8]) {
       if (!res) r_ld = d;
@@ -525,7 +528,7 @@ PyObject* mx_grouped_swiglu(PyObject*, PyObject* const* args, Py_ssize_t nargs, 
     const cudaStream_t s = stream_of(dev);
     const c10::cuda::CUDAGuard on(x.codes_t.device());
     Target t;
-    target(&t, w.format, x.n, w.n_out, c.v[3], c.v[4], x.codes_t, dev);
+    target(&t, w.format, x.n, w.n_out, 0, c.v[3], c.v[4], x.codes_t, dev);
     if (t.r.n != x.n) throw Refused{"out: of another number of rows"};
     const at::Tensor ws = workspace_of(c.v[5], x.codes_t, dev);
     call("moe_mx_grouped_swiglu", [&] {
@@ -613,7 +616,8 @@ PyMethodDef methods[] = {
     MX_CALL(mx_quantise,
             "mx_quantise(x, fmt, positions=None, out_rows=None, global_scale=None, out=None, stream=None) -> MxRows\n\n"
             "bf16 rows x [n, d] (any row stride that is a multiple of 8) into a format; row t goes to each of\n"
-            "positions[t] (int32 [n, k], default its own place) of `out` (out_rows rows, default n * k)."),
+            "positions[t] (int32 [n, k], entries outside the rows are skipped; default its own place, for which there\n"
+            "have to be n rows or more) of `out` (out_rows rows, default n * k)."),
     MX_CALL(mx_add_rmsnorm,
             "mx_add_rmsnorm(x, residual, gain, eps, fmt, positions=None, out_rows=None, global_scale=None,\n"
             "               sum_out=None, out=None, stream=None) -> (MxRows, sum)\n\n"

@@ -39,3 +39,19 @@ def test_other_rows_that_overlap_are_refused():
 def test_the_row_strides_of_residual_and_sum_have_to_agree():
     with pytest.raises(ValueError, match="row stride differs"):
         mx.mx_add_rmsnorm(bf16(5, 64), bf16(5, 128)[:, :64], bf16(64), 1e-6, 1, sum_out=bf16(5, 64))
+
+
+# ---------------------------------------------------------------- where rows go
+
+@pytest.mark.parametrize("fmt", range(4))
+def test_fewer_rows_than_x_are_refused_without_positions(fmt):
+    x, gain, few = bf16(5, 64), bf16(64), mx.mx_rows(fmt, 4, 64, "cpu")
+    for call in (lambda: mx.mx_quantise(x, fmt, out=few), lambda: mx.mx_quantise(x, fmt, out_rows=4),
+                 lambda: mx.mx_add_rmsnorm(x, x, gain, 1e-6, fmt, out=few),
+                 lambda: mx.mx_add_rmsnorm(x, x, gain, 1e-6, fmt, out_rows=4)):
+        with pytest.raises(ValueError, match="fewer rows than x, and no positions"):
+            call()
+    for call in (lambda: mx.mx_quantise(x, fmt, out=mx.mx_rows(fmt, 6, 64, "cpu")),          # more is room to spare
+                 lambda: mx.mx_quantise(x, fmt, positions=torch.zeros(5, 1, dtype=torch.int32), out_rows=4)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
