@@ -249,12 +249,15 @@ const float* factor_of(PyObject* rows, int dev, at::Tensor* held) {
   return p;
 }
 
-// Where a call writes its rows: a new MxRows or the caller's `out`.
+// Where a call writes its rows: a new MxRows or the caller's `out`, which gets its factor with the rows (take):
+// a call that is refused leaves both as they were.
 struct Target {
   Rows r;
   PyObject* object = nullptr;  // owned
+  PyObject* factor = nullptr;  // of the caller's rows; the call's argument
   ~Target() { Py_XDECREF(object); }
   PyObject* take() {
+    if (factor && PyObject_SetAttr(object, s_global_scale, factor) < 0) throw PythonError{};
     PyObject* o = object;
     object = nullptr;
     return o;
@@ -268,9 +271,8 @@ void target(Target* t, int64_t fmt, int64_t rows, int64_t cols, int64_t need, Py
     t->r = rows_of(out, &dev);
     if (t->r.fmt != fmt || t->r.cols != cols) throw Refused{"out: of another format or width"};
     if (t->r.n < need) throw Refused{"out: fewer rows than x, and no positions"};
-    if (PyObject_SetAttr(out, s_global_scale, global_scale ? global_scale : Py_None) < 0) throw PythonError{};
-    Py_INCREF(out);
-    t->object = out;
+    t->object = Py_NewRef(out);
+    t->factor = global_scale ? global_scale : Py_None;
     return;
   }
   int64_t cb, pitch;
@@ -375,13 +377,15 @@ PyObject* mx_add_rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyO
       return moe_mx_add_rmsnorm(t.r.fmt, n, static_cast<int32_t>(k), static_cast<int32_t>(d), x.const_data_ptr(), ld, res,
                                 r_ld, gain.const_data_ptr(), eps, pos, g, t.r.n, sum.data_ptr(), t.r.codes, t.r.scales, s);
     });
+    PyObject* rows = t.take();
     PyObject* sum_o = c.v[8] ? Py_NewRef(c.v[8]) : THPVariable_Wrap(sum);
     PyObject* both = sum_o ? PyTuple_New(2) : nullptr;
     if (!both) {
+      Py_DECREF(rows);
       Py_XDECREF(sum_o);
       throw PythonError{};
     }
-    PyTuple_SET_ITEM(both, 0, t.take());
+    PyTuple_SET_ITEM(both, 0, rows);
     PyTuple_SET_ITEM(both, 1, sum_o);
     return both;
   });

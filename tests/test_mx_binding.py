@@ -55,3 +55,19 @@ def test_fewer_rows_than_x_are_refused_without_positions(fmt):
                  lambda: mx.mx_quantise(x, fmt, positions=torch.zeros(5, 1, dtype=torch.int32), out_rows=4)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_a_refused_call_leaves_the_factor_of_out():
+    x, gain, old, new = bf16(5, 64), bf16(64), torch.ones(1), torch.full((1,), 2.0)
+    out = mx.mx_rows(3, 5, 64, "cpu", global_scale=old)
+    h = mx.mx_rows(3, 5, 64, "cpu", global_scale=old)
+    w = mx.MxWeights(3, 1, 64, 64, torch.zeros(mx.moe_mx_packed_bytes(mx.moe_mx_weights(3, 1, 64, 64, 1, None, None, None)),
+                                               dtype=torch.uint8), swiglu=True)
+    off = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: mx.mx_quantise(x, 3, global_scale=new, out=out),
+                 lambda: mx.mx_add_rmsnorm(x, x, gain, 1e-6, 3, global_scale=new, out=out),
+                 lambda: mx.mx_add_rmsnorm(x, x, gain, 1e-6, 3, out=out),
+                 lambda: mx.mx_grouped_swiglu(h, w, off, h_global=new, out=out)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+        assert out.global_scale is old

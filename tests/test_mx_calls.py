@@ -46,3 +46,19 @@ def test_residual_and_sum_keep_their_own_stride(own_sum):
     want, sums = mx.mx_add_rmsnorm(x, wide[:, :d].contiguous(), gain, 1e-6, 1)
     assert same(rows, want) and torch.equal(got, sums)
     assert torch.equal(total[:, d:], before[:, d:])
+
+
+# ---------------------------------------------------------------- the caller's rows
+
+def test_out_gets_its_factor_with_the_rows():
+    x, gain = bf16(1, 5, 64), bf16(2, 64)
+    old, new = torch.full((1,), 2.0**-4, device="cuda"), torch.full((1,), 2.0**-8, device="cuda")
+    out = mx.mx_quantise(x, 3, global_scale=old)
+    codes = out.codes.clone()
+    with pytest.raises(mx.MoeError):                             # refused by the library: rows not on 16 bytes
+        mx.mx_quantise(bf16(1, 5, 66)[:, 1:65], 3, global_scale=new, out=out)
+    assert out.global_scale is old and torch.equal(out.codes, codes)
+    assert mx.mx_quantise(x, 3, global_scale=new, out=out) is out
+    assert out.global_scale is new and same(out, mx.mx_quantise(x, 3, global_scale=new))
+    rows, _ = mx.mx_add_rmsnorm(x, None, gain, 1e-6, 3, out=out)
+    assert rows is out and out.global_scale is None
