@@ -213,8 +213,11 @@ struct Rows {
   at::Tensor codes_t, scales_t;  // what is held while the call runs
 };
 
+// (Widths that the C calls' 32 bits do not hold are refused here, before they are cut to them.)
 void widths(int64_t fmt, int64_t cols, int64_t* code_bytes, int64_t* pitch) {
-  *code_bytes = fmt < 0 || fmt > 3 ? 0 : static_cast<int64_t>(moe_mx_code_bytes(static_cast<int32_t>(fmt), cols));
+  *code_bytes = fmt < 0 || fmt > 3 || cols > INT32_MAX
+                    ? 0
+                    : static_cast<int64_t>(moe_mx_code_bytes(static_cast<int32_t>(fmt), cols));
   if (*code_bytes == 0) throw Failed{MOE_ERR_UNSUPPORTED, "moe_mx_code_bytes"};
   *pitch = static_cast<int64_t>(moe_mx_scale_pitch(static_cast<int32_t>(fmt), cols));
 }
@@ -306,6 +309,7 @@ const int32_t* positions_of(PyObject* o, int64_t n, int dev, int64_t* k) {
   const at::Tensor& t = tensor(o, "positions");
   two_dims(t, "positions");
   *k = t.size(1);
+  if (*k > INT32_MAX) throw Failed{MOE_ERR_UNSUPPORTED, "positions"};
   return static_cast<const int32_t*>(dense(o, "positions", at::kInt, {n, *k}, dev).const_data_ptr());
 }
 
@@ -480,6 +484,7 @@ PyObject* mx_grouped_product(PyObject*, PyObject* const* args, Py_ssize_t nargs,
     same_operands(x, w);
     const at::Tensor& off = dense(c.v[2], "offsets", at::kInt, {w.num_experts + 1}, dev);
     const int64_t type = c.v[7] ? integer(c.v[7], "out_type") : MOE_MX_OUT_BF16;
+    if (type != MOE_MX_OUT_BF16 && type != MOE_MX_OUT_F16) throw Failed{MOE_ERR_INVALID_ARG, "out_type"};
     const at::ScalarType dtype = type == MOE_MX_OUT_F16 ? at::kHalf : at::kBFloat16;
     int64_t out_rows = x.n, ld = w.n_out;
     if (c.v[3]) {
@@ -560,6 +565,7 @@ PyObject* mx_layer_forward(PyObject*, PyObject* const* args, Py_ssize_t nargs, P
     const at::Tensor& ids = tensor(c.v[4], "topk_ids");
     two_dims(ids, "topk_ids");
     const int64_t k = ids.size(1);
+    if (k > INT32_MAX) throw Failed{MOE_ERR_UNSUPPORTED, "topk_ids"};
     dense(c.v[4], "topk_ids", at::kInt, {n, k}, dev);
     const at::Tensor& weight = dense(c.v[5], "topk_weight", at::kFloat, {n, k}, dev);
     const Weights gu_all = weights_of(c.v[6], dev), dn_all = weights_of(c.v[7], dev);

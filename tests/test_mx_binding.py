@@ -71,3 +71,24 @@ def test_a_refused_call_leaves_the_factor_of_out():
         with pytest.raises(ValueError, match="CUDA"):
             call()
         assert out.global_scale is old
+
+
+# ---------------------------------------------------------------- sizes past 32 bits
+
+def test_sizes_past_32_bits_are_unsupported():
+    wide = (1 << 32) + 64                    # cut to 32 bits: 64, which would be done without a word
+    x = torch.empty(1, wide, dtype=torch.bfloat16, device="meta")
+    gain = torch.empty(wide, dtype=torch.bfloat16, device="meta")
+    rows = mx.MxRows(0, wide, torch.empty(1, 2 * wide, dtype=torch.uint8, device="meta"))
+    ids = torch.empty(1, wide, dtype=torch.int32, device="meta")
+    few = torch.empty(1, 64, dtype=torch.bfloat16, device="meta")
+    for call in (lambda: mx.mx_quantise(x, 0), lambda: mx.mx_add_rmsnorm(x, None, gain, 1e-6, 0),
+                 lambda: mx.mx_dequantise(rows), lambda: mx.mx_quantise(few, 0, positions=ids),
+                 lambda: mx.mx_layer_forward(few, None, None, 0.0, ids, ids.float(), None, None)):
+        with pytest.raises(mx.MoeError):
+            call()
+    w = mx.MxWeights(0, 1, 64, 64, torch.empty(32768, dtype=torch.uint8, device="meta"))
+    r = mx.MxRows(0, 64, torch.empty(1, 128, dtype=torch.uint8, device="meta"))
+    off = torch.empty(2, dtype=torch.int32, device="meta")
+    with pytest.raises(mx.MoeError):
+        mx.mx_grouped_product(r, w, off, out_type=1 << 32)
