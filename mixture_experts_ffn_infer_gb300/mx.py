@@ -19,9 +19,17 @@ _GROUP = (0, 32, 32, 16)
 
 
 def _on(stream, fn, *args):
-    """fn on another stream than the current one: what it allocates belongs to the stream that it launches on."""
+    """fn on another stream than the current one: what it allocates belongs to the stream that it launches on.  The
+    stream (an object, or a handle; 0 is the device's default stream) is of the device of fn's first argument."""
+    at = getattr(args[0], "codes", args[0]) if args else None
+    device = getattr(at, "device", None)
+    if device is None or device.type != "cuda":
+        return fn(*args)                         # which refuses them
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError(f"stream: of {stream.device}, the tensors are on {device}")
     with torch.cuda.stream(stream):
         return fn(*args)
 

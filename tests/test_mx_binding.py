@@ -92,3 +92,72 @@ def test_sizes_past_32_bits_are_unsupported():
     off = torch.empty(2, dtype=torch.int32, device="meta")
     with pytest.raises(mx.MoeError):
         mx.mx_grouped_product(r, w, off, out_type=1 << 32)
+
+
+# ---------------------------------------------------------------- the stream argument
+
+class Here:
+    """A tensor's place, without the device."""
+
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+
+class Stream:
+    cuda_stream = 77
+
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+
+@pytest.fixture
+def made(monkeypatch):
+    """Streams that _on makes and makes current, by fakes of torch's."""
+    import contextlib
+    log = []
+
+    def external(handle, device=None):
+        s = Stream(0 if device is None else device.index)       # torch's default is the current device, 0 here
+        log.append(("external", handle, s.device.index))
+        return s
+
+    @contextlib.contextmanager
+    def current(s):
+        log.append(("current", s.device.index))
+        yield
+
+    monkeypatch.setattr(torch.cuda, "ExternalStream", external)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: log.append(("default", device.index)) or Stream(device.index))
+    monkeypatch.setattr(torch.cuda, "stream", current)
+    return log
+
+
+def test_a_stream_handle_is_of_the_tensors_device(made):
+    from mixture_experts_ffn_infer_gb300.mx import _on
+    for first in (Here(1), mx.MxRows(1, 64, Here(1))):
+        assert _on(4096, lambda *a: len(a), first, None) == 2
+        assert made == [("external", 4096, 1), ("current", 1)]
+        made.clear()
+
+
+def test_stream_zero_is_the_default_stream(made):
+    # (an ExternalStream of handle 0 would be a new stream of torch's pool)
+    from mixture_experts_ffn_infer_gb300.mx import _on
+    _on(0, lambda *a: None, Here(1))
+    assert made == [("default", 1), ("current", 1)]
+
+
+def test_a_stream_of_another_device_is_refused(made):
+    from mixture_experts_ffn_infer_gb300.mx import _on
+    with pytest.raises(ValueError, match="stream: of cuda:0, the tensors are on cuda:1"):
+        _on(Stream(0), lambda *a: pytest.fail("called"), Here(1))
+    assert _on(Stream(1), lambda *a: 5, Here(1)) == 5 and made == [("current", 1)]
+
+
+def test_refusals_come_with_a_stream_too():
+    with pytest.raises(ValueError, match="CUDA"):
+        mx.mx_quantise(bf16(5, 64), 1, stream=0)
+    with pytest.raises(ValueError, match="x: expected a tensor"):
+        mx.mx_quantise(None, 1, stream=0)
+    with pytest.raises(ValueError, match="CUDA"):
+        mx.mx_pack(mx.mx_rows(1, 4, 64, "cpu"), 1, stream=4096)

@@ -62,3 +62,23 @@ def test_out_gets_its_factor_with_the_rows():
     assert out.global_scale is new and same(out, mx.mx_quantise(x, 3, global_scale=new))
     rows, _ = mx.mx_add_rmsnorm(x, None, gain, 1e-6, 3, out=out)
     assert rows is out and out.global_scale is None
+
+
+# ---------------------------------------------------------------- other streams
+
+@pytest.mark.parametrize("kind", ["object", "handle", "default"])
+def test_the_stream_argument(kind):
+    x, s = bf16(1, 2000, 4096), torch.cuda.Stream()
+    want = mx.mx_quantise(x, 1)
+    torch.cuda.synchronize()
+    stream = {"object": s, "handle": s.cuda_stream, "default": 0}[kind]
+    runs_on = torch.cuda.default_stream() if kind == "default" else s
+    with torch.cuda.stream(runs_on):
+        late = torch.zeros_like(x)
+        for _ in range(20):                      # work in front, so that a call elsewhere would read the zeros
+            torch.mm(x[:, :2000], x)
+        late.copy_(x)
+    with torch.cuda.stream(torch.cuda.Stream()):  # another one is current
+        rows = mx.mx_quantise(late, 1, stream=stream)
+    torch.cuda.synchronize()
+    assert same(rows, want)
