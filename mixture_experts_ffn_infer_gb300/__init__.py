@@ -527,7 +527,7 @@ def layer_forward(hidden, gain, eps, topk_ids, topk_weight, bank, shared=None, w
 
 # ---------------------------------------------------------------- microscaled formats (mx.py, which needs torch)
 
-_MX_NAMES = ("MxRows", "MxWeights", "mx_rows", "mx_workspace", "mx_quantise", "mx_add_rmsnorm", "mx_dequantise",
+_MX_NAMES = ("MxRows", "MxWeights", "mx_rows", "mx_workspace", "mx_get_error", "mx_quantise", "mx_add_rmsnorm", "mx_dequantise",
              "mx_pack", "mx_grouped_product", "mx_grouped_swiglu", "mx_layer_forward")
 
 

@@ -71,7 +71,7 @@ def compile_binding() -> str:
     inc, _ = _torch_paths()
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     obj = os.path.join(BUILD, "mx_torch.o")
-    cmd = ["g++", "-std=c++20", "-O2", "-fPIC", "-fvisibility=hidden", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=1", "-I", INCLUDE,
+    cmd = ["g++", "-std=c++20", "-O2", "-fPIC", "-fvisibility=hidden", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=1", "-I", INCLUDE, "-I", CSRC,
            *[f"-isystem{p}" for p in (*inc, sysconfig.get_paths()["include"], cuda)], "-c", BINDING_SRC, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

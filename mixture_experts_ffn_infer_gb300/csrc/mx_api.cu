@@ -3,6 +3,10 @@
 #include <cuda_runtime.h>
 
 #include "mx.cuh"
+#include "mx_default.h"
+
+// Host code must not pass the symbol itself on: it only names a stand-in there (moe_mx_default_workspace).
+static __device__ __align__(256) uint8_t mx_default_ws[MOE_MX_PRODUCT_WORKSPACE];
 
 namespace moe {
 namespace {
@@ -98,6 +102,91 @@ bool layer_layout(const moe_mx_weights* gu, const moe_mx_weights* dn, int32_t k,
 template <typename T>
 T* ws_at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
+}
+
+// moe_mx_layer_forward; the errors go to *err, or to the workspace's word, set back first, where it is null.
+moe_status layer_forward(const moe_mx_weights* gu, const moe_mx_weights* dn, int32_t top_k, int64_t n, const void* x,
+                         const void* residual, const void* gain, float eps, const int32_t* topk_ids,
+                         const float* topk_weight, const float* x_global, const float* h_global, void* sum, void* out,
+                         int32_t out_is_fp32, void* ws, size_t ws_bytes, uint32_t* err, cudaStream_t s) {
+  if (!gu || !dn || n < 0) return MOE_ERR_INVALID_ARG;
+  LayerLayout L;
+  if (!layer_layout(gu, dn, top_k, n, &L)) return MOE_ERR_UNSUPPORTED;
+  if (!ws || !is_aligned(ws, 256) || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (n == 0) return MOE_OK;
+  if (!x || !topk_ids || !topk_weight || !out || !is_aligned(x, 16) || !is_aligned(out, 16) || !gu->packed ||
+      !dn->packed || !is_aligned(gu->packed, 16) || !is_aligned(dn->packed, 16))
+    return MOE_ERR_INVALID_ARG;
+  if (gain ? (!sum || !is_aligned(sum, 16) || !is_aligned(gain, 16) || !(eps >= 0.f) ||
+              (residual && !is_aligned(residual, 16)))
+           : (sum || residual))
+    return MOE_ERR_INVALID_ARG;
+  const int32_t f = gu->format, d = gu->k, R = static_cast<int32_t>(n * top_k);
+  const bool reset = err == nullptr;
+  if (reset) err = static_cast<uint32_t*>(ws);
+  int32_t* offsets = ws_at<int32_t>(ws, L.offsets);
+  int32_t* sorted_pos = ws_at<int32_t>(ws, L.sorted_pos);
+  int32_t* inv_pos = ws_at<int32_t>(ws, L.inv_pos);
+  if (launch_route_permute(topk_ids, static_cast<int32_t>(n), top_k, gu->num_experts, ws_at<int32_t>(ws, L.counts),
+                           offsets, sorted_pos, inv_pos, 0, ws_at<int32_t>(ws, L.route), err, 0, nullptr, nullptr, s,
+                           reset) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  MxRowsLaunch a{};
+  a.n = n;
+  a.k = top_k;
+  a.d = d;
+  a.x = static_cast<const uint16_t*>(x);
+  a.x_ld = d;
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.r_ld = d;
+  a.gain = static_cast<const uint16_t*>(gain);
+  a.eps = eps;
+  a.positions = inv_pos;
+  a.global = x_global;
+  a.out_rows = R;
+  a.sum = static_cast<uint16_t*>(sum);
+  a.codes = ws_at<uint8_t>(ws, L.x_codes);
+  a.scales = ws_at<uint8_t>(ws, L.x_scales);
+  a.late = 1;
+  if (launch_mx_rows(f, a, s) != cudaSuccess) return MOE_ERR_CUDA;
+
+  MxProductLaunch g{};
+  g.w = gu;
+  g.rows = R;
+  g.x_codes = a.codes;
+  g.x_scales = a.scales;
+  g.x_global = x_global;
+  g.offsets = offsets;
+  g.h_global = h_global;
+  g.h_codes = ws_at<uint8_t>(ws, L.h_codes);
+  g.h_scales = ws_at<uint8_t>(ws, L.h_scales);
+  g.err = err;
+  g.num_sms = device_sms();
+  g.next = dn;
+  g.early = true;  // the routing plan was complete before the rows' kernel began
+  if (g.num_sms <= 0 || launch_mx_product(g, s) != cudaSuccess) return MOE_ERR_CUDA;
+
+  MxProductLaunch q{};
+  q.w = dn;
+  q.rows = R;
+  q.x_codes = g.h_codes;
+  q.x_scales = g.h_scales;
+  q.x_global = h_global;
+  q.offsets = offsets;
+  q.out = ws_at<void>(ws, L.rows);
+  q.out_f16 = 1;
+  q.out_rows = R;
+  q.out_ld = d;
+  q.out_pos = sorted_pos;
+  q.row_weight = topk_weight;
+  q.err = err;
+  q.num_sms = g.num_sms;
+  q.early = true;
+  if (launch_mx_product(q, s) != cudaSuccess) return MOE_ERR_CUDA;
+  return launch_combine(static_cast<const uint16_t*>(q.out), nullptr, static_cast<const uint16_t*>(sum),
+                        static_cast<int32_t>(n), top_k, d, out, out_is_fp32, s) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -273,83 +362,28 @@ moe_status moe_mx_layer_forward(const moe_mx_weights* gu, const moe_mx_weights* 
                                 const int32_t* topk_ids, const float* topk_weight, const float* x_global,
                                 const float* h_global, void* sum, void* out, int32_t out_is_fp32, void* ws,
                                 size_t ws_bytes, cudaStream_t s) {
+  return layer_forward(gu, dn, top_k, n, x, residual, gain, eps, topk_ids, topk_weight, x_global, h_global, sum, out,
+                       out_is_fp32, ws, ws_bytes, nullptr, s);
+}
+
+// ---------------------------------------------------------------- calls without a workspace (mx_default.h)
+
+void* moe_mx_default_workspace(void) {
+  void* p = nullptr;
+  return cudaGetSymbolAddress(&p, mx_default_ws) == cudaSuccess ? p : nullptr;
+}
+
+moe_status moe_mx_layer_forward_default(const moe_mx_weights* gu, const moe_mx_weights* dn, int32_t top_k, int64_t n,
+                                        const void* x, const void* residual, const void* gain, float eps,
+                                        const int32_t* topk_ids, const float* topk_weight, const float* x_global,
+                                        const float* h_global, void* sum, void* out, int32_t out_is_fp32, void* ws,
+                                        size_t ws_bytes, cudaStream_t s) {
   if (!gu || !dn || n < 0) return MOE_ERR_INVALID_ARG;
-  LayerLayout L;
-  if (!layer_layout(gu, dn, top_k, n, &L)) return MOE_ERR_UNSUPPORTED;
-  if (!ws || !is_aligned(ws, 256) || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   if (n == 0) return MOE_OK;
-  if (!x || !topk_ids || !topk_weight || !out || !is_aligned(x, 16) || !is_aligned(out, 16) || !gu->packed ||
-      !dn->packed || !is_aligned(gu->packed, 16) || !is_aligned(dn->packed, 16))
-    return MOE_ERR_INVALID_ARG;
-  if (gain ? (!sum || !is_aligned(sum, 16) || !is_aligned(gain, 16) || !(eps >= 0.f) ||
-              (residual && !is_aligned(residual, 16)))
-           : (sum || residual))
-    return MOE_ERR_INVALID_ARG;
-  const int32_t f = gu->format, d = gu->k, R = static_cast<int32_t>(n * top_k);
-  uint32_t* err = static_cast<uint32_t*>(ws);
-  int32_t* offsets = ws_at<int32_t>(ws, L.offsets);
-  int32_t* sorted_pos = ws_at<int32_t>(ws, L.sorted_pos);
-  int32_t* inv_pos = ws_at<int32_t>(ws, L.inv_pos);
-  if (launch_route_permute(topk_ids, static_cast<int32_t>(n), top_k, gu->num_experts, ws_at<int32_t>(ws, L.counts),
-                           offsets, sorted_pos, inv_pos, 0, ws_at<int32_t>(ws, L.route), err, 0, nullptr, nullptr,
-                           s) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  MxRowsLaunch a{};
-  a.n = n;
-  a.k = top_k;
-  a.d = d;
-  a.x = static_cast<const uint16_t*>(x);
-  a.x_ld = d;
-  a.residual = static_cast<const uint16_t*>(residual);
-  a.r_ld = d;
-  a.gain = static_cast<const uint16_t*>(gain);
-  a.eps = eps;
-  a.positions = inv_pos;
-  a.global = x_global;
-  a.out_rows = R;
-  a.sum = static_cast<uint16_t*>(sum);
-  a.codes = ws_at<uint8_t>(ws, L.x_codes);
-  a.scales = ws_at<uint8_t>(ws, L.x_scales);
-  a.late = 1;
-  if (launch_mx_rows(f, a, s) != cudaSuccess) return MOE_ERR_CUDA;
-
-  MxProductLaunch g{};
-  g.w = gu;
-  g.rows = R;
-  g.x_codes = a.codes;
-  g.x_scales = a.scales;
-  g.x_global = x_global;
-  g.offsets = offsets;
-  g.h_global = h_global;
-  g.h_codes = ws_at<uint8_t>(ws, L.h_codes);
-  g.h_scales = ws_at<uint8_t>(ws, L.h_scales);
-  g.err = err;
-  g.num_sms = device_sms();
-  g.next = dn;
-  g.early = true;  // the routing plan was complete before the rows' kernel began
-  if (g.num_sms <= 0 || launch_mx_product(g, s) != cudaSuccess) return MOE_ERR_CUDA;
-
-  MxProductLaunch q{};
-  q.w = dn;
-  q.rows = R;
-  q.x_codes = g.h_codes;
-  q.x_scales = g.h_scales;
-  q.x_global = h_global;
-  q.offsets = offsets;
-  q.out = ws_at<void>(ws, L.rows);
-  q.out_f16 = 1;
-  q.out_rows = R;
-  q.out_ld = d;
-  q.out_pos = sorted_pos;
-  q.row_weight = topk_weight;
-  q.err = err;
-  q.num_sms = g.num_sms;
-  q.early = true;
-  if (launch_mx_product(q, s) != cudaSuccess) return MOE_ERR_CUDA;
-  return launch_combine(static_cast<const uint16_t*>(q.out), nullptr, static_cast<const uint16_t*>(sum),
-                        static_cast<int32_t>(n), top_k, d, out, out_is_fp32, s) == cudaSuccess
-             ? MOE_OK
-             : MOE_ERR_CUDA;
+  uint32_t* err = static_cast<uint32_t*>(moe_mx_default_workspace());
+  if (!err) return MOE_ERR_CUDA;
+  return layer_forward(gu, dn, top_k, n, x, residual, gain, eps, topk_ids, topk_weight, x_global, h_global, sum, out,
+                       out_is_fp32, ws, ws_bytes, err, s);
 }
 
 }  // extern "C"

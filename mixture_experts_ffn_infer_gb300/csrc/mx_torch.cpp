@@ -11,7 +11,6 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_strided.h>
-#include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -20,7 +19,7 @@
 #include <sstream>
 #include <string>
 
-#include "moe_mx.h"
+#include "mx_default.h"
 
 namespace {
 
@@ -458,11 +457,23 @@ Weights weights_of(PyObject* o, int dev) {
   return all;
 }
 
-at::Tensor workspace_of(PyObject* o, const at::Tensor& like, int dev) {
-  if (!o) return at::zeros({static_cast<int64_t>(MOE_MX_PRODUCT_WORKSPACE)}, like.options().dtype(at::kByte));
+// The caller's workspace.
+at::Tensor workspace_of(PyObject* o, int dev) {
   const at::Tensor& t = tensor(o, "ws");
   if (t.get_device() != dev || !t.is_contiguous()) refuse("ws", "contiguous bytes on device " + std::to_string(dev), t);
   return t;
+}
+
+// A product's: the caller's, or the one that the library keeps for the current device (mx_get_error reads its word).
+struct Workspace {
+  void* at;
+  size_t bytes;
+  at::Tensor held;
+};
+Workspace product_workspace(PyObject* o, int dev) {
+  if (!o) return Workspace{moe_mx_default_workspace(), MOE_MX_PRODUCT_WORKSPACE, at::Tensor()};
+  const at::Tensor t = workspace_of(o, dev);
+  return Workspace{t.data_ptr(), t.nbytes(), t};
 }
 
 void same_operands(const Rows& x, const moe_mx_weights& w) {
@@ -500,7 +511,7 @@ PyObject* mx_grouped_product(PyObject*, PyObject* const* args, Py_ssize_t nargs,
     const float* weight = values(c.v[5], "row_weight", out_rows, dev);
     const cudaStream_t s = stream_of(dev);
     const c10::cuda::CUDAGuard on(x.codes_t.device());
-    const at::Tensor ws = workspace_of(c.v[6], x.codes_t, dev);
+    const Workspace ws = product_workspace(c.v[6], dev);
     at::Tensor out;
     if (c.v[3]) {
       out = tensor(c.v[3], "out");
@@ -513,7 +524,7 @@ PyObject* mx_grouped_product(PyObject*, PyObject* const* args, Py_ssize_t nargs,
     call("moe_mx_grouped_product", [&] {
       return moe_mx_grouped_product(&w, x.n, x.codes, x.scales, g, static_cast<const int32_t*>(off.const_data_ptr()),
                                     out.data_ptr(), static_cast<int32_t>(type), out_rows, ld, pos, weight,
-                                    ws.data_ptr(), ws.nbytes(), s);
+                                    ws.at, ws.bytes, s);
     });
     return c.v[3] ? Py_NewRef(c.v[3]) : THPVariable_Wrap(out);
   });
@@ -539,10 +550,10 @@ PyObject* mx_grouped_swiglu(PyObject*, PyObject* const* args, Py_ssize_t nargs, 
     Target t;
     target(&t, w.format, x.n, w.n_out, 0, c.v[3], c.v[4], x.codes_t, dev);
     if (t.r.n != x.n) throw Refused{"out: of another number of rows"};
-    const at::Tensor ws = workspace_of(c.v[5], x.codes_t, dev);
+    const Workspace ws = product_workspace(c.v[5], dev);
     call("moe_mx_grouped_swiglu", [&] {
       return moe_mx_grouped_swiglu(&w, x.n, x.codes, x.scales, g, static_cast<const int32_t*>(off.const_data_ptr()), hg,
-                  t.r.codes, t.r.scales, ws.data_ptr(), ws.nbytes(), s);
+                  t.r.codes, t.r.scales, ws.at, ws.bytes, s);
     });
     return t.take();
   });
@@ -578,7 +589,7 @@ PyObject* mx_layer_forward(PyObject*, PyObject* const* args, Py_ssize_t nargs, P
     const c10::cuda::CUDAGuard on(x.device());
     at::Tensor ws;
     if (c.v[10]) {
-      ws = workspace_of(c.v[10], x, dev);
+      ws = workspace_of(c.v[10], dev);
     } else {
       const size_t bytes = moe_mx_layer_workspace_size(&gu, &dn, static_cast<int32_t>(k), n);
       if (bytes == 0) throw Failed{MOE_ERR_UNSUPPORTED, "moe_mx_layer_workspace_size"};
@@ -588,7 +599,8 @@ PyObject* mx_layer_forward(PyObject*, PyObject* const* args, Py_ssize_t nargs, P
     if (gain) sum = at::empty({n, d}, x.options());
     const at::Tensor out = at::empty({n, d}, fp32 ? x.options().dtype(at::kFloat) : x.options());
     call("moe_mx_layer_forward", [&] {
-      return moe_mx_layer_forward(&gu, &dn, static_cast<int32_t>(k), n, x.const_data_ptr(), res, gain, eps,
+      return (c.v[10] ? moe_mx_layer_forward : moe_mx_layer_forward_default)(
+                  &gu, &dn, static_cast<int32_t>(k), n, x.const_data_ptr(), res, gain, eps,
                   static_cast<const int32_t*>(ids.const_data_ptr()),
                   static_cast<const float*>(weight.const_data_ptr()), xg, hg, gain ? sum.data_ptr() : nullptr,
                   out.data_ptr(), fp32, ws.data_ptr(), ws.nbytes(), s);
@@ -604,6 +616,20 @@ PyObject* mx_layer_forward(PyObject*, PyObject* const* args, Py_ssize_t nargs, P
     PyTuple_SET_ITEM(both, 0, sum_o);
     PyTuple_SET_ITEM(both, 1, out_o);
     return both;
+  });
+}
+
+// default_error(): moe_get_error of the current device's own workspace.
+PyObject* default_error(PyObject*, PyObject*) {
+  return guarded([&]() -> PyObject* {
+    void* const ws = moe_mx_default_workspace();
+    if (!ws) throw Failed{MOE_ERR_CUDA, "moe_mx_default_workspace"};
+    const cudaStream_t s = c10::cuda::getCurrentCUDAStream().stream();
+    moe_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = moe_get_error(ws, s);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
   });
 }
 
@@ -623,6 +649,7 @@ PyObject* setup(PyObject* self, PyObject* args) {
 
 PyMethodDef methods[] = {
     {"setup", setup, METH_VARARGS, nullptr},
+    {"default_error", default_error, METH_NOARGS, nullptr},
     MX_CALL(mx_quantise,
             "mx_quantise(x, fmt, positions=None, out_rows=None, global_scale=None, out=None, stream=None) -> MxRows\n\n"
             "bf16 rows x [n, d] (any row stride that is a multiple of 8) into a format; row t goes to each of\n"
@@ -639,15 +666,20 @@ PyMethodDef methods[] = {
             "                   out_type=MOE_MX_OUT_BF16, stream=None)\n\n"
             "out[p(r)] = row_weight[p(r)] * x[r] W_e^T for the rows offsets[e] .. offsets[e + 1] - 1 of each expert e;\n"
             "p = out_pos (int32 [rows], default r).  A new out has rows on 32-byte boundaries (its row stride is n_out\n"
-            "rounded up to 16)."),
+            "rounded up to 16).  Rows of no expert are left as they are, all of them where the offsets do not ascend within\n"
+            "the rows of x; in a new out they are uninitialised.  Device errors: moe_get_error(ws), mx_get_error() where no\n"
+            "ws is given."),
     MX_CALL(mx_grouped_swiglu,
             "mx_grouped_swiglu(x, w, offsets, h_global=None, out=None, ws=None, stream=None) -> MxRows\n\n"
-            "Rows of silu(x Wg_e^T) * (x Wu_e^T) in the format of x."),
+            "Rows of silu(x Wg_e^T) * (x Wu_e^T) in the format of x.  Rows of no expert and device errors as in\n"
+            "mx_grouped_product."),
     MX_CALL(mx_layer_forward,
             "mx_layer_forward(x, residual, gain, eps, topk_ids, topk_weight, gate_up, down, x_global=None,\n"
             "                 h_global=None, ws=None, out_is_fp32=False, stream=None) -> (sum, out)\n\n"
             "The MoE block on microscaled experts: sum = bf16(x + residual), out = sum + the routed experts on\n"
-            "rmsnorm(sum); with gain None (and residual None) (None, the routed experts on x)."),
+            "rmsnorm(sum); with gain None (and residual None) (None, the routed experts on x).  Device errors (ids outside\n"
+            "the experts, whose tokens' out rows are unspecified; expert rows beyond f16's range): moe_get_error(ws),\n"
+            "mx_get_error() where no ws is given."),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef definition = {PyModuleDef_HEAD_INIT, "_mx_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -355,7 +355,7 @@ int64_t route_scratch_ints(int64_t R, int32_t E) {
 cudaError_t launch_route_permute(const int32_t* ids, int32_t n, int32_t k, int32_t E, int32_t* counts,
                                  int32_t* offsets, int32_t* sorted_pos, int32_t* inv_pos, int32_t validate,
                                  int32_t* scratch, uint32_t* err, int32_t ntok, TileDesc* tiles, int32_t* n_tiles,
-                                 cudaStream_t s) {
+                                 cudaStream_t s, bool reset_err) {
   if (n <= 0) return cudaSuccess;
   const int64_t R = static_cast<int64_t>(n) * k;
   if (R <= kSingleCtaEntries) {
@@ -365,13 +365,13 @@ cudaError_t launch_route_permute(const int32_t* ids, int32_t n, int32_t k, int32
     if (e != cudaSuccess) return e;
     // dependent launch: placed while the previous kernel in the stream drains; it waits for it
     return launch_maybe_overlapped(route_permute_kernel, 1, kThreads, smem, s, true, ids, n, k, E, counts, offsets,
-                                   sorted_pos, inv_pos, validate, 1, err, ntok, tiles, n_tiles);
+                                   sorted_pos, inv_pos, validate, static_cast<int32_t>(reset_err), err, ntok, tiles, n_tiles);
   }
   if (!scratch) return cudaErrorInvalidValue;
   const int chunks = static_cast<int>((R + kChunkEntries - 1) / kChunkEntries);
   const size_t smem = sizeof(int32_t) * static_cast<size_t>(kChunkWarps) * E;
-  cudaError_t e = cudaMemsetAsync(err, 0, sizeof(uint32_t), s);  // a new routing plan starts a new error record
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (reset_err && (e = cudaMemsetAsync(err, 0, sizeof(uint32_t), s)) != cudaSuccess) return e;  // a new error record
   route_count_kernel<<<chunks, kChunkThreads, smem, s>>>(ids, n, k, E, validate, scratch, err);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   route_scan_kernel<<<1, kThreads, 0, s>>>(scratch, chunks, E, counts, offsets, ntok, tiles, n_tiles);

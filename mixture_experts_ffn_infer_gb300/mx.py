@@ -88,6 +88,14 @@ def mx_workspace(device="cuda"):
     return torch.zeros(MOE_MX_PRODUCT_WORKSPACE, dtype=_U8, device=device)
 
 
+def mx_get_error(device=None) -> int:
+    """The first error (MOE_ERR_*) that the device recorded in calls without a workspace since the last time, MOE_OK if
+    none; waits for the device.  (Calls with a workspace record theirs in it: moe_get_error.)"""
+    torch.cuda.synchronize(device)
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return _mx_torch.default_error()
+
+
 def _check_rows(r: MxRows, like=None):
     """Rows that are what their format and width say (and what `like` is)."""
     want = mx_rows(r.fmt, r.codes.shape[0], r.cols, "meta")

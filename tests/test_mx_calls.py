@@ -82,3 +82,82 @@ def test_the_stream_argument(kind):
         rows = mx.mx_quantise(late, 1, stream=stream)
     torch.cuda.synchronize()
     assert same(rows, want)
+
+
+# ---------------------------------------------------------------- errors where no workspace is given
+
+def weights(fmt, E, n_out, k, seed, up=False):
+    mats = [mx.mx_quantise(bf16(seed + i, E * n_out, k) * 0.05, fmt) for i in range(1 + up)]
+    return mx.mx_pack(mats[0], E, up=mats[1] if up else None)
+
+
+def offsets(*o):
+    return torch.tensor(o, dtype=torch.int32, device="cuda")
+
+
+@pytest.fixture
+def clean():
+    mx.mx_get_error()
+    yield
+    assert mx.mx_get_error() == mx.MOE_OK                       # each test read what it caused
+
+
+@pytest.mark.parametrize("bad", [(0, 5, 3, 8), (-1, 2, 4, 8), (0, 2, 4, 9)])
+def test_bad_offsets_are_reported_without_a_workspace(clean, bad):
+    x = mx.mx_quantise(bf16(1, 8, 64), 1)
+    mx.mx_grouped_product(x, weights(1, 3, 64, 64, 2), offsets(*bad))
+    assert mx.mx_get_error() == 4 and mx.mx_get_error() == 0    # MOE_ERR_ROUTING, once
+    mx.mx_grouped_swiglu(x, weights(1, 3, 64, 64, 2, up=True), offsets(*bad))
+    assert mx.mx_get_error("cuda:0") == 4
+
+
+def test_errors_stay_until_they_are_read(clean):
+    x, w = mx.mx_quantise(bf16(1, 8, 64), 1), weights(1, 1, 64, 64, 2)
+    good = mx.mx_grouped_product(x, w, offsets(0, 8))
+    assert mx.mx_get_error() == 0
+    s = torch.cuda.Stream()
+    mx.mx_grouped_product(x, w, offsets(0, 9), stream=s)        # on another stream, then good calls
+    assert torch.equal(mx.mx_grouped_product(x, w, offsets(0, 8)), good)
+    ws = mx.mx_workspace()
+    mx.mx_grouped_product(x, w, offsets(0, 9), ws=ws)
+    assert mx.mx_get_error() == 4 and mx.moe_get_error(ws) == 4
+
+
+def test_values_beyond_f16_are_reported_without_a_workspace(clean):
+    big = mx.mx_quantise(torch.full((4, 256), 300.0, device="cuda").to(torch.bfloat16), 0)
+    w = mx.mx_pack(mx.mx_quantise(torch.full((32, 256), 300.0, device="cuda").to(torch.bfloat16), 0), 1)
+    mx.mx_grouped_product(big, w, offsets(0, 4), out_type=mx.MOE_MX_OUT_F16)
+    assert mx.mx_get_error() == 6
+
+
+@pytest.mark.parametrize("n", [40, 5000])                        # the routing plan in one kernel, and in several
+def test_layer_errors_without_a_workspace(clean, n):
+    d, f, E, k = 128, 64, 4, 2
+    gate_up, down = weights(1, E, f, d, 1, up=True), weights(1, E, d, f, 3)
+    x, r, gain, w = bf16(4, n, d), bf16(5, n, d), bf16(6, d), torch.full((n, k), 0.5, device="cuda")
+    ids = torch.rand(n, E, generator=torch.Generator().manual_seed(7)).topk(k, 1).indices.to(torch.int32).cuda()
+    call = lambda i, **kw: mx.mx_layer_forward(x, r, gain, 1e-6, i, w, gate_up, down, **kw)[1]
+    good = call(ids)
+    assert mx.mx_get_error() == 0
+    bad = ids.clone()
+    bad[3, 1] = E
+    out = call(bad)
+    others = [t for t in range(n) if t != 3]
+    assert torch.equal(out[others], good[others])
+    assert torch.equal(call(ids), good)                          # a good call leaves the error
+    assert mx.mx_get_error() == 4
+    ws = torch.full((1 << 24,), 0xFF, dtype=torch.uint8, device="cuda")
+    assert torch.equal(call(ids, ws=ws), good) and mx.moe_get_error(ws) == 0   # the word is reset there
+
+
+def test_captured_calls_without_a_workspace(clean):
+    x, w, off = mx.mx_quantise(bf16(1, 8, 64), 1), weights(1, 1, 64, 64, 2), offsets(0, 8)
+    want = mx.mx_grouped_product(x, w, off)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = mx.mx_grouped_product(x, w, off)
+    graph.replay()
+    assert mx.mx_get_error() == 0 and torch.equal(out, want)
+    off.copy_(offsets(0, 9))
+    graph.replay()
+    assert mx.mx_get_error() == 4
