@@ -7,7 +7,9 @@ library with a static CUDA runtime.  The driver API is reached through
 
 Beside it goes ``_mx_torch``, the Python module of the microscaled-format calls
 on torch tensors (``csrc/mx_torch.cpp``): host code, compiled with g++ against
-torch's headers and linked to the library.
+torch's headers and linked to the library.  Where g++, Python's headers or
+torch's are not installed the library is built without it; it is built again
+when another torch is installed.
 
     python -m mixture_experts_ffn_infer_gb300.build [--force] [--verbose]
 """
@@ -16,6 +18,8 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -30,6 +34,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_ffn.so")
 BINDING = os.path.join(HERE, "_mx_torch" + sysconfig.get_config_var("EXT_SUFFIX"))
 BINDING_SRC = os.path.join(CSRC, "mx_torch.cpp")
+BINDING_FOR = "mx_torch.for"  # in BUILD: what the module was compiled against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
@@ -47,24 +52,58 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _deps():
-    return sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
-        os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [BINDING_SRC, os.path.abspath(__file__)]
+def _headers():
+    return [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
+        os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [os.path.abspath(__file__)]
+
+
+def _newer(made: str, deps) -> bool:
+    return os.path.exists(made) and all(os.path.getmtime(p) <= os.path.getmtime(made) for p in deps)
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, sources() + _headers())
+
+
+def binding_up_to_date() -> bool:
+    if not _newer(BINDING, [LIB, BINDING_SRC] + _headers()):
+        return False
+    try:
+        with open(os.path.join(BUILD, BINDING_FOR)) as f:
+            return f.read() == _torch_version()
+    except FileNotFoundError:
+        return False
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return library_up_to_date() and (binding_lacks() is not None or binding_up_to_date())
+
+
+def _torch_version() -> str:
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # not installed as a package: told apart by its place
+        return importlib.util.find_spec("torch").origin
 
 
 def _torch_paths():
     """(include directories, library directory) of the installed torch."""
-    import torch
-    root = os.path.dirname(os.path.abspath(torch.__file__))
+    root = os.path.dirname(os.path.abspath(importlib.util.find_spec("torch").origin))
     inc = os.path.join(root, "include")
     return [inc, os.path.join(inc, "torch", "csrc", "api", "include")], os.path.join(root, "lib")
+
+
+def binding_lacks() -> str | None:
+    """What the torch module cannot be built without and is not installed here, or None."""
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    if not os.path.exists(os.path.join(_torch_paths()[0][0], "ATen", "core", "Tensor.h")):
+        return "torch's headers"
+    if not os.path.exists(os.path.join(_torch_paths()[1], "libc10_cuda.so")):
+        return "a torch with CUDA"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers"
+    return None if shutil.which("g++") else "g++"
 
 
 def compile_binding() -> str:
@@ -88,12 +127,31 @@ def link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(os.path.join(BUILD, BINDING_FOR), "w") as f:
+        f.write(_torch_version())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
+    lacks = binding_lacks()
+    library = force or not library_up_to_date()
+    module = lacks is None and (library or not binding_up_to_date())
+    if not library and not module:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(compile_binding) if module else None  # the longest: first
+        if library:
+            build_library(verbose)
+        if binding:
+            link_binding(binding.result())
+        else:
+            print(f"built without the calls on torch tensors (mx.py): {lacks} not found", file=sys.stderr)
+            if os.path.exists(BINDING):
+                os.remove(BINDING)  # of the library before this one
+    return LIB
+
+
+def build_library(verbose: bool = False) -> None:
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if verbose else []
 
@@ -106,9 +164,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj, r.stdout + r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        binding = ex.submit(compile_binding)  # the longest: first
         results = list(ex.map(compile_one, sources()))
-        binding = binding.result()
     if verbose:
         for _, log in results:
             if log.strip():
@@ -120,8 +176,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    link_binding(binding)
-    return LIB
 
 
 if __name__ == "__main__":

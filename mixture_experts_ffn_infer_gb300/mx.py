@@ -10,8 +10,13 @@ import torch
 
 from . import MOE_MX_PRODUCT_WORKSPACE, MoeError, load_library, moe_mx_pack_weights, moe_mx_packed_bytes, moe_mx_weights
 
-load_library()          # says what to build where it is missing; the module below links to it
-from . import _mx_torch  # noqa: E402
+load_library()  # says what to build where it is missing; the module below links to it
+try:
+    from . import _mx_torch
+except ImportError as e:
+    raise ImportError("the module of the calls on torch tensors is missing or does not fit this torch; build it with "
+                      "`python -m mixture_experts_ffn_infer_gb300.build` (which needs g++ and the headers of Python and "
+                      "torch)") from e
 
 _U8 = torch.uint8
 _BITS = (16, 8, 4, 4)
