@@ -1,7 +1,8 @@
 // Rows into and out of the microscaled formats (moe_mx.h), and the packed
-// weight layout.  All four kernels move bytes: HBM bounds them.  Rows in and out
-// are dependent launches that wait before they read anything, so that in a
-// sequence of short calls one's launch overlaps the other's end.
+// weight layout.  All three kernels move bytes: HBM bounds them.  Rows in and out
+// are dependent launches, so that in a sequence of short calls one's launch
+// overlaps the other's end; they wait before they read anything (in the layer,
+// before the positions: MxRowsLaunch::late).
 //
 // mx_rows_kernel       - [add the residual, RMS norm,] quantise, write to each
 //                        position of the token.  One CTA per token, or one
@@ -82,9 +83,12 @@ __device__ __forceinline__ void store_codes(const MxRowsLaunch& a, int64_t pos, 
 
 // ---------------------------------------------------------------- the sum of squares
 // A code of 2 to 4 bits turns a difference in y's last bit into a step of a quarter where y
-// lies on a rounding border, and the norm's factor moves a whole row's.  So the row's sum is
-// carried over lanes and warps as a sum of two floats: whatever the order, it is the same to
-// the last bit (but for the threads' own few squares).
+// lies on a rounding border, and the norm's factor moves a whole row's.  The 16 squares of a piece
+// are summed in fp32, always in the same order (four sums of every fourth); the pieces' sums are
+// joined over a thread's pieces, lanes and warps as sums of two floats.  Those carry some 47 bits,
+// so the rounded sum, and with it a token's rows, does not depend on how many tokens come with it
+// (which decides the pieces a thread holds), unless it lies within 2^-44 of the middle between two
+// floats.
 
 struct Pair {
   float hi, lo;
@@ -106,11 +110,10 @@ __device__ __forceinline__ Pair warp_sum_pair(Pair v) {
   return v;
 }
 // ITER passes of blockDim.x pieces cover the row, held as the bf16 pairs they are
-// read as (the stored sum is bf16 too).  The sum of squares is taken per thread in
-// column order, then by shuffles, then over the warps.
+// read as (the stored sum is bf16 too).
 template <int FMT, bool NORM, int ITER, bool WARP>
-// (Two passes: five CTAs an SM with a few spilled words were faster than four without, 355 us against 369 for
-// 32,768 rows of 7168 to MXFP8 and back; 345 us since.)
+// (Two passes: five CTAs an SM, at 48 registers, were faster than four, 355 us against 369 for 32,768 rows of 7168
+// to MXFP8 and back, which take 338 now.)
 __global__ void __launch_bounds__(ITER == 1 ? kRowsMaxThreads : kRowsSplitThreads, ITER == 1 ? 1 : ITER == 2 ? 5 : 2)
 mx_rows_kernel(const MxRowsLaunch a) {
   __shared__ Pair part[32];
@@ -150,7 +153,7 @@ mx_rows_kernel(const MxRowsLaunch a) {
   const float global_early = gp ? __ldg(gp) : 1.f;
   float rs = 1.f;
   if constexpr (NORM) {
-    float sq[4] = {0.f, 0.f, 0.f, 0.f};
+    Pair mine{0.f, 0.f};
     if (a.residual) {
       uint32_t res[ITER][8];
 #pragma unroll
@@ -176,12 +179,14 @@ mx_rows_kernel(const MxRowsLaunch a) {
       if (a.sum && c < np) store_piece(a.sum + t * a.r_ld + kPiece * c, a.wide_r != 0, raw[it]);
       float v[16];
       unpack(raw[it], v);
+      float sq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 16; ++i) sq[i & 3] = fmaf(v[i], v[i], sq[i & 3]);
+      const Pair piece{(sq[0] + sq[1]) + (sq[2] + sq[3]), 0.f};
+      mine = it == 0 ? piece : add(mine, piece);
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = WARP ? 1 : blockDim.x >> 5;
-    // a thread's sum of a few squares is plain fp32 (the threads' roundings average out)
-    Pair ss = warp_sum_pair(Pair{(sq[0] + sq[1]) + (sq[2] + sq[3]), 0.f});
+    Pair ss = warp_sum_pair(mine);
     if (!WARP && warps > 1) {
       if (lane == 0) part[warp] = ss;
       __syncthreads();
