@@ -158,6 +158,11 @@ moe_status moe_mx_grouped_swiglu(const moe_mx_weights *w, int64_t rows, const vo
  *   E(v) = down(Q(silu(gate v) * up v))
  * i.e. moe_permute, moe_mx_add_rmsnorm to the sorted rows, moe_mx_grouped_swiglu,
  * moe_mx_grouped_product (f16 rows, weighted) and moe_combine.
+ * The norm is moe_mx_add_rmsnorm's, in fp32 until Q.  moe_layer_forward's rounds
+ * the normalised row and its product with the gain to bf16 each; on rows that are
+ * normalised that way this call, with gain NULL, is that block's routed sum.
+ * The weighted rows are f16 also where out is fp32: 2^-11 of each (2^-25 below
+ * 2^-14), and MOE_ERR_RANGE beyond 65504.
  *   gate_up, down  one format; gate_up->swiglu = 1, n_out = d_ff, k = d; down n_out = d, k = d_ff;
  *                  d a multiple of 128
  *   x, residual    [n, d] bf16;  residual may be NULL.  With gain NULL there is no norm and no residual

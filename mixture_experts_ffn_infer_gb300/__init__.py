@@ -348,7 +348,7 @@ def moe_get_error(ws, stream=None) -> int:
     return load_library().moe_get_error(_ptr(ws), _stream(stream))
 
 
-# microscaled formats
+# microscaled formats: the C ABI one to one, like the calls above (mx.py has the calls that check their tensors)
 
 def moe_mx_code_bytes(fmt: int, cols: int) -> int:
     return load_library().moe_mx_code_bytes(fmt, cols)

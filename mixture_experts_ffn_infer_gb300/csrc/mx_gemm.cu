@@ -259,7 +259,9 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
     if (clock64() - t0 > kWaitLimitCycles) return;
 }
 
-// silu(g) = g / (1 + e^-g); for g < -87 the denominator overflows and the result is 0.
+// silu(g) = g / (1 + e^-g).  By the documented bounds of the two fast functions within (5 + 1.2 |g|) 2^-23 of its
+// value; below -87 the denominator passes 2^126 and the result is 0.  (A correctly rounded division here, inlined 64
+// times, cost a single row 7.4 us of instruction fetches.)
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
 struct Unit {

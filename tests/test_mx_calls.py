@@ -161,3 +161,34 @@ def test_captured_calls_without_a_workspace(clean):
     off.copy_(offsets(0, 9))
     graph.replay()
     assert mx.mx_get_error() == 4
+
+
+# ---------------------------------------------------------------- the C ABI one to one
+
+@pytest.mark.parametrize("fmt", range(4))
+def test_the_unchecked_wrappers_do_the_same(fmt):
+    n, d, f, E = 9, 64, 96, 2
+    x, r, gain, g = bf16(1, n, d), bf16(2, n, d), bf16(3, d), torch.full((1,), 2.0**-6, device="cuda")
+    pos, off = torch.arange(n - 1, -1, -1, dtype=torch.int32, device="cuda")[:, None].contiguous(), offsets(0, 4, n)
+    new = lambda cols: mx.mx_rows(fmt, n, cols)
+    a, ws = new(d), mx.mx_workspace()
+    mx.moe_mx_quantise(fmt, n, 1, d, x, d, pos, g, n, a.codes, a.scales)
+    want = mx.mx_quantise(x, fmt, positions=pos, global_scale=g)
+    assert same(a, want)
+    back = torch.empty_like(x)
+    mx.moe_mx_dequantise(fmt, n, d, a.codes, a.scales, g, back, d)
+    assert torch.equal(back, mx.mx_dequantise(want))
+    total = torch.empty_like(x)
+    mx.moe_mx_add_rmsnorm(fmt, n, 1, d, x, d, r, d, gain, 1e-6, pos, g, n, total, a.codes, a.scales)
+    want, sums = mx.mx_add_rmsnorm(x, r, gain, 1e-6, fmt, positions=pos, global_scale=g)
+    assert same(a, want) and torch.equal(total, sums)
+    gate_up, down = weights(fmt, E, f, d, 4, up=True), weights(fmt, E, d, f, 6)
+    h = new(f)
+    mx.moe_mx_grouped_swiglu(gate_up.struct(), n, a.codes, a.scales, g, off, g, h.codes, h.scales, ws)
+    hidden = mx.mx_grouped_swiglu(want, gate_up, off, h_global=g)
+    assert same(h, hidden)
+    y = torch.empty(n, d, dtype=torch.bfloat16, device="cuda")
+    mx.moe_mx_grouped_product(down.struct(), n, h.codes, h.scales, g, off, y, mx.MOE_MX_OUT_BF16, n, d, None, None, ws)
+    assert torch.equal(y, mx.mx_grouped_product(hidden, down, off)) and mx.moe_get_error(ws) == mx.MOE_OK
+    with pytest.raises(mx.MoeError):
+        mx.moe_mx_quantise(fmt, n, 0, d, x, d, pos, g, n, a.codes, a.scales)
