@@ -56,17 +56,25 @@ constexpr int kStages = 4;
 constexpr int kTile = 128;
 constexpr int kMaxExperts = 1024;
 constexpr int kChunkTiles = 8;
-constexpr int kSplitChunks = 6;  // of a CTA, from which a cluster gains more than its exchange costs (about 2 us)
+// Chunks of a CTA from which units go to clusters.  Without / with them, us, one expert, weights that no call before has
+// read, by K: NVFP4 4096 outputs, 16 rows: 3584 (seven chunks a CTA of two) 9.3 / 9.4, 4096 10.0 / 9.7, 5120 11.4 /
+// 10.5, 7168 (seven of four) 14.3 / 10.1; MXFP8: 1536 (six of two) 8.4 / 9.0, 2048 9.7 / 9.6, 3584 (seven of four) 13.8 /
+// 10.0; bf16 2048 outputs: 1024 (eight of two) 9.2 / 9.1, 2048 (eight of four) 14.4 / 9.2, 7168 (14 of eight) 40 / 12.4;
+// 512 outputs, 100 rows: 1024 (eight of two) 8.5 / 9.3, 1536 (six of four) 12.2 / 10.2.  Two CTAs break even at seven or
+// eight chunks each, four gain from about four on (NVFP4 4096 outputs, K 4096: 8.7; 1024 outputs, K 5120: 8.4, two 10.2):
+// one number for all loses up to 0.8 us at the first and leaves up to 1.9 at the second.
+constexpr int kSplitChunks = 6;
 constexpr int kEarlyChunks = 8;  // 152 x 8 x 36 KB: 45 MB of the 129 MB L2, 6.6 us of HBM time
-// The weights' lines are the first to leave L2 where little else moves, up to kStreamRows rows an expert on average,
-// or where an expert's tiles run at the same time (kChunkTiles) and the weights are few enough for a part to stay for
-// the next call (K2 layer, NVFP4, 1 token 50.6 us, 56.5 with the normal policy; 16 experts x 7168 x 2048, 80 rows, 132
-// MB, 22.9 and 25.0; one bf16 expert x 4096 x 4096, 1000 rows, 27.4 and 29.6).  Elsewhere later tiles read them again,
-// or outputs push lines that are to leave first out before all their readers came (down product of 384 experts, 3.2
-// GB, 64 rows each 496 us with the normal policy, 520 without; layer of 256 tokens 1317 and 1347, of 4096 1616 and
-// 1655; one bf16 expert x 6093 x 480, 25,414 rows, 127 and 144; but 8 NVFP4 experts x 4096 x 4096, 16,384 rows, 122
-// and 120).
-constexpr int kStreamRows = 4;
+// The weights' lines are the first to leave L2 ("stream") where little else moves, up to kStreamRows rows an expert on
+// average, or where an expert's tiles run at the same time (kChunkTiles) and the weights are few.  Stream / normal, us,
+// weights that no call before has read: K2 layer (NVFP4, 384 experts x 7168 x 2048) of 1 token 50.8 / 57.2, of 8 226 /
+// 237, 64 962 / 967, 128 (2.7 rows an expert) 1230 / 1218, 192 1328 / 1293, 256 1350 / 1320, 4096 1649 / 1610; layer of
+// 64 experts x 4096 x 1024 of 8 tokens 69.5 / 80.1, of 128 95.8 / 106, of 512 112 / 121; NVFP4 16 experts x 7168 x 2048,
+// 80 rows 24.2 / 24.7, 2048 rows 32.8 / 34.4; one bf16 expert x 4096 x 4096, 1000 rows 26.1 / 28.4.  Elsewhere later
+// tiles read them again, or outputs push lines that are to leave first out before all their readers came (one bf16
+// expert x 6093 x 480, 25,414 rows, 142 / 125).  The rule loses where few weights meet outputs of L2's size: the 16
+// experts with 8192 rows 76.5 / 72.4.
+constexpr int kStreamRows = 2;
 constexpr int64_t kStreamBytes = int64_t(512) << 20;
 constexpr int kABytes = kTile * 128;
 constexpr uint32_t kTmemCols = 512;
