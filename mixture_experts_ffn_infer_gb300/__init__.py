@@ -66,6 +66,29 @@ MOE_MX_OUT_BF16, MOE_MX_OUT_F16 = 0, 1
 MOE_MX_PRODUCT_WORKSPACE = 256
 
 
+# the router (include/moe_router.h)
+class moe_router(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("logits_type", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("normalise", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+MOE_LOGITS_F32, MOE_LOGITS_BF16 = 0, 1
+
+
+# rows and weights in the FP8 bank's form (include/moe_fp8.h)
+class moe_fp8_weights(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("n_out", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+MOE_FP8_BLOCK = 128
+MOE_FP8_OUT_BF16, MOE_FP8_OUT_F16, MOE_FP8_OUT_F32 = range(3)
+MOE_FP8_PRODUCT_WORKSPACE = 256
+
+
 class moe_trace(ctypes.Structure):
     _fields_ = [("events", ctypes.c_void_p * MOE_TRACE_MAX), ("n_events", ctypes.c_int32),
                 ("n_recorded", ctypes.c_int32), ("labels", ctypes.c_char_p * MOE_TRACE_MAX),
@@ -141,6 +164,27 @@ _SIGS = {
                                             ctypes.c_int32, ctypes.c_int64] + [ctypes.c_void_p] * 3
                              + [ctypes.c_float] + [ctypes.c_void_p] * 6
                              + [ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_route": (ctypes.c_int, [ctypes.POINTER(moe_router), ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64]
+                  + [ctypes.c_void_p] * 4),
+    "moe_balance_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(moe_router), ctypes.c_int64, ctypes.c_int64]),
+    "moe_balance_loss": (ctypes.c_int, [ctypes.POINTER(moe_router), ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                        ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_int64]
+                         + [ctypes.c_void_p] * 3 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_route_backward": (ctypes.c_int, [ctypes.POINTER(moe_router), ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float]
+                           + [ctypes.c_void_p] * 3 + [ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                                      ctypes.c_void_p]),
+    "moe_fp8_scale_pitch": (ctypes.c_int64, [ctypes.c_int64]),
+    "moe_fp8_quantise": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                        ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64] + [ctypes.c_void_p] * 3),
+    "moe_fp8_dequantise": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32] + [ctypes.c_void_p] * 3
+                           + [ctypes.c_int64, ctypes.c_void_p]),
+    "moe_fp8_packed_bytes": (ctypes.c_size_t, [ctypes.POINTER(moe_fp8_weights)]),
+    "moe_fp8_pack_weights": (ctypes.c_int, [ctypes.POINTER(moe_fp8_weights), ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_int32] + [ctypes.c_void_p] * 3),
+    "moe_fp8_grouped_product": (ctypes.c_int, [ctypes.POINTER(moe_fp8_weights), ctypes.c_int64] + [ctypes.c_void_p] * 4
+                                + [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64] + [ctypes.c_void_p] * 3
+                                + [ctypes.c_size_t, ctypes.c_void_p]),
     "moe_check_bounded_wait": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "moe_get_error": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
 }
@@ -425,6 +469,69 @@ def moe_mx_layer_forward(gate_up: moe_mx_weights, down: moe_mx_weights, top_k, n
         raise MoeError(st, "moe_mx_layer_forward")
 
 
+# the router and the FP8 operators, one to one as well (fp8.py has the calls that check their tensors)
+
+def moe_route(r: moe_router, n_tokens, logits, logits_ld, bias, topk_ids, topk_weight, stream=None):
+    st = load_library().moe_route(ctypes.byref(r), n_tokens, _ptr(logits), logits_ld, _ptr(bias), _ptr(topk_ids),
+                                  _ptr(topk_weight), _raw_stream(stream, logits))
+    _check(st, "moe_route")
+
+
+def moe_balance_workspace_size(r: moe_router, n_tokens: int, num_sequences: int) -> int:
+    return load_library().moe_balance_workspace_size(ctypes.byref(r), n_tokens, num_sequences)
+
+
+def moe_balance_loss(r: moe_router, n_tokens, logits, logits_ld, topk_ids, coef, seq_offsets, num_sequences, counts,
+                     loss, ws, stream=None):
+    st = load_library().moe_balance_loss(ctypes.byref(r), n_tokens, _ptr(logits), logits_ld, _ptr(topk_ids), coef,
+                                         _ptr(seq_offsets), num_sequences, _ptr(counts), _ptr(loss), _ptr(ws),
+                                         ws.nbytes, _raw_stream(stream, logits))
+    _check(st, "moe_balance_loss")
+
+
+def moe_route_backward(r: moe_router, n_tokens, logits, logits_ld, topk_ids, d_weight, coef, counts, d_loss,
+                       seq_offsets, num_sequences, d_logits, d_ld, stream=None):
+    st = load_library().moe_route_backward(ctypes.byref(r), n_tokens, _ptr(logits), logits_ld, _ptr(topk_ids),
+                                           _ptr(d_weight), coef, _ptr(counts), _ptr(d_loss), _ptr(seq_offsets),
+                                           num_sequences, _ptr(d_logits), d_ld, _raw_stream(stream, logits))
+    _check(st, "moe_route_backward")
+
+
+def moe_fp8_scale_pitch(cols: int) -> int:
+    return load_library().moe_fp8_scale_pitch(cols)
+
+
+def moe_fp8_quantise(n, k, d, x, x_ld, positions, out_rows, codes, scales, stream=None):
+    st = load_library().moe_fp8_quantise(n, k, d, _ptr(x), x_ld, _ptr(positions), out_rows, _ptr(codes), _ptr(scales),
+                                         _raw_stream(stream, x))
+    _check(st, "moe_fp8_quantise")
+
+
+def moe_fp8_dequantise(rows, d, codes, scales, out, out_ld, stream=None):
+    st = load_library().moe_fp8_dequantise(rows, d, _ptr(codes), _ptr(scales), _ptr(out), out_ld,
+                                           _raw_stream(stream, out))
+    _check(st, "moe_fp8_dequantise")
+
+
+def moe_fp8_packed_bytes(w: moe_fp8_weights) -> int:
+    return load_library().moe_fp8_packed_bytes(ctypes.byref(w))
+
+
+def moe_fp8_pack_weights(w: moe_fp8_weights, codes, scales, transpose, packed, scales_out, stream=None):
+    st = load_library().moe_fp8_pack_weights(ctypes.byref(w), _ptr(codes), _ptr(scales), int(bool(transpose)),
+                                             _ptr(packed), _ptr(scales_out), _raw_stream(stream, packed))
+    _check(st, "moe_fp8_pack_weights")
+
+
+def moe_fp8_grouped_product(w: moe_fp8_weights, rows, x_codes, x_scales, expert_offsets, out, out_type, out_rows,
+                            out_ld, out_pos, row_weight, ws, stream=None):
+    st = load_library().moe_fp8_grouped_product(ctypes.byref(w), rows, _ptr(x_codes), _ptr(x_scales),
+                                                _ptr(expert_offsets), _ptr(out), out_type, out_rows, out_ld,
+                                                _ptr(out_pos), _ptr(row_weight), _ptr(ws), ws.nbytes,
+                                                _raw_stream(stream, out))
+    _check(st, "moe_fp8_grouped_product")
+
+
 # ---------------------------------------------------------------- allocating conveniences
 
 class TiledBank:
@@ -525,16 +632,23 @@ def layer_forward(hidden, gain, eps, topk_ids, topk_weight, bank, shared=None, w
     return out
 
 
-# ---------------------------------------------------------------- microscaled formats (mx.py, which needs torch)
+# ---------------------------------------------------------------- calls on torch tensors (mx.py, fp8.py, which need torch)
 
 _MX_NAMES = ("MxRows", "MxWeights", "mx_rows", "mx_workspace", "mx_get_error", "mx_quantise", "mx_add_rmsnorm", "mx_dequantise",
              "mx_pack", "mx_grouped_product", "mx_grouped_swiglu", "mx_layer_forward")
+_FP8_NAMES = ("Fp8Rows", "Fp8Weights", "fp8_rows", "fp8_quantise", "fp8_dequantise", "fp8_pack", "fp8_grouped_product", "route",
+              "balance_loss", "route_backward")
 
 
 def __getattr__(name):
-    if name not in _MX_NAMES:
+    if name in _MX_NAMES:
+        from . import mx as module
+        names = _MX_NAMES
+    elif name in _FP8_NAMES:
+        from . import fp8 as module
+        names = _FP8_NAMES
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import mx
-    for n in _MX_NAMES:
-        globals()[n] = getattr(mx, n)
+    for n in names:
+        globals()[n] = getattr(module, n)
     return globals()[name]

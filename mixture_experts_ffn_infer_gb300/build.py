@@ -5,8 +5,8 @@ arch=compute_103a,code=sm_103a``), in parallel, then linked into one shared
 library with a static CUDA runtime.  The driver API is reached through
 ``cudaGetDriverEntryPointByVersion``, so loading the library needs no GPU.
 
-Beside it goes ``_mx_torch``, the Python module of the microscaled-format calls
-on torch tensors (``csrc/mx_torch.cpp``): host code, compiled with g++ against
+Beside it goes ``_mx_torch``, the Python module of the microscaled-format, FP8
+and router calls on torch tensors (``csrc/*_torch.cpp``): host code, compiled with g++ against
 torch's headers and linked to the library.  Where g++, Python's headers or
 torch's are not installed the library is built without it; it is built again
 when another torch is installed.
@@ -33,7 +33,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_ffn.so")
 BINDING = os.path.join(HERE, "_mx_torch" + sysconfig.get_config_var("EXT_SUFFIX"))
-BINDING_SRC = os.path.join(CSRC, "mx_torch.cpp")
+BINDING_SRC = [os.path.join(CSRC, f) for f in ("mx_torch.cpp", "fp8_torch.cpp")]
 BINDING_FOR = "mx_torch.for"  # in BUILD: what the module was compiled against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -66,7 +66,7 @@ def library_up_to_date() -> bool:
 
 
 def binding_up_to_date() -> bool:
-    if not _newer(BINDING, [LIB, BINDING_SRC] + _headers()):
+    if not _newer(BINDING, [LIB, *BINDING_SRC] + _headers()):
         return False
     try:
         with open(os.path.join(BUILD, BINDING_FOR)) as f:
@@ -106,22 +106,27 @@ def binding_lacks() -> str | None:
     return None if shutil.which("g++") else "g++"
 
 
-def compile_binding() -> str:
+def compile_binding() -> list[str]:
+    with cf.ThreadPoolExecutor(max_workers=len(BINDING_SRC)) as ex:
+        return list(ex.map(_compile_host, BINDING_SRC))
+
+
+def _compile_host(src: str) -> str:
     inc, _ = _torch_paths()
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
-    obj = os.path.join(BUILD, "mx_torch.o")
+    obj = os.path.join(BUILD, os.path.basename(src)[:-4] + ".o")
     cmd = ["g++", "-std=c++20", "-O2", "-fPIC", "-fvisibility=hidden", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=1", "-I", INCLUDE, "-I", CSRC,
-           *[f"-isystem{p}" for p in (*inc, sysconfig.get_paths()["include"], cuda)], "-c", BINDING_SRC, "-o", obj]
+           *[f"-isystem{p}" for p in (*inc, sysconfig.get_paths()["include"], cuda)], "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
     return obj
 
 
-def link_binding(obj: str) -> None:
+def link_binding(objects: list[str]) -> None:
     _, lib = _torch_paths()
     tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, obj, "-Wl,--no-as-needed", LIB, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+    cmd = ["g++", "-shared", "-o", tmp, *objects, "-Wl,--no-as-needed", LIB, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
            "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -145,7 +150,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if binding:
             link_binding(binding.result())
         else:
-            print(f"built without the calls on torch tensors (mx.py): {lacks} not found", file=sys.stderr)
+            print(f"built without the calls on torch tensors (mx.py, fp8.py): {lacks} not found", file=sys.stderr)
             if os.path.exists(BINDING):
                 os.remove(BINDING)  # of the library before this one
     return LIB

@@ -128,6 +128,10 @@ cudaError_t launch_maybe_overlapped(void (*kern)(P...), int grid, int block, siz
   return cudaLaunchKernelEx(&cfg, kern, static_cast<A&&>(args)...);
 }
 
+// ---------------------------------------------------------------- api.cu
+bool encode_rows_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows);
+int device_sms();
+
 // ---------------------------------------------------------------- launchers
 // routing.cu
 // scratch: route_scratch_ints(n k, E) ints (none for small batches, which one CTA plans).

@@ -204,8 +204,4 @@ struct MxProductLaunch {
 };
 cudaError_t launch_mx_product(const MxProductLaunch& a, cudaStream_t s);
 
-// api.cu
-bool encode_rows_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows);
-int device_sms();
-
 }  // namespace moe

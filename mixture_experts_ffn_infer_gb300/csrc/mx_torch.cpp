@@ -5,191 +5,20 @@
 // tensors are checked in C++ and the C ABI is called directly.  The module holds
 // no computation: it checks arguments, allocates what a call returns and launches
 // on the current stream.
-#define PY_SSIZE_T_CLEAN
-#include <Python.h>
-
-#include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_strided.h>
-#include <c10/cuda/CUDAGuard.h>
-#include <c10/cuda/CUDAStream.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include <sstream>
-#include <string>
-
 #include "mx_default.h"
+#include "torch_args.h"
+
+// fp8_torch.cpp
+extern PyMethodDef moe_fp8_methods[];
+bool moe_fp8_names();
 
 namespace {
 
-PyObject* rows_class = nullptr;   // mx.MxRows
-PyObject* moe_error = nullptr;    // MoeError
-PyObject* on_stream = nullptr;    // mx._on
-PyObject* module_dict = nullptr;  // this module's, for a call handed to another stream
+using namespace torch_args;
 
-struct Refused {
-  std::string why;
-};
-struct Failed {
-  int status;
-  const char* where;
-};
-struct PythonError {};  // already set
-
-template <typename F>
-PyObject* guarded(F f) {
-  HANDLE_TH_ERRORS
-  try {
-    return f();
-  } catch (const Refused& r) {
-    PyErr_SetString(PyExc_ValueError, r.why.c_str());
-  } catch (const Failed& s) {
-    PyObject* e = PyObject_CallFunction(moe_error, "is", s.status, s.where);
-    if (e) {
-      PyErr_SetObject(moe_error, e);
-      Py_DECREF(e);
-    }
-  } catch (const PythonError&) {
-  }
-  return nullptr;
-  END_HANDLE_TH_ERRORS
-}
-
-// ---------------------------------------------------------------- arguments
-
-template <size_t N>
-struct Call {
-  PyObject* v[N] = {};
-  Call(const char* fn, const char* const (&names)[N], size_t required, PyObject* const* args, Py_ssize_t nargs,
-       PyObject* kwnames) {
-    if (static_cast<size_t>(nargs) > N) {
-      PyErr_Format(PyExc_TypeError, "%s() takes at most %d arguments (%d given)", fn, static_cast<int>(N),
-                   static_cast<int>(nargs));
-      throw PythonError{};
-    }
-    for (Py_ssize_t i = 0; i < nargs; ++i) v[i] = args[i];
-    const Py_ssize_t kw = kwnames ? PyTuple_GET_SIZE(kwnames) : 0;
-    for (Py_ssize_t j = 0; j < kw; ++j) {
-      PyObject* name = PyTuple_GET_ITEM(kwnames, j);
-      size_t i = 0;
-      while (i < N && PyUnicode_CompareWithASCIIString(name, names[i]) != 0) ++i;
-      if (i == N || v[i]) {
-        PyErr_Format(PyExc_TypeError, i == N ? "%s() got an unexpected keyword argument %R"
-                                             : "%s() got multiple values for argument %R", fn, name);
-        throw PythonError{};
-      }
-      v[i] = args[nargs + j];
-    }
-    for (size_t i = 0; i < N; ++i) {
-      if (!v[i] && i < required) {
-        PyErr_Format(PyExc_TypeError, "%s() missing required argument '%s'", fn, names[i]);
-        throw PythonError{};
-      }
-      if (v[i] == Py_None) v[i] = nullptr;
-    }
-  }
-};
-
-// The call again with `stream` (the last argument) current.
-template <size_t N>
-PyObject* hand_over(const char* fn, const Call<N>& c) {
-  PyObject* self = PyDict_GetItemString(module_dict, fn);
-  PyObject* args[N + 1] = {c.v[N - 1], self};
-  for (size_t i = 0; i + 1 < N; ++i) args[2 + i] = c.v[i] ? c.v[i] : Py_None;
-  return PyObject_Vectorcall(on_stream, args, N + 1, nullptr);
-}
-
-const at::Tensor& tensor(PyObject* o, const char* name) {
-  if (!o || !THPVariable_Check(o)) throw Refused{std::string(name) + ": expected a tensor"};
-  return THPVariable_Unpack(o);
-}
-
-int64_t integer(PyObject* o, const char* name) {
-  if (!o) throw Refused{std::string(name) + ": expected an integer"};
-  const long long v = PyLong_AsLongLong(o);
-  if (v == -1 && PyErr_Occurred()) throw PythonError{};
-  return v;
-}
-float number(PyObject* o, const char* name) {
-  if (!o) throw Refused{std::string(name) + ": expected a number"};
-  const double v = PyFloat_AsDouble(o);
-  if (v == -1.0 && PyErr_Occurred()) throw PythonError{};
-  return static_cast<float>(v);
-}
-
-[[noreturn]] void refuse(const char* name, const std::string& wanted, const at::Tensor& t) {
-  std::ostringstream s;
-  s << name << ": expected " << wanted << ", got " << t.scalar_type() << " " << t.sizes() << " on " << t.device();
-  throw Refused{s.str()};
-}
-
-// A tensor that the library reads through its pointer: dense, on the device, of this type and shape.
-const at::Tensor& dense(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape, int dev) {
-  const at::Tensor& t = tensor(o, name);
-  if (t.scalar_type() != type || t.sizes() != shape || t.get_device() != dev || !t.is_contiguous()) {
-    std::ostringstream s;
-    s << "a contiguous " << type << " tensor " << shape << " on device " << dev;
-    refuse(name, s.str(), t);
-  }
-  return t;
-}
-
-// fp32 values, or null.
-const float* values(PyObject* o, const char* name, int64_t count, int dev) {
-  if (!o || o == Py_None) return nullptr;
-  const at::Tensor& t = tensor(o, name);
-  if (t.scalar_type() != at::kFloat || t.numel() != count || t.get_device() != dev || !t.is_contiguous())
-    refuse(name, std::to_string(count) + " fp32 value(s) on device " + std::to_string(dev), t);
-  return static_cast<const float*>(t.const_data_ptr());
-}
-
-// bf16 rows: the row stride in elements, d or more (that of a single row is not used, and torch may report any).
-int64_t row_stride(const at::Tensor& t, const char* name, int64_t n, int64_t d, int dev) {
-  if (t.scalar_type() != at::kBFloat16 || t.dim() != 2 || t.size(0) != n || t.size(1) != d || t.get_device() != dev ||
-      t.stride(1) != 1)
-    refuse(name, "bf16 rows [" + std::to_string(n) + ", " + std::to_string(d) + "] on device " + std::to_string(dev), t);
-  if (n <= 1) return d;
-  // expanded rows, or a window that slides by less than a row
-  if (t.stride(0) < d) refuse(name, "rows of their own, not " + std::to_string(t.stride(0)) + " elements apart", t);
-  return t.stride(0);
-}
-
-void two_dims(const at::Tensor& t, const char* name) {
-  if (t.dim() != 2) refuse(name, "two dimensions", t);
-}
-
-// The stream to launch on; the device is made current by the caller's guard.
-cudaStream_t stream_of(int dev) {
-  if (dev < 0) throw Refused{"expected tensors on a CUDA device"};
-  return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
-}
-// A library call without the interpreter's lock: a launch waits where the GPU's queue is full.  What it
-// points to is held by the caller's arguments or by tensors of the call.
-template <typename F>
-void call(const char* where, F f) {
-  moe_status st;
-  {
-    struct Unlocked {
-      PyThreadState* state = PyEval_SaveThread();
-      ~Unlocked() { PyEval_RestoreThread(state); }
-    } unlocked;
-    st = f();
-  }
-  if (st != MOE_OK) throw Failed{st, where};
-}
+PyObject* rows_class = nullptr;  // mx.MxRows
 
 // ---------------------------------------------------------------- rows
-
-struct Field {
-  PyObject* o;
-  Field(PyObject* from, PyObject* name) : o(PyObject_GetAttr(from, name)) {
-    if (!o) throw PythonError{};
-  }
-  Field(const Field&) = delete;
-  ~Field() { Py_XDECREF(o); }
-  PyObject* get() const { return o == Py_None ? nullptr : o; }
-};
 
 PyObject* s_fmt;
 PyObject* s_cols;
@@ -644,24 +473,21 @@ PyObject* setup(PyObject* self, PyObject* args) {
   Py_RETURN_NONE;
 }
 
-#define MX_CALL(name, doc) \
-  {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL | METH_KEYWORDS, doc}
-
 PyMethodDef methods[] = {
     {"setup", setup, METH_VARARGS, nullptr},
     {"default_error", default_error, METH_NOARGS, nullptr},
-    MX_CALL(mx_quantise,
+    MOE_TORCH_CALL(mx_quantise,
             "mx_quantise(x, fmt, positions=None, out_rows=None, global_scale=None, out=None, stream=None) -> MxRows\n\n"
             "bf16 rows x [n, d] (any row stride that is a multiple of 8) into a format; row t goes to each of\n"
             "positions[t] (int32 [n, k], entries outside the rows are skipped; default its own place, for which there\n"
             "have to be n rows or more) of `out` (out_rows rows, default n * k)."),
-    MX_CALL(mx_add_rmsnorm,
+    MOE_TORCH_CALL(mx_add_rmsnorm,
             "mx_add_rmsnorm(x, residual, gain, eps, fmt, positions=None, out_rows=None, global_scale=None,\n"
             "               sum_out=None, out=None, stream=None) -> (MxRows, sum)\n\n"
             "sum = bf16(x + residual) (residual may be None), rows = Q(rmsnorm(sum)) written as by mx_quantise.\n"
             "sum_out may be x or residual."),
-    MX_CALL(mx_dequantise, "mx_dequantise(r, out=None, stream=None)\n\nbf16 values of rows."),
-    MX_CALL(mx_grouped_product,
+    MOE_TORCH_CALL(mx_dequantise, "mx_dequantise(r, out=None, stream=None)\n\nbf16 values of rows."),
+    MOE_TORCH_CALL(mx_grouped_product,
             "mx_grouped_product(x, w, offsets, out=None, out_pos=None, row_weight=None, ws=None,\n"
             "                   out_type=MOE_MX_OUT_BF16, stream=None)\n\n"
             "out[p(r)] = row_weight[p(r)] * x[r] W_e^T for the rows offsets[e] .. offsets[e + 1] - 1 of each expert e;\n"
@@ -669,11 +495,11 @@ PyMethodDef methods[] = {
             "rounded up to 16).  Rows of no expert are left as they are, all of them where the offsets do not ascend within\n"
             "the rows of x; in a new out they are uninitialised.  Device errors: moe_get_error(ws), mx_get_error() where no\n"
             "ws is given."),
-    MX_CALL(mx_grouped_swiglu,
+    MOE_TORCH_CALL(mx_grouped_swiglu,
             "mx_grouped_swiglu(x, w, offsets, h_global=None, out=None, ws=None, stream=None) -> MxRows\n\n"
             "Rows of silu(x Wg_e^T) * (x Wu_e^T) in the format of x.  Rows of no expert and device errors as in\n"
             "mx_grouped_product."),
-    MX_CALL(mx_layer_forward,
+    MOE_TORCH_CALL(mx_layer_forward,
             "mx_layer_forward(x, residual, gain, eps, topk_ids, topk_weight, gate_up, down, x_global=None,\n"
             "                 h_global=None, ws=None, out_is_fp32=False, stream=None) -> (sum, out)\n\n"
             "The MoE block on microscaled experts: sum = bf16(x + residual), out = sum + the routed experts on\n"
@@ -696,5 +522,8 @@ PyMODINIT_FUNC PyInit__mx_torch() {
                {&s_swiglu, "swiglu"}};
   for (auto& n : names)
     if (!(*n.at = PyUnicode_InternFromString(n.name))) return nullptr;
-  return PyModule_Create(&definition);
+  if (!moe_fp8_names()) return nullptr;
+  PyObject* module = PyModule_Create(&definition);
+  if (module && PyModule_AddFunctions(module, moe_fp8_methods) < 0) Py_CLEAR(module);
+  return module;
 }

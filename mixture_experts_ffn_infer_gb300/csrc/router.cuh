@@ -1,0 +1,202 @@
+// Rows of router logits (moe_router.h): how a warp holds one, their scores, and
+// the launchers of route.cu and balance.cu.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "moe_router.h"
+
+namespace moe {
+
+constexpr float kInf = __builtin_huge_valf();
+constexpr float kNaN = __builtin_nanf("");
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// A row of E values over a warp, V to a lane.  VEC: four neighbours to a lane, read
+// and written together (E and the row stride multiples of 4, rows aligned to four
+// values); else every 32nd.
+template <typename T, int V, bool VEC>
+struct WarpRow {
+  using type = T;
+  static constexpr int width = V;
+  static __device__ __forceinline__ int expert(int i, int lane) {
+    return VEC ? 128 * (i >> 2) + 4 * lane + (i & 3) : 32 * i + lane;
+  }
+  // Values past the row are `fill`.
+  static __device__ __forceinline__ void load(const T* p, int E, int lane, float fill, float (&v)[V]) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < V / 4; ++j) {
+        const int e = 128 * j + 4 * lane;
+        if (e < E) {
+          if constexpr (sizeof(T) == 4) {
+            const float4 q = *reinterpret_cast<const float4*>(p + e);
+            v[4 * j] = q.x, v[4 * j + 1] = q.y, v[4 * j + 2] = q.z, v[4 * j + 3] = q.w;
+          } else {
+            const uint2 q = *reinterpret_cast<const uint2*>(p + e);
+            v[4 * j] = __uint_as_float(q.x << 16), v[4 * j + 1] = __uint_as_float(q.x & 0xffff0000u);
+            v[4 * j + 2] = __uint_as_float(q.y << 16), v[4 * j + 3] = __uint_as_float(q.y & 0xffff0000u);
+          }
+        } else {
+          v[4 * j] = v[4 * j + 1] = v[4 * j + 2] = v[4 * j + 3] = fill;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = 32 * i + lane < E ? to_float(p[32 * i + lane]) : fill;
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, int E, int lane, const float (&v)[V]) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < V / 4; ++j) {
+        const int e = 128 * j + 4 * lane;
+        if (e >= E) continue;
+        if constexpr (sizeof(T) == 4) {
+          *reinterpret_cast<float4*>(p + e) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        } else {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(v[4 * j], v[4 * j + 1]),
+                               hi = __floats2bfloat162_rn(v[4 * j + 2], v[4 * j + 3]);
+          *reinterpret_cast<uint2*>(p + e) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (32 * i + lane < E) {
+          if constexpr (sizeof(T) == 4) p[32 * i + lane] = v[i];
+          else p[32 * i + lane] = __float2bfloat16_rn(v[i]);
+        }
+    }
+  }
+};
+
+// The larger value, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max_nan(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// 1 / (1 + e^-l); the fast reciprocal is within an ulp, and 0 where e^-l passes 2^126.
+__device__ __forceinline__ float sigmoid_of(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
+
+// What a row's softmax needs of the whole row: score = exp(l - shift) * inv.  A row of -inf alone has
+// shift 0 and scores 0.
+struct SoftmaxRow {
+  float shift, inv;
+};
+template <int V>
+__device__ __forceinline__ SoftmaxRow softmax_row(const float (&l)[V], float top, float (&s)[V]) {
+  SoftmaxRow r;
+  r.shift = top == -kInf ? 0.f : top;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    s[i] = expf(l[i] - r.shift);
+    sum += s[i];
+  }
+  sum = warp_sum(sum);
+  r.inv = sum > 0.f ? __frcp_rn(sum) : 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) s[i] *= r.inv;
+  return r;
+}
+
+struct RouteLaunch {
+  moe_router r;
+  int64_t n;
+  const void* logits;
+  int64_t ld;
+  const float* bias;
+  int32_t* ids;
+  float* weight;
+};
+cudaError_t launch_route(const RouteLaunch& a, cudaStream_t s);
+
+// Rows of a CTA and the number of CTAs of the loss's first kernel.
+struct BalancePlan {
+  int64_t chunk;
+  int32_t chunks;
+};
+BalancePlan balance_plan(int64_t n);
+
+struct BalanceLaunch {
+  moe_router r;
+  int64_t n;
+  const void* logits;
+  int64_t ld;
+  const int32_t* ids;
+  float coef;
+  const int32_t* offsets;  // null: one sequence
+  int32_t sequences;
+  int32_t* counts;
+  float* loss;
+  // workspace: a ticket, the sequences' parts of the loss [S][balance_parts(E)], and of each piece (the rows of
+  // one CTA in one sequence, piece CTA + sequence) the shares' sums [E] and the counts [E]
+  uint32_t* ticket;
+  float* parts;
+  float* sums;
+  int32_t* hist;
+};
+constexpr int kBalanceCols = 32;  // experts of a CTA of the loss's second kernel
+inline int32_t balance_parts(int32_t E) { return (E + kBalanceCols - 1) / kBalanceCols; }
+cudaError_t launch_balance(const BalanceLaunch& a, cudaStream_t s);
+
+struct RouteGradLaunch {
+  moe_router r;
+  int64_t n;
+  const void* logits;
+  int64_t ld;
+  const int32_t* ids;
+  const float* d_weight;
+  float coef;
+  const int32_t* counts;
+  const float* d_loss;
+  const int32_t* offsets;
+  int32_t sequences;
+  void* d_logits;
+  int64_t d_ld;
+};
+cudaError_t launch_route_grad(const RouteGradLaunch& a, cudaStream_t s);
+
+// Calls f with a WarpRow for the logits' type, number and alignment.
+template <typename F>
+cudaError_t with_row(const moe_router& r, bool vec, F f) {
+  auto by_width = [&](auto type) -> cudaError_t {
+    using T = decltype(type);
+    const int E = r.num_experts;
+    if (vec) {
+      if (E <= 128) return f(WarpRow<T, 4, true>{});
+      if (E <= 256) return f(WarpRow<T, 8, true>{});
+      if (E <= 384) return f(WarpRow<T, 12, true>{});
+      if (E <= 512) return f(WarpRow<T, 16, true>{});
+      return f(WarpRow<T, 32, true>{});
+    }
+    if (E <= 64) return f(WarpRow<T, 2, false>{});
+    if (E <= 256) return f(WarpRow<T, 8, false>{});
+    if (E <= 512) return f(WarpRow<T, 16, false>{});
+    return f(WarpRow<T, 32, false>{});
+  };
+  return r.logits_type == MOE_LOGITS_F32 ? by_width(float{}) : by_width(__nv_bfloat16{});
+}
+// Rows that can be read four values at a time.
+inline bool rows_by_four(const moe_router& r, const void* p, int64_t ld) {
+  return r.num_experts % 4 == 0 && ld % 4 == 0 &&
+         reinterpret_cast<uintptr_t>(p) % (r.logits_type == MOE_LOGITS_F32 ? 16 : 8) == 0;
+}
+
+}  // namespace moe

@@ -1,0 +1,405 @@
+"""The router's choice, balance loss and gradient on the GPU against plain 64-bit statements (router_plain.py)."""
+
+import math
+
+import pytest
+import torch
+
+import mixture_experts_ffn_infer_gb300 as mx
+from tests import router_plain as plain
+from tests.router_plain import EPS
+
+pytestmark = pytest.mark.gpu
+INF = math.inf
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def logits_of(seed, n, E, dtype=torch.float32, std=1.5):
+    return (torch.randn(n, E, generator=gen(seed)) * std).to(dtype)
+
+
+def check_choice(logits, k, kind, bias=None, groups=1, top_groups=1, normalise=True, scale=1.0, on_gpu=None):
+    x = logits.cuda() if on_gpu is None else on_gpu
+    ids, w = mx.route(x, k, mx.MOE_SCORES[kind], bias=None if bias is None else bias.cuda(), groups=groups,
+                      top_groups=top_groups, normalise=normalise, scale=scale)
+    want_ids, want_w = plain.choice(logits, k, kind, bias, groups, top_groups, normalise, scale)
+    assert ids.dtype == torch.int32 and torch.equal(ids.cpu(), want_ids)
+    w = w.cpu().double()
+    nan = want_w.isnan()
+    assert torch.equal(w.isnan(), nan)
+    # a score, the chosen ones' sum (their errors and k + 5 additions), a quotient and a product
+    tol = (2 * plain.score_error(logits) + k + 9) * EPS
+    err = ((w - want_w).abs() - tol * want_w.abs())[~nan]
+    assert err.numel() == 0 or err.max() <= 1e-37
+    return ids, w
+
+
+# ---------------------------------------------------------------- the choice
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,E,k,bias", [(1, 1, 1, False), (1, 384, 8, True), (5, 384, 8, False), (3, 7, 7, True),
+                                        (40, 60, 3, True), (7, 128, 4, False), (9, 129, 16, True), (4, 256, 32, False),
+                                        (3, 32, 32, True), (3, 500, 32, True), (2, 1024, 9, True), (400, 16, 4, False),
+                                        (33, 1000, 5, False), (2000, 66, 2, True)])
+def test_choice(kind, dtype, n, E, k, bias):
+    b = torch.randn(E, generator=gen(E)) * 0.1 if bias else None
+    check_choice(logits_of(n + E, n, E, dtype), k, kind, b, normalise=n % 2 == 0, scale=2.5)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top,k,bias", [(256, 8, 4, 8, True), (256, 8, 4, 8, False), (96, 6, 2, 5, True),
+                                                 (60, 5, 3, 7, False), (32, 32, 3, 3, True), (64, 2, 1, 32, True),
+                                                 (30, 10, 10, 12, False), (1024, 32, 5, 9, True), (93, 31, 7, 4, False)])
+def test_groups(kind, E, groups, top, k, bias):
+    b = torch.randn(E, generator=gen(E)) * 0.1 if bias else None
+    for dtype in (torch.float32, torch.bfloat16):
+        check_choice(logits_of(E + top, 50, E, dtype), k, kind, b, groups, top, normalise=top % 2 == 0)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_strides_and_alignments(kind):
+    wide = logits_of(1, 30, 203)
+    for dtype in (torch.float32, torch.bfloat16):
+        x = wide.to(dtype).cuda()
+        for a, E in ((0, 64), (1, 64), (2, 64), (3, 200), (0, 203)):
+            rows = x[:, a:a + E]
+            check_choice(rows.cpu(), 6, kind, on_gpu=rows)
+            check_choice(rows[:1].cpu(), 6, kind, on_gpu=rows[:1])
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,top", [(1, 1), (4, 2)])
+def test_equal_values_go_to_the_lowest_index(kind, groups, top):
+    E, k = 64, 8
+    flat = torch.zeros(3, E)
+    few = (torch.randint(0, 3, (20, E), generator=gen(1)).float() - 1).to(torch.bfloat16)
+    for logits in (flat, few):
+        for bias in (None, torch.zeros(E), torch.randint(0, 2, (E,), generator=gen(2)).float() * 0.25):
+            check_choice(logits, k, kind, bias, groups, top)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top", [(24, 1, 1), (64, 1, 1), (384, 1, 1), (64, 8, 3)])
+def test_scores_closer_than_fp32_tells_apart(kind, E, groups, top):
+    # biases that bring every expert's choice to the same value within fp32's rounding: the order is in the bits below
+    logits = logits_of(E + top, 1, E, std=1.0)
+    bias = (1.0 - plain.scores(logits, kind)[0]).float()
+    check_choice(logits, 8, kind, bias, groups, top)
+    # and pairs of them among others
+    many = logits_of(E, 40, E, std=1.0)
+    s = plain.scores(many, kind)[0]
+    pairs = torch.randn(E, generator=gen(3)) * 0.05
+    pairs[1::2] = (s[0::2] + pairs[0::2].double() - s[1::2]).float()
+    check_choice(many, 8, kind, pairs, groups, top)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [1, 4])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_masks_and_values_that_are_not_finite(kind, groups, with_bias):
+    E, k = 40, 6
+    x = logits_of(5, 12, E)
+    x[0] = -INF                                   # nothing left
+    x[1, 3:] = -INF                               # fewer than k
+    x[2, ::2] = -INF
+    x[3, 7] = math.nan
+    x[4, 9] = INF
+    x[5] = torch.finfo(torch.float32).min         # the type's lowest value masks nothing: all equal
+    x[6, 1:] = torch.finfo(torch.float32).min
+    x[7] = 200.0
+    x[8] = -200.0                                 # sigmoid: below fp32
+    x[9, :10] = -INF                              # a whole group
+    bias = None
+    if with_bias:
+        bias = torch.randn(E, generator=gen(6)) * 0.1
+        bias[5], bias[11], bias[30] = -INF, math.nan, INF
+    if kind == "sigmoid":
+        x[8] = -60.0 - torch.arange(E) / 64       # in range, and apart in 64 bits
+    check_choice(x, k, kind, bias, groups, max(1, groups // 2))
+    check_choice(x, k, kind, bias, groups, max(1, groups // 2), normalise=False)
+
+
+def test_the_callers_tensors_and_nothing_around_them():
+    n, E, k = 70, 48, 5
+    x = logits_of(1, n, E).cuda()
+    want = mx.route(x, k, mx.MOE_SCORE_SIGMOID)
+    room_i, room_w = torch.full((n + 2, k), -7, dtype=torch.int32).cuda(), torch.full((n + 2, k), -7.0).cuda()
+    got = mx.route(x, k, mx.MOE_SCORE_SIGMOID, ids=room_i[1:-1], weights=room_w[1:-1])
+    assert got[0].data_ptr() == room_i[1:].data_ptr() and torch.equal(room_i[1:-1], want[0]) and torch.equal(room_w[1:-1], want[1])
+    for room in (room_i, room_w):
+        assert (room[0] == -7).all() and (room[-1] == -7).all()
+    empty = mx.route(x[:0], k, mx.MOE_SCORE_SIGMOID)
+    assert empty[0].shape == (0, k) and empty[1].shape == (0, k)
+
+
+# ---------------------------------------------------------------- the loss
+
+def ragged(seed, n, S):
+    cut = torch.randint(0, n + 1, (S - 1,), generator=gen(seed)).sort().values
+    if S > 3:
+        cut[1] = cut[0]
+    return torch.cat([torch.tensor([0]), cut, torch.tensor([n])]).to(torch.int32)
+
+
+def ids_of(seed, n, k, E):
+    return torch.rand(n, E, generator=gen(seed)).topk(k, 1).indices.to(torch.int32)
+
+
+def loss_error(logits, live_rows):
+    """Relative: a share, and sums of positive values: a CTA's run of max(64, n / 304) rows by eight warps, eight warps,
+    up to 305 pieces by eight warps, 32 experts and E / 32 parts, besides a handful of products."""
+    n, E = logits.shape
+    run = max(64, n / 304)
+    return (2 * plain.score_error(logits) + run / 8 + 8 + 39 + 8 + 5 + E / 32 + 10) * EPS
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,E,k,S,pad", [(1, 1, 1, 1, 0), (1, 384, 8, 1, 0), (64, 16, 4, 1, 0), (65, 33, 2, 3, 1),
+                                         (1001, 60, 3, 5, 37), (500, 384, 8, 500, 0), (3000, 130, 6, 40, 5),
+                                         (130, 1024, 32, 2, 0), (2000, 8, 2, 6000, 300)])
+def test_loss_and_counts(kind, dtype, n, E, k, S, pad):
+    logits, ids = logits_of(n + E, n, E, dtype), ids_of(n, n, k, E)
+    offsets = None if S == 1 and pad == 0 else ragged(S, n - pad, S)
+    loss, counts = mx.balance_loss(logits.cuda(), ids.cuda(), 0.01, mx.MOE_SCORES[kind],
+                                   seq_offsets=None if offsets is None else offsets.cuda())
+    want, want_counts = plain.balance(logits, ids, 0.01, kind, offsets)
+    assert loss.shape == () and counts.dtype == torch.int32 and torch.equal(counts.cpu(), want_counts)
+    assert abs(loss.item() - want.item()) <= loss_error(logits, n) * abs(want.item())
+
+
+def test_even_shares_cost_the_coefficient():
+    n, E, k = 96, 48, 4
+    ids = torch.arange(n * k).reshape(n, k).remainder(E).to(torch.int32).cuda()
+    for score in (mx.MOE_SCORE_SOFTMAX, mx.MOE_SCORE_SIGMOID):
+        loss, counts = mx.balance_loss(torch.zeros(n, E).cuda(), ids, 0.125, score)
+        assert (counts == n * k // E).all() and abs(loss.item() - 0.125) < 0.125 * 100 * EPS
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_loss_of_odd_rows(kind):
+    n, E, k = 50, 20, 3
+    logits, ids = logits_of(1, n, E), ids_of(2, n, k, E)
+    logits[3] = -INF
+    logits[4, 5:] = -INF
+    ids[7] = torch.tensor([-1, E, 1 << 30], dtype=torch.int32)   # counted nowhere
+    ids[8] = 4                                                    # one expert three times
+    offsets = torch.tensor([5, 5, 30, 45], dtype=torch.int32)     # rows in front of the first and behind the last
+    for o in (None, offsets):
+        args = dict(seq_offsets=None if o is None else o.cuda())
+        loss, counts = mx.balance_loss(logits.cuda(), ids.cuda(), 1.0, mx.MOE_SCORES[kind], **args)
+        want, want_counts = plain.balance(logits, ids, 1.0, kind, o)
+        assert torch.equal(counts.cpu(), want_counts)
+        assert abs(loss.item() - want.item()) <= loss_error(logits, n) * want.item()
+    logits[10, 2] = math.nan
+    loss, counts = mx.balance_loss(logits.cuda(), ids.cuda(), 1.0, mx.MOE_SCORES[kind])
+    assert loss.isnan() and torch.equal(counts.cpu(), plain.balance(logits, ids, 1.0, kind)[1])
+    loss, _ = mx.balance_loss(logits.cuda(), ids.cuda(), 1.0, mx.MOE_SCORES[kind],      # the NaN is padding
+                              seq_offsets=torch.tensor([0, 10], dtype=torch.int32).cuda())
+    assert loss.isfinite()
+
+
+@pytest.mark.parametrize("offsets", [[0, 30, 20, 50], [-1, 10, 20, 50], [0, 10, 20, 51], [60, 10, 5, 0]])
+def test_offsets_that_do_not_ascend_give_nan(offsets):
+    n, E, k = 50, 20, 3
+    logits, ids = logits_of(1, n, E).cuda(), ids_of(2, n, k, E).cuda()
+    o = torch.tensor(offsets, dtype=torch.int32).cuda()
+    loss, counts = mx.balance_loss(logits, ids, 1.0, mx.MOE_SCORE_SOFTMAX, seq_offsets=o)
+    assert loss.isnan()
+    grad = mx.route_backward(logits, ids, mx.MOE_SCORE_SOFTMAX, counts=counts, coef=1.0, seq_offsets=o)
+    assert grad.shape == (n, E)
+    torch.cuda.synchronize()
+
+
+def test_no_rows():
+    E, k = 12, 2
+    for o in (None, torch.zeros(4, dtype=torch.int32).cuda()):
+        loss, counts = mx.balance_loss(torch.zeros(0, E).cuda(), torch.zeros(0, k, dtype=torch.int32).cuda(), 1.0, 0, seq_offsets=o)
+        assert loss.item() == 0.0 and (counts == 0).all() and counts.shape[1] == E
+    assert mx.route_backward(torch.zeros(0, E).cuda(), torch.zeros(0, k, dtype=torch.int32).cuda(), 0).shape == (0, E)
+
+
+# ---------------------------------------------------------------- the gradient
+
+def check_gradient(logits, ids, kind, offsets=None, coef=None, d_loss=None, out=None, **kw):
+    cuda = lambda t: None if t is None else t.cuda()
+    x = logits.cuda()
+    args = dict(kw, d_weights=cuda(kw.get("d_weights")))
+    if coef is not None:
+        _, counts = mx.balance_loss(x, ids.cuda(), coef, mx.MOE_SCORES[kind], seq_offsets=cuda(offsets))
+        args |= dict(counts=counts, coef=coef, seq_offsets=cuda(offsets), d_loss=cuda(d_loss))
+    got = mx.route_backward(x, ids.cuda(), mx.MOE_SCORES[kind], out=out(x) if out else None, **args)
+    assert got.dtype == logits.dtype
+    scale = 1.0 if d_loss is None else d_loss.item()
+    want = plain.gradient(logits, ids, kind, coef=coef, d_loss=scale, offsets=offsets, **kw)
+    size = plain.gradient_size(logits, ids, kind, coef=coef, d_loss=scale, offsets=offsets, **kw)
+    # every factor of every term is a score, a sum of scores or a product with one; the counts' factor has eight roundings
+    tol = (6 * plain.score_error(logits) + 2 * ids.shape[1] + 30) * EPS
+    half = torch.finfo(logits.dtype).eps / 2
+    err = (got.cpu().double() - want).abs() - tol * size - half * (want.abs() + tol * size)
+    assert err.max() <= 1e-37, (err.max(), want.abs().max())
+    return got, want
+
+
+CASES = [(1, 1, 1, 1, 0), (1, 384, 8, 1, 0), (64, 16, 4, 1, 0), (65, 33, 2, 3, 1), (1001, 60, 3, 5, 37),
+         (300, 384, 8, 300, 0), (3000, 130, 6, 40, 5), (130, 1024, 32, 2, 0), (500, 8, 2, 2000, 100)]
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,E,k,S,pad", CASES)
+def test_gradient(kind, dtype, n, E, k, S, pad):
+    logits, ids = logits_of(n + E, n, E, dtype), ids_of(n, n, k, E)
+    offsets = None if S == 1 and pad == 0 else ragged(S, n - pad, S)
+    d_weights = torch.randn(n, k, generator=gen(4))
+    both = dict(d_weights=d_weights, coef=0.7, d_loss=torch.tensor([3.0]), offsets=offsets, scale=2.5)
+    check_gradient(logits, ids, kind, normalise=True, **both)
+    check_gradient(logits, ids, kind, normalise=False, **both)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_gradient_of_each_part_alone(kind):
+    n, E, k = 90, 40, 4
+    logits, ids = logits_of(1, n, E), ids_of(2, n, k, E)
+    d_weights = torch.randn(n, k, generator=gen(4))
+    check_gradient(logits, ids, kind, d_weights=d_weights, normalise=True)
+    check_gradient(logits, ids, kind, d_weights=d_weights, normalise=False, scale=0.5)
+    offsets = torch.tensor([10, 10, 60, 80], dtype=torch.int32)
+    got, _ = check_gradient(logits, ids, kind, coef=2.0, offsets=offsets)
+    assert (got[:10] == 0).all() and (got[80:] == 0).all() and (got[10:80] != 0).any()
+    nothing = mx.route_backward(logits.cuda(), ids.cuda(), mx.MOE_SCORES[kind])
+    assert (nothing == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_gradient_against_differences(kind):
+    n, E, k = 40, 24, 3
+    logits, ids = logits_of(1, n, E), ids_of(2, n, k, E)
+    offsets = torch.tensor([0, 15, 33], dtype=torch.int32)
+    kw = dict(d_weights=torch.randn(n, k, generator=gen(4)), normalise=True, scale=2.5, coef=5.0, offsets=offsets)
+    got, _ = check_gradient(logits, ids, kind, **kw)
+    step = torch.randn(n, E, generator=gen(5), dtype=torch.float64)
+    h = 1e-5
+    up, down = (plain.objective(logits.double() + s * h * step, ids, kind, **kw) for s in (1, -1))
+    along = (got.cpu().double() * step).sum()
+    # h^2 times the third derivative (below 10 a term of order 1), the difference's rounding, the gradient's own error
+    size = (plain.gradient_size(logits, ids, kind, **kw) * step.abs()).sum()
+    assert abs((up - down) / (2 * h) - along) <= 10 * h * h * size + 1e-15 / h * n + 400 * EPS * size
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalise", [False, True])
+def test_gradient_of_odd_rows(kind, normalise):
+    n, E, k = 30, 40, 6
+    logits, ids = logits_of(1, n, E), ids_of(2, n, k, E)
+    logits[0] = -INF
+    logits[1, 3:] = -INF
+    ids[1] = torch.tensor([0, 1, 2, -1, -1, -1], dtype=torch.int32)
+    logits[2, ::2] = -INF
+    ids[3] = torch.tensor([5, 5, 5, 7, 7, E], dtype=torch.int32)    # named twice, and none
+    ids[4] = -1
+    logits[5] = 30.0
+    logits[6] = -30.0
+    d_weights = torch.randn(n, k, generator=gen(4))
+    finite = logits.clone()
+    finite[logits == -INF] = -1e4                                   # the same scores of 0, without inf - inf in the formula
+    cuda = logits.cuda()
+    for row in range(7):
+        one, i, g = logits[row:row + 1], ids[row:row + 1], d_weights[row:row + 1]
+        got = mx.route_backward(cuda[row:row + 1], i.cuda(), mx.MOE_SCORES[kind], d_weights=g.cuda(), normalise=normalise)
+        if row == 0:
+            assert (got == 0).all()
+            continue
+        kw = dict(d_weights=g, normalise=normalise)
+        want, size = (f(finite[row:row + 1], i, kind, **kw) for f in (plain.gradient, plain.gradient_size))
+        tol = (6 * plain.score_error(one) + 2 * k + 30) * EPS
+        assert ((got.cpu().double() - want).abs() - tol * size - EPS * want.abs()).max() <= 1e-37
+        assert (got.cpu()[one == -INF] == 0).all()
+    bad = logits.clone()
+    bad[9, 1] = math.nan
+    grads = [mx.route_backward(x.cuda(), ids.cuda(), mx.MOE_SCORES[kind], d_weights=d_weights.cuda(), normalise=normalise)
+             for x in (bad, logits)]
+    assert grads[0][9].isnan().all()
+    keep = torch.arange(n) != 9
+    assert torch.equal(grads[0][keep], grads[1][keep])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_gradient_into_strided_rows_and_in_place(dtype, kind):
+    n, E, k = 60, 36, 4
+    ids, d_weights = ids_of(2, n, k, E), torch.randn(n, k, generator=gen(4))
+    logits = logits_of(1, n, E, dtype)
+    for a, width in ((0, 40), (1, 41), (4, 48)):
+        room = torch.full((n, width), 9.0, dtype=dtype).cuda()
+        check_gradient(logits, ids, kind, d_weights=d_weights, coef=1.0, out=lambda x: room[:, a:a + E])
+        assert (room[:, :a] == 9).all() and (room[:, a + E:] == 9).all()
+    got, _ = check_gradient(logits, ids, kind, d_weights=d_weights, coef=1.0, out=lambda x: x)
+
+
+# ---------------------------------------------------------------- as a program runs them
+
+def test_the_same_bits_each_time_and_in_a_graph():
+    n, E, k = 5000, 384, 8
+    x, x2 = logits_of(1, n, E).cuda(), logits_of(2, n, E).cuda()
+    offsets = ragged(3, n, 7).cuda()
+    bias = (torch.randn(E, generator=gen(4)) * 0.05).cuda()
+    d_weights, d_loss = torch.randn(n, k, generator=gen(5)).cuda(), torch.tensor([0.5]).cuda()
+
+    def step(x):
+        ids, w = mx.route(x, k, mx.MOE_SCORE_SIGMOID, bias=bias, scale=2.5)
+        loss, counts = mx.balance_loss(x, ids, 1e-3, mx.MOE_SCORE_SIGMOID, seq_offsets=offsets)
+        grad = mx.route_backward(x, ids, mx.MOE_SCORE_SIGMOID, d_weights=d_weights, scale=2.5, counts=counts, coef=1e-3,
+                                 d_loss=d_loss, seq_offsets=offsets)
+        return ids, w, loss, counts, grad
+
+    want = [step(x), step(x2)]
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(step(x), want[0]))
+    held = x.clone()
+    torch.cuda.synchronize()
+    graph, other = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(held)
+    with torch.cuda.graph(other):
+        got2 = step(held)
+    for data, w in ((x2, want[1]), (x, want[0]), (x2, want[1])):
+        held.copy_(data)
+        graph.replay()
+        other.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, w)) and all(torch.equal(a, b) for a, b in zip(got2, w))
+
+
+def test_another_stream():
+    n, E, k = 3000, 100, 4
+    x, s = logits_of(1, n, E).cuda(), torch.cuda.Stream()
+    want_ids, want_w = mx.route(x, k, mx.MOE_SCORE_SOFTMAX)
+    want_loss, want_counts = mx.balance_loss(x, want_ids, 1.0, mx.MOE_SCORE_SOFTMAX)
+    want_grad = mx.route_backward(x, want_ids, mx.MOE_SCORE_SOFTMAX, counts=want_counts, coef=1.0)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        late = torch.zeros_like(x)
+        big = torch.zeros(4096, 4096, device="cuda")
+        for _ in range(20):
+            big = big @ big
+        late.copy_(x)
+    ids, w = mx.route(late, k, mx.MOE_SCORE_SOFTMAX, stream=s)
+    loss, counts = mx.balance_loss(late, ids, 1.0, mx.MOE_SCORE_SOFTMAX, stream=s.cuda_stream)
+    grad = mx.route_backward(late, ids, mx.MOE_SCORE_SOFTMAX, counts=counts, coef=1.0, stream=s)
+    s.synchronize()
+    for a, b in ((ids, want_ids), (w, want_w), (loss, want_loss), (counts, want_counts), (grad, want_grad)):
+        assert torch.equal(a, b)
+
+
+def test_the_routing_plan_takes_the_choice():
+    n, E, k = 600, 48, 5
+    x = logits_of(1, n, E).cuda()
+    ids, _ = mx.route(x, k, mx.MOE_SCORE_SOFTMAX)
+    _, counts = mx.balance_loss(x, ids, 1.0, mx.MOE_SCORE_SOFTMAX)
+    assert torch.equal(mx.permute(ids, E, validate=True)[0], counts[0])
