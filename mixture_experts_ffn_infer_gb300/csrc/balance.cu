@@ -37,7 +37,7 @@ __device__ __forceinline__ void shares(bool sigmoid, const float (&l)[Row::width
       sum += q[i];
     }
     sum = warp_sum(sum);
-    const float inv = sum == 0.f ? 0.f : __frcp_rn(sum);
+    const float inv = sum == 0.f ? 0.f : __frcp_rn(sum);  // (a masked row's shares are 0)
 #pragma unroll
     for (int i = 0; i < V; ++i) q[i] *= inv;
   } else {
@@ -66,7 +66,7 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int sequences
 }
 
 template <typename Row>
-__global__ void __launch_bounds__(32 * kRowWarps)
+__global__ void __launch_bounds__(32 * kRowWarps, Row::width <= 12 ? 4 : 1)
 balance_rows_kernel(const BalanceLaunch a, const BalancePlan plan) {
   using T = typename Row::type;
   constexpr int V = Row::width;
@@ -196,8 +196,12 @@ balance_loss_kernel(const BalanceLaunch a, const BalancePlan plan) {
   }
 }
 
+// CTAs of the gradient that an SM holds.
 template <typename Row>
-__global__ void __launch_bounds__(32 * kRowWarps)
+constexpr int kGradResident = Row::width <= 12 ? 3 : Row::width <= 16 ? 2 : 1;
+
+template <typename Row>
+__global__ void __launch_bounds__(32 * kRowWarps, kGradResident<Row>)
 route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
   using T = typename Row::type;
   constexpr int V = Row::width;
@@ -257,7 +261,7 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
       }
       until = in ? hi : lo > t ? lo : a.n;
     }
-    float s[V];
+    float s[V], u[V];  // scores; sigmoid: e^-l s = 1 - s
     float dj;  // ds of the lane's chosen expert
     float top = l[0];
 #pragma unroll
@@ -267,7 +271,8 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
     if (sigmoid) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        s[i] = sigmoid_of(l[i]);
+        s[i] = sigmoid_of(l[i], u[i]);
+        u[i] *= s[i];
         total += s[i];
       }
     } else {
@@ -278,7 +283,7 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
     if (a.d_weight) {
       dj = g;
       if (a.r.normalise) {
-        const float sj = id < 0 ? 0.f : sigmoid ? sigmoid_of(lj) : expf(lj - soft.shift) * soft.inv;
+        const float sj = id < 0 ? 0.f : sigmoid ? sigmoid_of(lj) : softmax_term(lj, soft.shift) * soft.inv;
         const float sum = warp_sum(sj) + kTiny, dot = warp_sum(g * sj);
         dj = __fdividef(g - __fdividef(dot, sum), sum);
       }
@@ -317,11 +322,7 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
         for (int i = 0; i < V; ++i) d[i] = fmaf(c[i] - dot, inv, d[i]);
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        // 1 - s: above 0 e^-l s, where 1 - s would cancel
-        const float rest = l[i] > 0.f ? expf(-l[i]) * s[i] : 1.f - s[i];
-        d[i] = d[i] * s[i] * rest;
-      }
+      for (int i = 0; i < V; ++i) d[i] = d[i] * s[i] * u[i];
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -344,8 +345,8 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
 }  // namespace
 
 BalancePlan balance_plan(int64_t n) {
-  // Runs of eight rows a warp at least, two CTAs an SM at most: more pieces cost the second kernel as much.
-  constexpr int64_t kMost = 304, kLeast = 64;
+  // Runs of eight rows a warp at least, four CTAs an SM at most.
+  constexpr int64_t kMost = 608, kLeast = 64;
   int64_t chunk = (n + kMost - 1) / kMost;
   if (chunk < kLeast) chunk = kLeast;
   if (chunk > n) chunk = n < 1 ? 1 : n;
@@ -378,11 +379,12 @@ cudaError_t launch_route_grad(const RouteGradLaunch& a, cudaStream_t s) {
   if (sms <= 0) return cudaErrorInvalidValue;
   int warps = 1;
   while (warps < kRowWarps && a.n > sms * warps) warps *= 2;
-  // two rounds of the CTAs that an SM holds, so that the last ones to start are not the last to end
-  const int64_t most = sms * 16 * warps, run = (a.n + most - 1) / most, ctas = (a.n + run * warps - 1) / (run * warps);
   const size_t smem = sizeof(float) * static_cast<size_t>(warps) * a.r.num_experts;
   const bool vec = rows_by_four(a.r, a.logits, a.ld) && rows_by_four(a.r, a.d_logits, a.d_ld);
   return with_row(a.r, vec, [&](auto row) {
+    // one round of the CTAs that the SMs hold
+    const int64_t most = sms * kGradResident<decltype(row)> * kRowWarps, run = (a.n + most - 1) / most;
+    const int64_t ctas = (a.n + run * warps - 1) / (run * warps);
     return launch_maybe_overlapped(route_grad_kernel<decltype(row)>, static_cast<int>(ctas), 32 * warps, smem, s, true, a,
                                    run);
   });

@@ -1,20 +1,22 @@
 // The router's choice of experts (moe_route in moe_router.h).
 //
 // A warp takes a row: its scores, the k largest and their weights in one read of the
-// row.  HBM would bound it; what has to be kept below that is the number of
-// instructions, of which a plain "largest, k times" over E / 32 values a lane would
-// take most.  So
+// row.  HBM would bound it (32,768 rows of 384 fp32 logits: 7.9 us); what has to be kept
+// below that is the number of instructions, of which a plain "largest, k times" over
+// E / 32 values a lane would take most.  So
 //  1. each lane's largest value, and the (k + 1)-th largest of the 32 (k + 1 warp
-//     maxima): no value of the k + 1 largest is below it;
-//  2. the values from there up, some k + 3, one to a lane;
-//  3. these in order, by warp maxima over one value a lane.
+//     maxima): no value of the k + 1 largest is below it.  Scores here are short ones,
+//     within 2^-20;
+//  2. the values from there up (less a margin for the short scores), some k + 3, one to
+//     a lane, and their scores again, within 2^-21 of each;
+//  3. the rank of each among them, by comparing with all: no step waits for the last.
 // Step 2 finds more than 32 only where many values are equal; such rows take the slow
-// way, k maxima over all values.
+// way, k maxima over all values in 64 bits.
 //
 // The choice is that of the exact scores.  With a bias (or groups) fp32 scores order two
-// experts wrongly where they are closer than the scores' errors: adjacent ones of the
+// experts wrongly where they are closer than the scores' errors: neighbours among the
 // k + 1 largest that are closer than `tolerance` and not equal by their inputs send the
-// row (one in a thousand of random ones) to the comparison in 64 bits.
+// row (three in a thousand of random ones) to the same ranking in 64 bits.
 #include "router.cuh"
 
 namespace moe {
@@ -45,10 +47,9 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// The bound of |difference of two fp32 choices - the exact one|, doubled for safety.  Sigmoid: expf within 2 ulp, the
-// sum and the reciprocal 1 ulp each: below 2^-21 of a score, twice, and the sums with the bias 2^-24 each.  Softmax:
-// besides these l - shift rounds (|l - shift| 2^-24 of the score, at most 104 of them before it is 0) and the row's
-// sum has (V + 5) 2^-24.
+// How far two fp32 choices' difference may be from the exact one, twice over.  A sigmoid is within 2^-21 of itself; a
+// softmax term within 2^-21 too, its difference from the row's largest rounds (2^-24 of up to 104, below which it is 0)
+// and the row's sum has (V + 5) 2^-24; the sums with the bias 2^-24 each.
 __device__ __forceinline__ float tolerance(bool sigmoid, float s, float x) {
   return fmaf(sigmoid ? 0x1p-19f : 0x1p-15f, s, 0x1p-21f * fabsf(x));
 }
@@ -145,8 +146,94 @@ __device__ __noinline__ int exact_choice(const moe_router r, const typename Row:
   return id;
 }
 
+// The rank of this lane's value among those of lanes 0 .. count - 1, ties to the lower e; next: the nearest larger one.
+__device__ __forceinline__ int rank_of(uint32_t key, int e, int count, uint32_t& next) {
+  int rank = 0;
+  next = 0xffffffffu;
+  const uint64_t mine = static_cast<uint64_t>(key) << 32 | static_cast<uint32_t>(~e);
+#pragma unroll 4
+  for (int j = 0; j < count; ++j) {
+    const uint32_t kj = __shfl_sync(kAll, key, j), ej = __shfl_sync(kAll, static_cast<uint32_t>(~e), j);
+    rank += (static_cast<uint64_t>(kj) << 32 | ej) > mine ? 1 : 0;
+    if (kj > key) next = min(next, kj);
+  }
+  return rank;
+}
+
+// The same in 64 bits: the value is the exact score of logit l plus bias b.
 template <typename Row>
-__global__ void __launch_bounds__(32 * kWarps)
+__device__ __noinline__ int exact_rank(const typename Row::type* p, int E, bool sigmoid, float shift, float l, float b, int e,
+                                       int count) {
+  const int lane = threadIdx.x & 31;
+  double total = 0.0;
+  if (!sigmoid) {
+#pragma unroll 1
+    for (int at = lane; at < E; at += 32) total += exp(static_cast<double>(to_float(p[at])) - static_cast<double>(shift));
+    total = warp_sum(total);
+  }
+  const double x = (sigmoid ? exact_sigmoid(l) : exact_softmax(l, shift, total)) + static_cast<double>(b);
+  int rank = 0;
+#pragma unroll 1
+  for (int j = 0; j < count; ++j) {
+    const double xj = __shfl_sync(kAll, x, j);
+    const int ej = __shfl_sync(kAll, e, j);
+    rank += xj > x || (xj == x && ej < e) ? 1 : 0;
+  }
+  return rank;
+}
+
+// The kept groups' bits.  x: the warp's choices (-inf: not to be chosen), by way of `row` in shared memory; unsure: the
+// last kept and the first other group are too close.
+template <typename Row>
+__device__ __forceinline__ uint32_t kept_groups(const moe_router& r, const float (&x)[Row::width], float* row, float most,
+                                                bool& unsure) {
+  const int E = r.num_experts, lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < Row::width; ++i) {
+    const int e = Row::expert(i, lane);
+    if (e < E) row[e] = x[i];
+  }
+  __syncwarp();
+  // A group's experts over 32 / groups lanes (rounded down to a power of two).
+  const int share = 1 << (31 - __clz(32 / r.groups)), size = E / r.groups, g = lane / share;
+  float one = -kInf, two = -kInf;
+  if (g < r.groups)
+    for (int i = lane % share; i < size; i += share) {
+      const float v = row[g * size + i];
+      two = fmaxf(two, fminf(one, v));
+      one = fmaxf(one, v);
+    }
+  for (int o = share >> 1; o > 0; o >>= 1) {
+    const float q1 = __shfl_xor_sync(kAll, one, o), q2 = __shfl_xor_sync(kAll, two, o);
+    two = fmaxf(fmaxf(two, q2), fminf(one, q1));
+    one = fmaxf(one, q1);
+  }
+  // one value a group, on its first lane
+  const bool mine = lane % share == 0 && one > -kInf;
+  uint32_t key = mine ? key_of(one + (two > -kInf ? two : 0.f)) : 0u, kept = 0, last = 0;
+  for (int j = 0; j < r.top_groups; ++j) {
+    const uint32_t best = __reduce_max_sync(kAll, key);
+    if (best == 0) break;
+    const int at = __ffs(__ballot_sync(kAll, key == best)) - 1;
+    kept |= 1u << (at / share);
+    last = best;
+    if (lane == at) key = 0;
+  }
+  const uint32_t next = __reduce_max_sync(kAll, key);
+  if (next != 0) {
+    const float a = value_of(last), b = value_of(next);
+    unsure = !(a - b > tolerance(r.score == MOE_SCORE_SIGMOID, 4.f * most, fabsf(a) + fabsf(b)));  // of four scores
+  }
+  return kept;
+}
+
+// CTAs that an SM holds (64 or 128 registers a thread).
+template <typename Row>
+constexpr int kResident = Row::width <= 16 ? 4 : 2;
+
+template <typename Row>
+__global__ void __launch_bounds__(32 * kWarps, kResident<Row>)
 route_kernel(const RouteLaunch a, const int group_inv) {
   using T = typename Row::type;
   constexpr int V = Row::width;
@@ -159,113 +246,98 @@ route_kernel(const RouteLaunch a, const int group_inv) {
   const int E = r.num_experts, k = r.top_k;
   const bool sigmoid = r.score == MOE_SCORE_SIGMOID;
   const bool by_logit = a.bias == nullptr;  // the choice within the groups is the logits' order
+  const bool by_score = !by_logit || r.groups > 1;
+  const int deep = by_logit ? k : k + 1;    // of the logits' order nothing is unsure
+  float bias[V];  // -inf: not to be chosen, whatever the score
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = Row::expert(i, lane);
+    const float b = e < E && a.bias ? __ldg(a.bias + e) : 0.f;
+    bias[i] = e < E && b == b ? b : -kInf;
+  }
   const int64_t rows = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp; t < a.n; t += rows) {
     const T* p = static_cast<const T*>(a.logits) + t * a.ld;
-    float l[V], s[V];
-    Row::load(p, E, lane, -kInf, l);
-    float top = l[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) top = max_nan(top, l[i]);
-    SoftmaxRow soft{0.f, 0.f};
-    if (!sigmoid) {
-      top = warp_max_nan(top);
-      soft = softmax_row(l, top, s);
-    } else if (!by_logit || r.groups > 1) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) s[i] = sigmoid_of(l[i]);
-    }
     int32_t* ids = a.ids + t * k;
     float* weight = a.weight + t * k;
-    if (__any_sync(kAll, top != top || (!sigmoid && top == kInf))) {
+    float x[V];
+    Row::load(p, E, lane, -kInf, x);
+    SoftmaxRow soft{0.f, 0.f};
+    bool bad = false, slow = false;
+    if (!sigmoid) {
+      float top = x[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) top = max_nan(top, x[i]);
+      top = warp_max_nan(top);
+      bad = !(top < kInf);
+      float s[V];
+      soft = softmax_row(x, top, s);
+      if (by_score) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = x[i] == -kInf ? -kInf : s[i] + bias[i];
+      }
+    } else if (by_score) {
+      float low = x[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) low = fminf(low, x[i]);
+      const bool masked = __any_sync(kAll, low == -kInf);
+      uint32_t off = 0;
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) off |= x[i] == -kInf ? 1u << i : 0u;
+      }
+      if (r.groups > 1) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = sigmoid_of(x[i]) + bias[i];
+      } else {
+        // Short scores: the exponent's rounding, 2^-24 of |l|, weighs s (1 - s) |l| < 2^-1; the two functions and the
+        // sum 2^-21 of s.
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          float e;
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504f * x[i]));
+          x[i] = reciprocal(1.0f + e) + bias[i];
+        }
+      }
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (off >> i & 1u) x[i] = -kInf;
+      }
+    }
+    const float most = sigmoid ? 1.f : soft.inv;  // no score is larger
+    float local = x[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) local = max_nan(local, x[i]);
+    bad |= local != local;
+    if (__any_sync(kAll, bad)) {
       if (lane < k) ids[lane] = -1, weight[lane] = kNaN;
       continue;
     }
-    const float most = sigmoid ? 1.f : soft.inv;  // no score is larger
-    uint32_t key[V];
-    uint32_t local = 0;
-    bool slow = false;
-    if (by_logit && r.groups == 1) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = key_if(true, l[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = Row::expert(i, lane);
-        key[i] = key_if(e < E && l[i] > -kInf, s[i] + (a.bias && e < E ? __ldg(a.bias + e) : 0.f));
-      }
-    }
     if (r.groups > 1) {
-      // A group's two largest: its experts over 32 / groups lanes (rounded down to a power of two).
-      float* row = group_row + warp * E;
-      __syncwarp();
+      const uint32_t kept = kept_groups<Row>(r, x, group_row + warp * E, most, slow);
+      if (by_logit) Row::load(p, E, lane, -kInf, x);
+      local = -kInf;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int e = Row::expert(i, lane);
-        if (e < E) row[e] = __uint_as_float(key[i]);
-      }
-      __syncwarp();
-      const int share = 1 << (31 - __clz(32 / r.groups)), size = E / r.groups;
-      const int g = lane / share, first = g * size;
-      uint32_t one = 0, two = 0;
-      if (g < r.groups)
-        for (int i = lane % share; i < size; i += share) {
-          const uint32_t v = __float_as_uint(row[first + i]);
-          two = max(two, min(one, v));
-          one = max(one, v);
-        }
-      for (int o = share >> 1; o > 0; o >>= 1) {
-        const uint32_t q1 = __shfl_xor_sync(kAll, one, o), q2 = __shfl_xor_sync(kAll, two, o);
-        two = max(max(two, q2), min(one, q1));
-        one = max(one, q1);
-      }
-      // one value a group, on its first lane
-      const bool mine = lane % share == 0 && one != 0;
-      const float sum = mine ? value_of(one) + (two ? value_of(two) : 0.f) : 0.f;
-      uint32_t gk = mine ? key_of(sum) : 0u, kept = 0, last = 0;
-      for (int j = 0; j < r.top_groups; ++j) {
-        const uint32_t best = __reduce_max_sync(kAll, gk);
-        if (best == 0) break;
-        const int at = __ffs(__ballot_sync(kAll, gk == best)) - 1;
-        kept |= 1u << (at / share);
-        last = best;
-        if (lane == at) gk = 0;
-      }
-      const uint32_t next = __reduce_max_sync(kAll, gk);
-      if (next != 0) {
-        const float x = value_of(last), y = value_of(next);
-        const float size_of = fabsf(x) + fabsf(y);
-        slow = !(x - y > tolerance(sigmoid, 4.f * most, size_of));  // of four scores
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = Row::expert(i, lane);
-        if (!(kept >> ((e * group_inv >> 20) & 31) & 1u)) key[i] = 0u;
-        else if (by_logit) key[i] = key_if(e < E, l[i]);
+        if (e >= E || !(kept >> ((e * group_inv >> 20) & 31) & 1u)) x[i] = -kInf;
+        local = fmaxf(local, x[i]);
       }
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) local = max(local, key[i]);
-    // the (k + 1)-th largest of the lanes' largest (by logits the k-th: their order needs no margin)
-    const int deep = by_logit ? k : k + 1;
-    uint32_t from = 0;
-    if (deep <= 32) {
-      uint32_t left = local;
-      for (int j = 0; j < deep; ++j) {
-        from = __reduce_max_sync(kAll, left);
-        if (from == 0) break;
-        if (left == from) left = 0;
-      }
+    // the k + 1st largest of the lanes' largest, less the margin of the short scores (twice their error)
+    uint32_t from = 0, left = key_if(true, local);
+    for (int j = 0; j < deep; ++j) {
+      from = __reduce_max_sync(kAll, left);
+      if (from == 0) break;
+      if (left == from) left = 0;
     }
-    if (!by_logit && from != 0) {
-      const float x = value_of(from);
-      const float low = x - tolerance(sigmoid, most, x);
-      from = low > -kInf ? key_of(low) : 1u;
-    }
-    from = max(from, 1u);
+    float low = from != 0 && deep <= 32 ? value_of(from) : -kInf;
+    if (!by_logit) low -= fmaf(0x1p-21f, fabsf(low), fmaxf(0x1p-18f, tolerance(sigmoid, most, 0.f)));
+    if (!(low > -kInf)) low = -3.4028234663852886e38f;  // all that can be chosen
     uint32_t mask = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) mask |= key[i] >= from ? 1u << i : 0u;
+    for (int i = 0; i < V; ++i) mask |= x[i] >= low ? 1u << i : 0u;
     int found = 0;
     for (uint32_t who; (who = __ballot_sync(kAll, mask != 0)) != 0;) {
       if (mask != 0) {
@@ -276,78 +348,50 @@ route_kernel(const RouteLaunch a, const int group_inv) {
       found += __popc(who);
     }
     __syncwarp();
-    // one of them to a lane
-    const int e = lane < min(found, 32) ? list[warp][lane] : -1;
-    __syncwarp();
-    float cl = -kInf, cb = 0.f, cs = 0.f, cx = 0.f;
-    if (e >= 0) {
-      cl = to_float(p[e]);
-      cs = sigmoid ? sigmoid_of(cl) : expf(cl - soft.shift) * soft.inv;
-      if (a.bias) cb = __ldg(a.bias + e);
-      cx = by_logit ? cl : cs + cb;
-    }
-    int id = -1, src = 0;
-    float w = 0.f;
     if (found > 32) slow = true;
+    int id = -1, rank = lane;
+    float w = 0.f;
     if (!slow) {
-      uint32_t ck = e >= 0 ? key_of(cx) : 0u, got = 0;
-      for (int j = 0; j < deep; ++j) {
-        const uint32_t best = __reduce_max_sync(kAll, ck);
-        if (best == 0) break;
-        const int first = __reduce_min_sync(kAll, ck == best ? e : 0x7fffffff);
-        const int at = __ffs(__ballot_sync(kAll, e == first)) - 1;
-        if (lane == j) id = first, src = at, got = best;
-        if (lane == at) ck = 0;
+      // one of them to a lane
+      id = lane < found ? list[warp][lane] : -1;
+      float l = -kInf, b = 0.f, y = 0.f;
+      uint32_t key = 0;
+      if (id >= 0) {
+        l = to_float(p[id]);
+        w = sigmoid ? sigmoid_of(l) : softmax_term(l, soft.shift) * soft.inv;
+        if (!by_logit) b = __ldg(a.bias + id);
+        y = by_logit ? l : w + b;
+        key = key_of(y);
       }
+      uint32_t next;
+      rank = rank_of(key, id, found, next);
       if (!by_logit) {
-        // lane j against the one behind it (lane 32 is not asked: deep is at most 32 here)
-        const float x = value_of(got), sj = __shfl_sync(kAll, cs, src), lj = __shfl_sync(kAll, cl, src),
-                    bj = __shfl_sync(kAll, cb, src);
-        const uint32_t got1 = __shfl_down_sync(kAll, got, 1);
-        const float s1 = __shfl_down_sync(kAll, sj, 1), l1 = __shfl_down_sync(kAll, lj, 1),
-                    b1 = __shfl_down_sync(kAll, bj, 1);
-        const bool close = lane < k && lane < 31 && got != 0 && got1 != 0 && !(lj == l1 && bj == b1) &&
-                           !(x - value_of(got1) > tolerance(sigmoid, fmaxf(sj, s1), fabsf(x) + fabsf(value_of(got1))));
-        if (__any_sync(kAll, close)) {
-          // the same values in 64 bits
-          double total = 0.0;
-          if (!sigmoid) {
-#pragma unroll 1
-            for (int i = 0; i < V; ++i) {
-              const int at = Row::expert(i, lane);
-              if (at < E) total += exp(static_cast<double>(to_float(p[at])) - static_cast<double>(soft.shift));
-            }
-            total = warp_sum(total);
-          }
-          Best mine{0.0, e};
-          if (e >= 0)
-            mine.x = (sigmoid ? exact_sigmoid(cl) : exact_softmax(cl, soft.shift, total)) + static_cast<double>(cb);
-          id = -1;
-          for (int j = 0; j < k; ++j) {
-            const Best b = warp_best(mine);
-            if (b.e < 0) break;
-            const int at = __ffs(__ballot_sync(kAll, e == b.e)) - 1;
-            if (lane == j) id = b.e, src = at;
-            if (lane == at) mine.e = -1;
-          }
+        // the one in front, where both are not behind the k + 1st
+        bool close = id >= 0 && rank <= k && next != 0xffffffffu &&
+                     !(value_of(next) - y > tolerance(sigmoid, most, fabsf(y) + fabsf(value_of(next))));
+        const uint32_t same = __match_any_sync(kAll, key);
+        if (__any_sync(kAll, id >= 0 && (same & (same - 1u)) != 0)) {
+          // equal values: of the same inputs, or not known to be equal
+          const int first = __ffs(same) - 1;
+          const float l0 = __shfl_sync(kAll, l, first), b0 = __shfl_sync(kAll, b, first);
+          close |= id >= 0 && rank <= k && !(l == l0 && b == b0);
         }
+        if (__any_sync(kAll, close))
+          rank = exact_rank<Row>(p, E, sigmoid, soft.shift, l, b, id, found);
       }
-      w = __shfl_sync(kAll, cs, src);
-      if (lane >= k || id < 0) id = -1, w = 0.f;
+      if (id < 0) rank = lane;  // behind those that were found
+      if (rank >= k) w = 0.f;
     } else {
       id = exact_choice<Row>(r, p, a.bias, group_inv, lane);
       if (lane >= k) id = -1;
       if (id >= 0) {
-        const float li = to_float(p[id]);
-        w = sigmoid ? sigmoid_of(li) : expf(li - soft.shift) * soft.inv;
+        const float l = to_float(p[id]);
+        w = sigmoid ? sigmoid_of(l) : softmax_term(l, soft.shift) * soft.inv;
       }
     }
-    if (r.normalise) {
-      // in fp32, over the chosen ones
-      const float sum = warp_sum(w) + kTiny;
-      w = __fdiv_rn(w, sum);
-    }
-    if (lane < k) ids[lane] = id, weight[lane] = w * r.scale;
+    __syncwarp();  // the list is read
+    if (r.normalise) w = __fdiv_rn(w, warp_sum(w) + kTiny);
+    if (rank < k) ids[rank] = id, weight[rank] = w * r.scale;
   }
 }
 
@@ -360,9 +404,10 @@ cudaError_t launch_route(const RouteLaunch& a, cudaStream_t s) {
   if (sms <= 0) return cudaErrorInvalidValue;
   int warps = 1;
   while (warps < kWarps && a.n > sms * warps) warps *= 2;
-  const int64_t ctas = (a.n + warps - 1) / warps, most = sms * 16;
+  const int64_t ctas = (a.n + warps - 1) / warps;
   const size_t smem = a.r.groups > 1 ? static_cast<size_t>(warps) * a.r.num_experts * sizeof(float) : 0;
   return with_row(a.r, rows_by_four(a.r, a.logits, a.ld), [&](auto row) {
+    const int64_t most = sms * kResident<decltype(row)> * kWarps / warps;
     return launch_maybe_overlapped(route_kernel<decltype(row)>, static_cast<int>(ctas < most ? ctas : most), 32 * warps, smem,
                                    s, true, a, inv);
   });

@@ -91,14 +91,45 @@ __device__ __forceinline__ float warp_max_nan(float v) {
   return v;
 }
 
-// 1 / (1 + e^-l); the fast reciprocal is within an ulp, and 0 where e^-l passes 2^126.
-__device__ __forceinline__ float sigmoid_of(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
+// e^x for -128 <= x <= 88.1 (0 below -87.3): 2^h (1 + r) with h = x log2(e) rounded to a float and r = x - h ln(2), which
+// two FMAs get from h in two parts of ln(2).  |r| is below 2^-17, so 1 + r is e^r to 2^-35; ex2.approx is within 2^-22:
+// together 2^-22 + 2^-24 of the value.
+__device__ __forceinline__ float exp_of(float x) {
+  constexpr float kLog2E = 1.44269504f, kLn2Hi = 0.693147182f, kLn2Lo = -1.90465421e-9f;
+  const float h = x * kLog2E;
+  const float r = fmaf(-h, kLn2Lo, fmaf(-h, kLn2Hi, x));
+  float t;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(h));
+  return fmaf(t, r, t);
+}
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
-// What a row's softmax needs of the whole row: score = exp(l - shift) * inv.  A row of -inf alone has
+// 1 / (1 + e^-l), NaN of a NaN; t gets e^-l, never infinite.  From -88.1 down t is above 2^127 and its reciprocal is
+// flushed to 0.  The reciprocal is within an ulp: together below 2^-21 of the score.
+__device__ __forceinline__ float sigmoid_of(float l, float& t) {
+  t = exp_of(-min_nan(max_nan(l, -88.1f), 128.f));
+  return reciprocal(1.0f + t);
+}
+__device__ __forceinline__ float sigmoid_of(float l) {
+  float t;
+  return sigmoid_of(l, t);
+}
+
+// What a row's softmax needs of the whole row: score = e^(l - shift) inv.  A row of -inf alone has
 // shift 0 and scores 0.
 struct SoftmaxRow {
   float shift, inv;
 };
+__device__ __forceinline__ float softmax_term(float l, float shift) { return exp_of(max_nan(l - shift, -128.f)); }
 template <int V>
 __device__ __forceinline__ SoftmaxRow softmax_row(const float (&l)[V], float top, float (&s)[V]) {
   SoftmaxRow r;
@@ -106,11 +137,11 @@ __device__ __forceinline__ SoftmaxRow softmax_row(const float (&l)[V], float top
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    s[i] = expf(l[i] - r.shift);
+    s[i] = softmax_term(l[i], r.shift);
     sum += s[i];
   }
   sum = warp_sum(sum);
-  r.inv = sum > 0.f ? __frcp_rn(sum) : 0.f;
+  r.inv = sum == 0.f ? 0.f : __frcp_rn(sum);
 #pragma unroll
   for (int i = 0; i < V; ++i) s[i] *= r.inv;
   return r;
