@@ -25,33 +25,33 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRowWarps = 8;
 constexpr float kTiny = 1e-20f;
 
-// The shares q of a row (sum 1, or all 0 where every logit is -inf).
+// The scores of a row and what makes shares of them (0 where every logit is -inf).
 template <typename Row>
-__device__ __forceinline__ void shares(bool sigmoid, const float (&l)[Row::width], float (&q)[Row::width]) {
+__device__ __forceinline__ float share_scores(bool sigmoid, const float (&l)[Row::width], float2 (&s)[Row::width / 2]) {
   constexpr int V = Row::width;
-  if (sigmoid) {
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      q[i] = sigmoid_of(l[i]);
-      sum += q[i];
-    }
-    sum = warp_sum(sum);
-    const float inv = sum == 0.f ? 0.f : __frcp_rn(sum);  // (a masked row's shares are 0)
-#pragma unroll
-    for (int i = 0; i < V; ++i) q[i] *= inv;
-  } else {
+  float shift = 0.f;
+  if (!sigmoid) {
     float top = l[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) top = max_nan(top, l[i]);
-    softmax_row(l, warp_max_nan(top), q);
+    top = warp_max_nan(top);
+    shift = top == -kInf ? 0.f : top;
   }
+  float2 sum = both(0.f);
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    const float2 v = make_float2(l[2 * i], l[2 * i + 1]);
+    s[i] = sigmoid ? sigmoid_of(v) : softmax_term(v, shift);
+    sum = add2(sum, s[i]);
+  }
+  const float total = warp_sum(sum.x + sum.y);
+  return total == 0.f ? 0.f : __frcp_rn(total);
 }
 
 // Row ranges of sequence s, held within [0, n] whatever the offsets say.
 __device__ __forceinline__ int64_t offset_at(const int32_t* offsets, int64_t n, int s) {
   if (!offsets) return s == 0 ? 0 : n;
-  const int64_t o = __ldg(offsets + s);
+  const int64_t o = offsets[s];
   return o < 0 ? 0 : o > n ? n : o;
 }
 // The first sequence that ends behind row t (the number of sequences: none).
@@ -65,46 +65,60 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int sequences
   return lo;
 }
 
+// The offsets in shared memory where they fit (one read of all instead of one behind the other).
+constexpr int kHeld = 1025;
+__device__ __forceinline__ const int32_t* hold_offsets(const int32_t* offsets, int sequences, int32_t* held) {
+  if (!offsets || sequences + 1 > kHeld) return offsets;
+  for (int i = threadIdx.x; i <= sequences; i += blockDim.x) held[i] = __ldg(offsets + i);
+  return held;
+}
+
 template <typename Row>
 __global__ void __launch_bounds__(32 * kRowWarps, Row::width <= 12 ? 4 : 1)
 balance_rows_kernel(const BalanceLaunch a, const BalancePlan plan) {
   using T = typename Row::type;
   constexpr int V = Row::width;
+  __shared__ int32_t held[kHeld];
   extern __shared__ float joined[];  // [warps][E], then the counts [E]
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = a.r.num_experts, k = a.r.top_k;
   const bool sigmoid = a.r.score == MOE_SCORE_SIGMOID;
+  const int64_t r0 = blockIdx.x * plan.chunk, r1 = min(r0 + plan.chunk, a.n);
+  const T* logits = static_cast<const T*>(a.logits);
+  float l[V];  // the next row's, read a row ahead
+  if (r0 + warp < r1) Row::load(logits + (r0 + warp) * a.ld, E, lane, -kInf, l);
+  const int32_t* offsets = hold_offsets(a.offsets, a.sequences, held);
   int32_t* hist = reinterpret_cast<int32_t*>(joined + kRowWarps * E);
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
   for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
-  const int64_t r0 = blockIdx.x * plan.chunk, r1 = min(r0 + plan.chunk, a.n);
   __syncthreads();
-  for (int s = sequence_of(a.offsets, a.sequences, a.n, r0); s < a.sequences; ++s) {
-    const int64_t lo = max(r0, offset_at(a.offsets, a.n, s)), hi = min(r1, offset_at(a.offsets, a.n, s + 1));
+  int64_t t = r0 + warp;  // l's row
+  for (int s = sequence_of(offsets, a.sequences, a.n, r0); s < a.sequences; ++s) {
+    const int64_t lo = max(r0, offset_at(offsets, a.n, s)), hi = min(r1, offset_at(offsets, a.n, s + 1));
     if (lo >= r1) break;
     if (lo >= hi) continue;
-    float sum[V];
+    float2 sum[V / 2];
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum[i] = 0.f;
-    const T* logits = static_cast<const T*>(a.logits);
-    float l[V];
-    if (lo + warp < hi) Row::load(logits + (lo + warp) * a.ld, E, lane, -kInf, l);
-    for (int64_t t = lo + warp; t < hi; t += kRowWarps) {
-      float q[V];
-      shares<Row>(sigmoid, l, q);
-      if (t + kRowWarps < hi) Row::load(logits + (t + kRowWarps) * a.ld, E, lane, -kInf, l);
-      if (lane < k) {
+    for (int i = 0; i < V / 2; ++i) sum[i] = both(0.f);
+    for (; t < hi; t += kRowWarps) {
+      const bool in = t >= lo;  // (rows in front of the first sequence are not)
+      if (in && lane < k) {
         const int id = a.ids[t * k + lane];
         if (id >= 0 && id < E) atomicAdd(hist + id, 1);
       }
+      float2 q[V / 2];
+      const float inv = share_scores<Row>(sigmoid, l, q);
+      if (t + kRowWarps < r1) Row::load(logits + (t + kRowWarps) * a.ld, E, lane, -kInf, l);
+      if (in) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum[i] += q[i];
+        for (int i = 0; i < V / 2; ++i) sum[i] = fma2(q[i], both(inv), sum[i]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (Row::expert(i, lane) < E) joined[warp * E + Row::expert(i, lane)] = sum[i];
+      if (Row::expert(i, lane) < E) joined[warp * E + Row::expert(i, lane)] = i & 1 ? sum[i >> 1].y : sum[i >> 1].x;
     __syncthreads();
     const int64_t piece = static_cast<int64_t>(blockIdx.x) + s;
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
@@ -124,8 +138,6 @@ __global__ void __launch_bounds__(256)
 balance_loss_kernel(const BalanceLaunch a, const BalancePlan plan) {
   __shared__ float psum[8][32];
   __shared__ int pcount[8][32];
-  __shared__ double total[8];
-  __shared__ int lives[8];
   __shared__ bool last;
   pdl_wait();
   pdl_launch_dependents();
@@ -137,11 +149,13 @@ balance_loss_kernel(const BalanceLaunch a, const BalancePlan plan) {
     float sum = 0.f;
     int count = 0;
     if (lo < hi && e < E) {
-      const int64_t c1 = (hi - 1) / plan.chunk;
-#pragma unroll 4
-      for (int64_t c = lo / plan.chunk + warp; c <= c1; c += 8) {
-        sum += a.sums[(c + s) * E + e];
-        count += a.hist[(c + s) * E + e];
+      const uint32_t chunk = static_cast<uint32_t>(plan.chunk);  // (rows and runs are below 2^31)
+      const int c0 = static_cast<int>(static_cast<uint32_t>(lo) / chunk), c1 = static_cast<int>((static_cast<uint32_t>(hi) - 1) / chunk);
+#pragma unroll 8
+      for (int c = c0 + warp; c <= c1; c += 8) {
+        const int64_t at = static_cast<int64_t>(c + s) * E + e;
+        sum += a.sums[at];
+        count += a.hist[at];
       }
     }
     psum[warp][lane] = sum;
@@ -165,7 +179,7 @@ balance_loss_kernel(const BalanceLaunch a, const BalancePlan plan) {
   __syncthreads();
   if (!last) return;
   __threadfence();
-  double sum = 0.0;
+  float sum = 0.f;
   int live = 0;
   bool bad = false;  // offsets that do not ascend within the rows
   for (int s = threadIdx.x; s < a.sequences; s += blockDim.x) {
@@ -176,23 +190,21 @@ balance_loss_kernel(const BalanceLaunch a, const BalancePlan plan) {
     if (offset_at(a.offsets, a.n, s + 1) <= offset_at(a.offsets, a.n, s)) continue;
     ++live;
     float part = 0.f;
+#pragma unroll 4
     for (int i = 0; i < parts; ++i) part += __ldcg(a.parts + static_cast<int64_t>(s) * parts + i);
     sum += part;
   }
   bad = __syncthreads_or(bad);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    sum += __shfl_xor_sync(kAll, sum, o);
-    live += __shfl_xor_sync(kAll, live, o);
-  }
-  if (lane == 0) total[warp] = sum, lives[warp] = live;
+  sum = warp_sum(sum);
+  live = __reduce_add_sync(kAll, live);
+  if (lane == 0) psum[0][warp] = sum, pcount[0][warp] = live;
   __syncthreads();
   if (threadIdx.x == 0) {
-    sum = 0.0;
+    sum = 0.f;
     live = 0;
-    for (int w = 0; w < 8; ++w) sum += total[w], live += lives[w];
-    const double factor = static_cast<double>(a.coef) * E / a.r.top_k;
-    *a.loss = bad ? kNaN : live ? static_cast<float>(sum * factor / live) : 0.f;
+    for (int w = 0; w < 8; ++w) sum += psum[0][w], live += pcount[0][w];
+    const float factor = a.coef * static_cast<float>(E) / (static_cast<float>(a.r.top_k) * static_cast<float>(live));
+    *a.loss = bad ? kNaN : live ? sum * factor : 0.f;
   }
 }
 
@@ -207,18 +219,21 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
   constexpr int V = Row::width;
   extern __shared__ float scatter[];  // [warps][E]: ds at the chosen experts, zeros elsewhere
   __shared__ int lives[kRowWarps];
+  __shared__ int32_t held[kHeld];
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = a.r.num_experts, k = a.r.top_k;
   const bool sigmoid = a.r.score == MOE_SCORE_SIGMOID;
+  const int32_t* offsets = a.counts ? hold_offsets(a.offsets, a.sequences, held) : nullptr;
   float* ds = scatter + warp * E;
   for (int e = lane; e < E; e += 32) ds[e] = 0.f;
   float factor = 0.f;  // d_loss coef E / (S k)
   if (a.counts) {
+    __syncthreads();
     int live = 0;
     for (int s = threadIdx.x; s < a.sequences; s += blockDim.x)
-      live += offset_at(a.offsets, a.n, s + 1) > offset_at(a.offsets, a.n, s) ? 1 : 0;
+      live += offset_at(offsets, a.n, s + 1) > offset_at(offsets, a.n, s) ? 1 : 0;
     live = __reduce_add_sync(kAll, live);
     if (lane == 0) lives[warp] = live;
     __syncthreads();
@@ -231,61 +246,81 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
   const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp) * run, t1 = min(t0 + run, a.n);
   if (t0 >= t1) return;
   const T* logits = static_cast<const T*>(a.logits);
-  float c[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) c[i] = 0.f;
-  int seq = a.counts ? sequence_of(a.offsets, a.sequences, a.n, t0) : 0;
-  int64_t until = t0;  // where c changes next
-  for (int64_t t = t0; t < t1; ++t) {
-    const T* p = logits + t * a.ld;
-    float l[V];
-    Row::load(p, E, lane, -kInf, l);
-    int id = -1;
-    float g = 0.f, lj = -kInf;
+  // The next row, read a row ahead: its logits, its chosen experts (one a lane, -1: none) and their weights' gradients.
+  float l[V];
+  int next_id = -1;
+  float next_g = 0.f;
+  auto read = [&](int64_t t) {
+    Row::load(logits + t * a.ld, E, lane, -kInf, l);
     if (a.d_weight && lane < k) {
-      id = a.ids[t * k + lane];
-      if (id < 0 || id >= E) id = -1;
-      else g = a.d_weight[t * k + lane] * a.r.scale, lj = to_float(p[id]);
+      next_id = a.ids[t * k + lane];
+      next_g = a.d_weight[t * k + lane];
+      if (next_id < 0 || next_id >= E) next_id = -1, next_g = 0.f;
     }
+  };
+  read(t0);
+  float2 c[V / 2];
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) c[i] = both(0.f);
+  int seq = a.counts ? sequence_of(offsets, a.sequences, a.n, t0) : 0;
+  int64_t until = t0;  // where c changes next
+#pragma unroll 1
+  for (int64_t t = t0; t < t1; ++t) {
+    const int id = next_id;
+    const float g = next_g * a.r.scale;
+    const float lj = id >= 0 ? to_float(logits[t * a.ld + id]) : -kInf;
     if (a.counts && t >= until) {
       // sequences that end at or in front of t are over; between two (and behind the last) there are none
-      while (seq < a.sequences && offset_at(a.offsets, a.n, seq + 1) <= t) ++seq;
-      const int64_t lo = seq < a.sequences ? offset_at(a.offsets, a.n, seq) : a.n,
-                    hi = seq < a.sequences ? offset_at(a.offsets, a.n, seq + 1) : a.n;
+      while (seq < a.sequences && offset_at(offsets, a.n, seq + 1) <= t) ++seq;
+      const int64_t lo = seq < a.sequences ? offset_at(offsets, a.n, seq) : a.n,
+                    hi = seq < a.sequences ? offset_at(offsets, a.n, seq + 1) : a.n;
       const bool in = lo <= t && t < hi;
       const float rows = static_cast<float>(hi - lo), f = in ? factor / (rows * rows) : 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = Row::expert(i, lane);
-        c[i] = in && e < E ? f * static_cast<float>(__ldg(a.counts + static_cast<int64_t>(seq) * E + e)) : 0.f;
+      for (int i = 0; i < V / 2; ++i) {
+        const int e0 = Row::expert(2 * i, lane), e1 = Row::expert(2 * i + 1, lane);
+        const int32_t* p = a.counts + static_cast<int64_t>(seq) * E;
+        c[i].x = in && e0 < E ? f * static_cast<float>(__ldg(p + e0)) : 0.f;
+        c[i].y = in && e1 < E ? f * static_cast<float>(__ldg(p + e1)) : 0.f;
       }
       until = in ? hi : lo > t ? lo : a.n;
     }
-    float s[V], u[V];  // scores; sigmoid: e^-l s = 1 - s
-    float dj;  // ds of the lane's chosen expert
-    float top = l[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) top = max_nan(top, l[i]);
-    SoftmaxRow soft{0.f, 0.f};
-    float total = 0.f;
+    // v: what the bracket of the gradient's formula is multiplied by
+    float2 v[V / 2], total2 = both(0.f), dot2 = both(0.f);
+    float top = -kInf, shift = 0.f;
     if (sigmoid) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        s[i] = sigmoid_of(l[i], u[i]);
-        u[i] *= s[i];
-        total += s[i];
+      for (int i = 0; i < V / 2; ++i) {
+        float2 t2;
+        const float2 s = sigmoid_of(make_float2(l[2 * i], l[2 * i + 1]), t2);
+        total2 = add2(total2, s);
+        dot2 = fma2(c[i], s, dot2);
+        v[i] = mul2(mul2(t2, s), s);  // s (1 - s): e^-l s is 1 - s
       }
     } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) top = max_nan(top, l[i]);
       top = warp_max_nan(top);
-      soft = softmax_row(l, top, s);
+      shift = top == -kInf ? 0.f : top;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        v[i] = softmax_term(make_float2(l[2 * i], l[2 * i + 1]), shift);
+        total2 = add2(total2, v[i]);
+        dot2 = fma2(c[i], v[i], dot2);
+      }
     }
-    const bool bad = __any_sync(kAll, top != top || (!sigmoid && top == kInf));
+    if (t + 1 < t1) read(t + 1);
+    const float total = warp_sum(total2.x + total2.y), inv = total == 0.f ? 0.f : __frcp_rn(total);
+    // (NaN of a row that holds one: total is)
+    const bool bad = total != total;
+    float dot = dot2.x + dot2.y, dj = 0.f;  // dj: ds of the lane's chosen expert
+    const float sj = sigmoid ? sigmoid_of(lj) : softmax_term(lj, shift) * inv;
     if (a.d_weight) {
       dj = g;
       if (a.r.normalise) {
-        const float sj = id < 0 ? 0.f : sigmoid ? sigmoid_of(lj) : softmax_term(lj, soft.shift) * soft.inv;
-        const float sum = warp_sum(sj) + kTiny, dot = warp_sum(g * sj);
-        dj = __fdividef(g - __fdividef(dot, sum), sum);
+        const float chosen = id >= 0 ? sj : 0.f;
+        const float sum = warp_sum(chosen) + kTiny, with = warp_sum(g * chosen);
+        dj = __fdividef(g - __fdividef(with, sum), sum);
       }
       const uint32_t same = __match_any_sync(kAll, id);
       if (__any_sync(kAll, id >= 0 && (same & (same - 1u)) != 0)) {
@@ -299,39 +334,31 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
       }
       __syncwarp();
     }
-    float d[V];
-    float dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = Row::expert(i, lane);
-      d[i] = a.d_weight && e < E ? ds[e] : 0.f;
-    }
-    if (a.d_weight) {
-      __syncwarp();
-      if (id >= 0) ds[id] = 0.f;
-    }
+    // d = (c scale + rest + ds) v
+    float scale = 0.f, rest = 0.f;
     if (sigmoid) {
       if (a.counts) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) dot = fmaf(c[i], s[i], dot);
-        total = warp_sum(total);
-        dot = warp_sum(dot);
-        const float inv = total == 0.f ? 0.f : __frcp_rn(total);
-        dot *= inv;
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = fmaf(c[i] - dot, inv, d[i]);
+        dot = warp_sum(dot) * inv;
+        scale = inv;
+        rest = -dot * inv;
       }
-#pragma unroll
-      for (int i = 0; i < V; ++i) d[i] = d[i] * s[i] * u[i];
     } else {
+      // of the shares: v inv
+      dot = warp_sum(fmaf(dot, inv, id >= 0 ? dj * sj : 0.f));
+      scale = inv;
+      rest = -dot * inv;
+    }
+    const float ds_scale = sigmoid ? 1.f : inv;
+    float d[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        d[i] += c[i];
-        dot = fmaf(d[i], s[i], dot);
+    for (int i = 0; i < V / 2; ++i) {
+      float2 w = fma2(c[i], both(scale), both(rest));
+      if (a.d_weight) {
+        const int e0 = Row::expert(2 * i, lane), e1 = Row::expert(2 * i + 1, lane);
+        w = fma2(make_float2(e0 < E ? ds[e0] : 0.f, e1 < E ? ds[e1] : 0.f), both(ds_scale), w);
       }
-      dot = warp_sum(dot);
-#pragma unroll
-      for (int i = 0; i < V; ++i) d[i] = s[i] * (d[i] - dot);
+      w = mul2(w, v[i]);
+      d[2 * i] = w.x, d[2 * i + 1] = w.y;
     }
     if (bad) {
 #pragma unroll
@@ -339,14 +366,16 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
     }
     Row::store(static_cast<T*>(a.d_logits) + t * a.d_ld, E, lane, d);
     __syncwarp();
+    if (id >= 0) ds[id] = 0.f;
+    __syncwarp();
   }
 }
 
 }  // namespace
 
 BalancePlan balance_plan(int64_t n) {
-  // Runs of eight rows a warp at least, four CTAs an SM at most.
-  constexpr int64_t kMost = 608, kLeast = 64;
+  // A row a warp at least, four CTAs an SM at most.
+  constexpr int64_t kMost = 608, kLeast = 8;
   int64_t chunk = (n + kMost - 1) / kMost;
   if (chunk < kLeast) chunk = kLeast;
   if (chunk > n) chunk = n < 1 ? 1 : n;

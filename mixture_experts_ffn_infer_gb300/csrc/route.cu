@@ -286,18 +286,21 @@ route_kernel(const RouteLaunch a, const int group_inv) {
 #pragma unroll
         for (int i = 0; i < V; ++i) off |= x[i] == -kInf ? 1u << i : 0u;
       }
-      if (r.groups > 1) {
+      // Short scores (without groups): the exponent's rounding, 2^-24 of |l|, weighs s (1 - s) |l| < 2^-1; the two
+      // functions and the sum 2^-21 of s.
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = sigmoid_of(x[i]) + bias[i];
-      } else {
-        // Short scores: the exponent's rounding, 2^-24 of |l|, weighs s (1 - s) |l| < 2^-1; the two functions and the
-        // sum 2^-21 of s.
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          float e;
-          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504f * x[i]));
-          x[i] = reciprocal(1.0f + e) + bias[i];
+      for (int i = 0; i < V; i += 2) {
+        const float2 l = make_float2(x[i], x[i + 1]);
+        float2 s;
+        if (r.groups > 1) {
+          s = sigmoid_of(l);
+        } else {
+          const float2 h = mul2(l, both(-1.44269504f));
+          const float2 d = add2(both(1.0f), make_float2(exp2_approx(h.x), exp2_approx(h.y)));
+          s = make_float2(reciprocal(d.x), reciprocal(d.y));
         }
+        s = add2(s, make_float2(bias[i], bias[i + 1]));
+        x[i] = s.x, x[i + 1] = s.y;
       }
       if (masked) {
 #pragma unroll

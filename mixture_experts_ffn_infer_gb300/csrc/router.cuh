@@ -91,16 +91,34 @@ __device__ __forceinline__ float warp_max_nan(float v) {
   return v;
 }
 
-// e^x for -128 <= x <= 88.1 (0 below -87.3): 2^h (1 + r) with h = x log2(e) rounded to a float and r = x - h ln(2), which
-// two FMAs get from h in two parts of ln(2).  |r| is below 2^-17, so 1 + r is e^r to 2^-35; ex2.approx is within 2^-22:
-// together 2^-22 + 2^-24 of the value.
-__device__ __forceinline__ float exp_of(float x) {
-  constexpr float kLog2E = 1.44269504f, kLn2Hi = 0.693147182f, kLn2Lo = -1.90465421e-9f;
-  const float h = x * kLog2E;
-  const float r = fmaf(-h, kLn2Lo, fmaf(-h, kLn2Hi, x));
+// Two values at a time (each rounded as one alone would be): an issue slot for both.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
+        "l"(reinterpret_cast<const unsigned long long&>(c)));
+  return reinterpret_cast<const float2&>(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return reinterpret_cast<const float2&>(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return reinterpret_cast<const float2&>(d);
+}
+__device__ __forceinline__ float exp2_approx(float h) {
   float t;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(h));
-  return fmaf(t, r, t);
+  return t;
 }
 __device__ __forceinline__ float reciprocal(float v) {
   float r;
@@ -113,35 +131,53 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return r;
 }
 
+// e^x for -128 <= x <= 88.1 (0 below -87.3): 2^h (1 + r) with h = x log2(e) rounded to a float and r = x - h ln(2), which
+// two FMAs get from h in two parts of ln(2).  |r| is below 2^-17, so 1 + r is e^r to 2^-35; ex2.approx is within 2^-22:
+// together 2^-22 + 2^-24 of the value.
+__device__ __forceinline__ float2 exp_of(float2 x) {
+  constexpr float kLog2E = 1.44269504f, kLn2Hi = 0.693147182f, kLn2Lo = -1.90465421e-9f;
+  const float2 h = mul2(x, both(kLog2E));
+  const float2 r = fma2(h, both(-kLn2Lo), fma2(h, both(-kLn2Hi), x));
+  const float2 t = make_float2(exp2_approx(h.x), exp2_approx(h.y));
+  return fma2(t, r, t);
+}
+
 // 1 / (1 + e^-l), NaN of a NaN; t gets e^-l, never infinite.  From -88.1 down t is above 2^127 and its reciprocal is
 // flushed to 0.  The reciprocal is within an ulp: together below 2^-21 of the score.
-__device__ __forceinline__ float sigmoid_of(float l, float& t) {
-  t = exp_of(-min_nan(max_nan(l, -88.1f), 128.f));
-  return reciprocal(1.0f + t);
+__device__ __forceinline__ float2 sigmoid_of(float2 l, float2& t) {
+  t = exp_of(make_float2(max_nan(min_nan(-l.x, 88.1f), -128.f), max_nan(min_nan(-l.y, 88.1f), -128.f)));
+  const float2 d = add2(both(1.0f), t);
+  return make_float2(reciprocal(d.x), reciprocal(d.y));
 }
-__device__ __forceinline__ float sigmoid_of(float l) {
-  float t;
+__device__ __forceinline__ float2 sigmoid_of(float2 l) {
+  float2 t;
   return sigmoid_of(l, t);
 }
+__device__ __forceinline__ float sigmoid_of(float l) { return sigmoid_of(both(l)).x; }
 
 // What a row's softmax needs of the whole row: score = e^(l - shift) inv.  A row of -inf alone has
 // shift 0 and scores 0.
 struct SoftmaxRow {
   float shift, inv;
 };
-__device__ __forceinline__ float softmax_term(float l, float shift) { return exp_of(max_nan(l - shift, -128.f)); }
+__device__ __forceinline__ float2 softmax_term(float2 l, float shift) {
+  const float2 x = add2(l, both(-shift));
+  return exp_of(make_float2(max_nan(x.x, -128.f), max_nan(x.y, -128.f)));
+}
+__device__ __forceinline__ float softmax_term(float l, float shift) { return softmax_term(both(l), shift).x; }
 template <int V>
 __device__ __forceinline__ SoftmaxRow softmax_row(const float (&l)[V], float top, float (&s)[V]) {
   SoftmaxRow r;
   r.shift = top == -kInf ? 0.f : top;
-  float sum = 0.f;
+  float2 sum = both(0.f);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    s[i] = softmax_term(l[i], r.shift);
-    sum += s[i];
+  for (int i = 0; i < V; i += 2) {
+    const float2 e = softmax_term(make_float2(l[i], l[i + 1]), r.shift);
+    s[i] = e.x, s[i + 1] = e.y;
+    sum = add2(sum, e);
   }
-  sum = warp_sum(sum);
-  r.inv = sum == 0.f ? 0.f : __frcp_rn(sum);
+  const float total = warp_sum(sum.x + sum.y);
+  r.inv = total == 0.f ? 0.f : __frcp_rn(total);
 #pragma unroll
   for (int i = 0; i < V; ++i) s[i] *= r.inv;
   return r;
