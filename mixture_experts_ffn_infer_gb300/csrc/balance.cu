@@ -45,7 +45,7 @@ __device__ __forceinline__ float share_scores(bool sigmoid, const float (&l)[Row
     sum = add2(sum, s[i]);
   }
   const float total = warp_sum(sum.x + sum.y);
-  return total == 0.f ? 0.f : __frcp_rn(total);
+  return total == 0.f ? 0.f : reciprocal(total);
 }
 
 // Row ranges of sequence s, held within [0, n] whatever the offsets say.
@@ -79,7 +79,7 @@ balance_rows_kernel(const BalanceLaunch a, const BalancePlan plan) {
   using T = typename Row::type;
   constexpr int V = Row::width;
   __shared__ int32_t held[kHeld];
-  extern __shared__ float joined[];  // [warps][E], then the counts [E]
+  extern __shared__ __align__(16) float joined[];  // [warps][E], the counts [E], the rings
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -87,14 +87,23 @@ balance_rows_kernel(const BalanceLaunch a, const BalancePlan plan) {
   const bool sigmoid = a.r.score == MOE_SCORE_SIGMOID;
   const int64_t r0 = blockIdx.x * plan.chunk, r1 = min(r0 + plan.chunk, a.n);
   const T* logits = static_cast<const T*>(a.logits);
-  float l[V];  // the next row's, read a row ahead
-  if (r0 + warp < r1) Row::load(logits + (r0 + warp) * a.ld, E, lane, -kInf, l);
+  // this warp's rows: r0 + warp and every eighth from there on
+  const int64_t first = r0 + warp;
+  const RowRing<Row> ring{smem_u32(joined + (kRowWarps + 1) * E) + static_cast<uint32_t>(warp * RowRing<Row>::warp_bytes(E)),
+                          RowRing<Row>::row_bytes(E)};
+  auto row_at = [&](int64_t t) { return t < r1 ? logits + t * a.ld : nullptr; };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) ring.ask(i, row_at(first + kRowWarps * i), E, lane);
   const int32_t* offsets = hold_offsets(a.offsets, a.sequences, held);
   int32_t* hist = reinterpret_cast<int32_t*>(joined + kRowWarps * E);
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
   for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
   __syncthreads();
-  int64_t t = r0 + warp;  // l's row
+  int64_t t = first;
+  int number = 0;  // t's in the ring
+  // the chosen experts of the next two rows, one a lane
+  auto id_at = [&](int64_t t) { return lane < k && t < r1 ? a.ids[t * k + lane] : -1; };
+  int ids[2] = {id_at(first), id_at(first + kRowWarps)};
   for (int s = sequence_of(offsets, a.sequences, a.n, r0); s < a.sequences; ++s) {
     const int64_t lo = max(r0, offset_at(offsets, a.n, s)), hi = min(r1, offset_at(offsets, a.n, s + 1));
     if (lo >= r1) break;
@@ -102,15 +111,16 @@ balance_rows_kernel(const BalanceLaunch a, const BalancePlan plan) {
     float2 sum[V / 2];
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) sum[i] = both(0.f);
-    for (; t < hi; t += kRowWarps) {
+    for (; t < hi; t += kRowWarps, ++number) {
       const bool in = t >= lo;  // (rows in front of the first sequence are not)
-      if (in && lane < k) {
-        const int id = a.ids[t * k + lane];
-        if (id >= 0 && id < E) atomicAdd(hist + id, 1);
-      }
+      float l[V];
+      ring.take(number, logits + t * a.ld, E, lane, -kInf, l);
+      ring.ask(number + kAhead, row_at(t + kRowWarps * kAhead), E, lane);
+      if (in && ids[0] >= 0 && ids[0] < E) atomicAdd(hist + ids[0], 1);
+      ids[0] = ids[1];
+      ids[1] = id_at(t + 2 * kRowWarps);
       float2 q[V / 2];
       const float inv = share_scores<Row>(sigmoid, l, q);
-      if (t + kRowWarps < r1) Row::load(logits + (t + kRowWarps) * a.ld, E, lane, -kInf, l);
       if (in) {
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) sum[i] = fma2(q[i], both(inv), sum[i]);
@@ -131,6 +141,7 @@ balance_rows_kernel(const BalanceLaunch a, const BalancePlan plan) {
     }
     __syncthreads();
   }
+  ring.end();
 }
 
 // Grid (parts, sequences): 32 experts of a sequence, a warp every eighth piece.
@@ -168,7 +179,7 @@ balance_loss_kernel(const BalanceLaunch a, const BalancePlan plan) {
       for (int w = 0; w < 8; ++w) sum += psum[w][lane], count += pcount[w][lane];
       if (e < E) a.counts[static_cast<int64_t>(s) * E + e] = count;
       const float rows = static_cast<float>(hi - lo), part = warp_sum(static_cast<float>(count) * sum) / (rows * rows);
-      if (lane == 0) a.parts[static_cast<int64_t>(s) * parts + blockIdx.x] = part;
+      if (lane == 0) a.parts[s * parts + blockIdx.x] = lo < hi ? part : 0.f;
     }
     __syncthreads();
   }
@@ -182,17 +193,13 @@ balance_loss_kernel(const BalanceLaunch a, const BalancePlan plan) {
   float sum = 0.f;
   int live = 0;
   bool bad = false;  // offsets that do not ascend within the rows
-  for (int s = threadIdx.x; s < a.sequences; s += blockDim.x) {
-    if (a.offsets) {
-      const int64_t o0 = __ldg(a.offsets + s), o1 = __ldg(a.offsets + s + 1);
-      bad |= o0 < 0 || o1 < o0 || o1 > a.n;
-    }
-    if (offset_at(a.offsets, a.n, s + 1) <= offset_at(a.offsets, a.n, s)) continue;
-    ++live;
-    float part = 0.f;
+  // (the parts of a sequence without rows are 0)
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i) part += __ldcg(a.parts + static_cast<int64_t>(s) * parts + i);
-    sum += part;
+  for (int i = threadIdx.x; i < a.sequences * parts; i += blockDim.x) sum += __ldcg(a.parts + i);
+  for (int s = threadIdx.x; s < a.sequences; s += blockDim.x) {
+    const int64_t o0 = a.offsets ? __ldg(a.offsets + s) : 0, o1 = a.offsets ? __ldg(a.offsets + s + 1) : a.n;
+    bad |= o0 < 0 || o1 < o0 || o1 > a.n;
+    live += o1 > o0 ? 1 : 0;
   }
   bad = __syncthreads_or(bad);
   sum = warp_sum(sum);
@@ -217,7 +224,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, kGradResident<Row>)
 route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
   using T = typename Row::type;
   constexpr int V = Row::width;
-  extern __shared__ float scatter[];  // [warps][E]: ds at the chosen experts, zeros elsewhere
+  extern __shared__ __align__(16) float scatter[];  // [warps][32 V]: ds at the chosen experts, zeros elsewhere; the rings
   __shared__ int lives[kRowWarps];
   __shared__ int32_t held[kHeld];
   pdl_wait();
@@ -226,8 +233,9 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
   const int E = a.r.num_experts, k = a.r.top_k;
   const bool sigmoid = a.r.score == MOE_SCORE_SIGMOID;
   const int32_t* offsets = a.counts ? hold_offsets(a.offsets, a.sequences, held) : nullptr;
-  float* ds = scatter + warp * E;
-  for (int e = lane; e < E; e += 32) ds[e] = 0.f;
+  float* ds = scatter + warp * (32 * V);
+#pragma unroll
+  for (int i = 0; i < V; ++i) ds[32 * i + lane] = 0.f;
   float factor = 0.f;  // d_loss coef E / (S k)
   if (a.counts) {
     __syncthreads();
@@ -242,23 +250,30 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
     factor = (a.d_loss ? __ldg(a.d_loss) : 1.f) * (a.coef * static_cast<float>(E) / (static_cast<float>(k) * live));
   }
   __syncwarp();
+  const uint32_t ds_at = smem_u32(ds + 4 * lane);  // this lane's first four
   // a warp's rows follow one another, so that a sequence's counts stay in its registers
   const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp) * run, t1 = min(t0 + run, a.n);
   if (t0 >= t1) return;
   const T* logits = static_cast<const T*>(a.logits);
-  // The next row, read a row ahead: its logits, its chosen experts (one a lane, -1: none) and their weights' gradients.
-  float l[V];
-  int next_id = -1;
-  float next_g = 0.f;
-  auto read = [&](int64_t t) {
-    Row::load(logits + t * a.ld, E, lane, -kInf, l);
-    if (a.d_weight && lane < k) {
-      next_id = a.ids[t * k + lane];
-      next_g = a.d_weight[t * k + lane];
-      if (next_id < 0 || next_id >= E) next_id = -1, next_g = 0.f;
+  const RowRing<Row> ring{smem_u32(scatter + (blockDim.x >> 5) * (32 * V)) + static_cast<uint32_t>(warp * RowRing<Row>::warp_bytes(E)),
+                          RowRing<Row>::row_bytes(E)};
+  auto row_at = [&](int64_t t) { return t < t1 ? logits + t * a.ld : nullptr; };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) ring.ask(i, row_at(t0 + i), E, lane);
+  // Chosen experts, one a lane (-1: none), and their weights' gradients, of the next two rows.
+  int ids[2] = {-1, -1};
+  float gs[2] = {0.f, 0.f};
+  auto read = [&](int64_t t, int& id, float& g) {
+    id = -1;
+    g = 0.f;
+    if (a.d_weight && lane < k && t < t1) {
+      id = a.ids[t * k + lane];
+      g = a.d_weight[t * k + lane];
+      if (id < 0 || id >= E) id = -1, g = 0.f;
     }
   };
-  read(t0);
+  read(t0, ids[0], gs[0]);
+  read(t0 + 1, ids[1], gs[1]);
   float2 c[V / 2];
 #pragma unroll
   for (int i = 0; i < V / 2; ++i) c[i] = both(0.f);
@@ -266,9 +281,17 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
   int64_t until = t0;  // where c changes next
 #pragma unroll 1
   for (int64_t t = t0; t < t1; ++t) {
-    const int id = next_id;
-    const float g = next_g * a.r.scale;
-    const float lj = id >= 0 ? to_float(logits[t * a.ld + id]) : -kInf;
+    const int id = ids[0];
+    const float g = gs[0] * a.r.scale;
+    ids[0] = ids[1];
+    gs[0] = gs[1];
+    read(t + 2, ids[1], gs[1]);
+    float l[V];
+    const int number = static_cast<int>(t - t0);
+    ring.take(number, logits + t * a.ld, E, lane, -kInf, l);
+    ring.ask(number + kAhead, row_at(t + kAhead), E, lane);
+    __syncwarp();  // (the row is in the ring for every lane)
+    const float lj = id >= 0 ? ring.one(number, logits + t * a.ld, id) : -kInf;
     if (a.counts && t >= until) {
       // sequences that end at or in front of t are over; between two (and behind the last) there are none
       while (seq < a.sequences && offset_at(offsets, a.n, seq + 1) <= t) ++seq;
@@ -309,8 +332,7 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
         dot2 = fma2(c[i], v[i], dot2);
       }
     }
-    if (t + 1 < t1) read(t + 1);
-    const float total = warp_sum(total2.x + total2.y), inv = total == 0.f ? 0.f : __frcp_rn(total);
+    const float total = warp_sum(total2.x + total2.y), inv = total == 0.f ? 0.f : reciprocal(total);
     // (NaN of a row that holds one: total is)
     const bool bad = total != total;
     float dot = dot2.x + dot2.y, dj = 0.f;  // dj: ds of the lane's chosen expert
@@ -349,13 +371,25 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
       rest = -dot * inv;
     }
     const float ds_scale = sigmoid ? 1.f : inv;
-    float d[V];
+    float d[V], add[V];
+    if (a.d_weight) {
+      if constexpr (Row::vec) {
+#pragma unroll
+        for (int j = 0; j < V / 4; ++j) {
+          const uint4 q = lds128(ds_at + 512 * j);
+          add[4 * j] = __uint_as_float(q.x), add[4 * j + 1] = __uint_as_float(q.y), add[4 * j + 2] = __uint_as_float(q.z),
+                  add[4 * j + 3] = __uint_as_float(q.w);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) add[i] = ds[32 * i + lane];
+      }
+    }
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
       float2 w = fma2(c[i], both(scale), both(rest));
       if (a.d_weight) {
-        const int e0 = Row::expert(2 * i, lane), e1 = Row::expert(2 * i + 1, lane);
-        w = fma2(make_float2(e0 < E ? ds[e0] : 0.f, e1 < E ? ds[e1] : 0.f), both(ds_scale), w);
+        w = fma2(make_float2(add[2 * i], add[2 * i + 1]), both(ds_scale), w);
       }
       w = mul2(w, v[i]);
       d[2 * i] = w.x, d[2 * i + 1] = w.y;
@@ -369,13 +403,21 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
     if (id >= 0) ds[id] = 0.f;
     __syncwarp();
   }
+  ring.end();
 }
 
 }  // namespace
 
+// (A kernel's own 48 KB need no leave.)
+template <typename K>
+static cudaError_t allow_smem(K kern, size_t bytes) {
+  if (bytes <= 40 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+}
+
 BalancePlan balance_plan(int64_t n) {
-  // A row a warp at least, four CTAs an SM at most.
-  constexpr int64_t kMost = 608, kLeast = 8;
+  // A row a warp at least; at most what the SMs hold at once of 384 experts (67 KB each: three an SM).
+  constexpr int64_t kMost = 456, kLeast = 8;
   int64_t chunk = (n + kMost - 1) / kMost;
   if (chunk < kLeast) chunk = kLeast;
   if (chunk > n) chunk = n < 1 ? 1 : n;
@@ -385,9 +427,13 @@ BalancePlan balance_plan(int64_t n) {
 
 cudaError_t launch_balance(const BalanceLaunch& a, cudaStream_t s) {
   const BalancePlan plan = balance_plan(a.n);
-  const size_t smem = (kRowWarps + 1) * sizeof(float) * a.r.num_experts;
   cudaError_t e = with_row(a.r, rows_by_four(a.r, a.logits, a.ld), [&](auto row) {
-    return launch_maybe_overlapped(balance_rows_kernel<decltype(row)>, plan.chunks, 32 * kRowWarps, smem, s, true, a, plan);
+    using Row = decltype(row);
+    auto kern = balance_rows_kernel<Row>;
+    const size_t smem = (kRowWarps + 1) * sizeof(float) * a.r.num_experts + kRowWarps * RowRing<Row>::warp_bytes(a.r.num_experts);
+    const cudaError_t st = allow_smem(kern, smem);
+    if (st != cudaSuccess) return st;
+    return launch_maybe_overlapped(kern, plan.chunks, 32 * kRowWarps, smem, s, true, a, plan);
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -408,14 +454,17 @@ cudaError_t launch_route_grad(const RouteGradLaunch& a, cudaStream_t s) {
   if (sms <= 0) return cudaErrorInvalidValue;
   int warps = 1;
   while (warps < kRowWarps && a.n > sms * warps) warps *= 2;
-  const size_t smem = sizeof(float) * static_cast<size_t>(warps) * a.r.num_experts;
   const bool vec = rows_by_four(a.r, a.logits, a.ld) && rows_by_four(a.r, a.d_logits, a.d_ld);
   return with_row(a.r, vec, [&](auto row) {
     // one round of the CTAs that the SMs hold
     const int64_t most = sms * kGradResident<decltype(row)> * kRowWarps, run = (a.n + most - 1) / most;
     const int64_t ctas = (a.n + run * warps - 1) / (run * warps);
-    return launch_maybe_overlapped(route_grad_kernel<decltype(row)>, static_cast<int>(ctas), 32 * warps, smem, s, true, a,
-                                   run);
+    const size_t smem = static_cast<size_t>(warps) * (sizeof(float) * 32 * decltype(row)::width +
+                                                      RowRing<decltype(row)>::warp_bytes(a.r.num_experts));
+    auto kern = route_grad_kernel<decltype(row)>;
+    const cudaError_t st = allow_smem(kern, smem);
+    if (st != cudaSuccess) return st;
+    return launch_maybe_overlapped(kern, static_cast<int>(ctas), 32 * warps, smem, s, true, a, run);
   });
 }
 

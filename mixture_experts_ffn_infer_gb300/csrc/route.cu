@@ -34,7 +34,6 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
-__device__ __forceinline__ uint32_t key_if(bool on, float x) { return on && x > -kInf ? key_of(x) : 0u; }
 
 // Scores in 64 bits.
 __device__ __forceinline__ double exact_sigmoid(float l) { return 1.0 / (1.0 + exp(-static_cast<double>(l))); }
@@ -146,16 +145,13 @@ __device__ __noinline__ int exact_choice(const moe_router r, const typename Row:
   return id;
 }
 
-// The rank of this lane's value among those of lanes 0 .. count - 1, ties to the lower e; next: the nearest larger one.
-__device__ __forceinline__ int rank_of(uint32_t key, int e, int count, uint32_t& next) {
+// The rank of this lane's key among those of the lanes (0: none, lanes from `count` on have it), equal ones together.
+__device__ __forceinline__ int rank_of(uint32_t key, int count) {
   int rank = 0;
-  next = 0xffffffffu;
-  const uint64_t mine = static_cast<uint64_t>(key) << 32 | static_cast<uint32_t>(~e);
-#pragma unroll 4
-  for (int j = 0; j < count; ++j) {
-    const uint32_t kj = __shfl_sync(kAll, key, j), ej = __shfl_sync(kAll, static_cast<uint32_t>(~e), j);
-    rank += (static_cast<uint64_t>(kj) << 32 | ej) > mine ? 1 : 0;
-    if (kj > key) next = min(next, kj);
+#pragma unroll 1
+  for (int j0 = 0; j0 < count; j0 += 8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rank += __shfl_sync(kAll, key, j0 + j) > key ? 1 : 0;
   }
   return rank;
 }
@@ -180,6 +176,43 @@ __device__ __noinline__ int exact_rank(const typename Row::type* p, int E, bool 
     rank += xj > x || (xj == x && ej < e) ? 1 : 0;
   }
   return rank;
+}
+
+// The j-th largest (from 1) of the lanes' values.  K. Batcher's bitonic sort (1968): 15 exchanges; up to the 16th, of the
+// larger values of pairs of lanes, 10 (a value no larger, with one or two more from it up among all).  dirs: bit i of a
+// lane is whether it keeps the larger one in exchange i.  (Nine maxima of the warp one after the other took 130
+// instructions.)
+__device__ __forceinline__ uint32_t sort_directions(int lane) {
+  uint32_t dirs = 0;
+  int i = 0;
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+    for (int o = size / 2; o > 0; o /= 2, ++i) dirs |= ((lane & o) == 0) == ((lane & size) == 0) ? 1u << i : 0u;
+  // (as the last round of 16 the fourth sorts downwards everywhere)
+#pragma unroll
+  for (int o = 8; o > 0; o /= 2, ++i) dirs |= (lane & o) == 0 ? 1u << i : 0u;
+  return dirs;
+}
+__device__ __forceinline__ float warp_nth(float v, int j, uint32_t dirs) {
+  auto exchange = [&](int o, int i) {
+    const float w = __shfl_xor_sync(kAll, v, o);
+    v = dirs >> i & 1u ? fmaxf(v, w) : fminf(v, w);
+  };
+  if (j <= 16) {
+    v = fmaxf(v, __shfl_xor_sync(kAll, v, 16));
+    exchange(1, 0);
+    exchange(2, 1), exchange(1, 2);
+    exchange(4, 3), exchange(2, 4), exchange(1, 5);
+    exchange(8, 15), exchange(4, 16), exchange(2, 17), exchange(1, 18);
+  } else {
+    exchange(1, 0);
+    exchange(2, 1), exchange(1, 2);
+    exchange(4, 3), exchange(2, 4), exchange(1, 5);
+    exchange(8, 6), exchange(4, 7), exchange(2, 8), exchange(1, 9);
+    exchange(16, 10), exchange(8, 11), exchange(4, 12), exchange(2, 13), exchange(1, 14);
+  }
+  return __shfl_sync(kAll, v, j - 1);
 }
 
 // The kept groups' bits.  x: the warp's choices (-inf: not to be chosen), by way of `row` in shared memory; unsure: the
@@ -255,6 +288,7 @@ route_kernel(const RouteLaunch a, const int group_inv) {
     const float b = e < E && a.bias ? __ldg(a.bias + e) : 0.f;
     bias[i] = e < E && b == b ? b : -kInf;
   }
+  const uint32_t dirs = sort_directions(lane);
   const int64_t rows = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp; t < a.n; t += rows) {
     const T* p = static_cast<const T*>(a.logits) + t * a.ld;
@@ -329,13 +363,7 @@ route_kernel(const RouteLaunch a, const int group_inv) {
       }
     }
     // the k + 1st largest of the lanes' largest, less the margin of the short scores (twice their error)
-    uint32_t from = 0, left = key_if(true, local);
-    for (int j = 0; j < deep; ++j) {
-      from = __reduce_max_sync(kAll, left);
-      if (from == 0) break;
-      if (left == from) left = 0;
-    }
-    float low = from != 0 && deep <= 32 ? value_of(from) : -kInf;
+    float low = deep <= 32 ? warp_nth(local, deep, dirs) : -kInf;
     if (!by_logit) low -= fmaf(0x1p-21f, fabsf(low), fmaxf(0x1p-18f, tolerance(sigmoid, most, 0.f)));
     if (!(low > -kInf)) low = -3.4028234663852886e38f;  // all that can be chosen
     uint32_t mask = 0;
@@ -366,21 +394,29 @@ route_kernel(const RouteLaunch a, const int group_inv) {
         y = by_logit ? l : w + b;
         key = key_of(y);
       }
-      uint32_t next;
-      rank = rank_of(key, id, found, next);
-      if (!by_logit) {
-        // the one in front, where both are not behind the k + 1st
-        bool close = id >= 0 && rank <= k && next != 0xffffffffu &&
-                     !(value_of(next) - y > tolerance(sigmoid, most, fabsf(y) + fabsf(value_of(next))));
+      rank = rank_of(key, found);
+      // The lanes by rank: an equal one's place is another's.
+      if (id >= 0) list[warp][rank] = lane;
+      __syncwarp();
+      bool close = false;
+      if (__any_sync(kAll, id >= 0 && list[warp][rank & 31] != lane)) {
+        // Equal values go by index, if they are of the same inputs; else they are not known to be equal.
         const uint32_t same = __match_any_sync(kAll, key);
-        if (__any_sync(kAll, id >= 0 && (same & (same - 1u)) != 0)) {
-          // equal values: of the same inputs, or not known to be equal
-          const int first = __ffs(same) - 1;
-          const float l0 = __shfl_sync(kAll, l, first), b0 = __shfl_sync(kAll, b, first);
-          close |= id >= 0 && rank <= k && !(l == l0 && b == b0);
-        }
-        if (__any_sync(kAll, close))
-          rank = exact_rank<Row>(p, E, sigmoid, soft.shift, l, b, id, found);
+        const int first = __ffs(same) - 1;
+        const float l0 = __shfl_sync(kAll, l, first), b0 = __shfl_sync(kAll, b, first);
+        close = !by_logit && id >= 0 && rank <= k && !(l == l0 && b == b0);
+        int before = 0;
+        for (int j = 0; j < found; ++j) before += __shfl_sync(kAll, id, j) < id && (same >> j & 1u) ? 1 : 0;
+        rank += before;
+        if (id >= 0) list[warp][rank] = lane;
+        __syncwarp();
+      }
+      if (!by_logit) {
+        // the one in front, where both are not behind the k + 1st (equal ones: as above)
+        const float front = __shfl_sync(kAll, y, id >= 0 && rank > 0 ? list[warp][rank - 1] : lane);
+        close |= id >= 0 && rank > 0 && rank <= k && front != y &&
+                 !(front - y > tolerance(sigmoid, most, fabsf(y) + fabsf(front)));
+        if (__any_sync(kAll, close)) rank = exact_rank<Row>(p, E, sigmoid, soft.shift, l, b, id, found);
       }
       if (id < 0) rank = lane;  // behind those that were found
       if (rank >= k) w = 0.f;
@@ -393,7 +429,7 @@ route_kernel(const RouteLaunch a, const int group_inv) {
       }
     }
     __syncwarp();  // the list is read
-    if (r.normalise) w = __fdiv_rn(w, warp_sum(w) + kTiny);
+    if (r.normalise) w = __fdividef(w, warp_sum(w) + kTiny);  // (a sum of 1e-20 to 32)
     if (rank < k) ids[rank] = id, weight[rank] = w * r.scale;
   }
 }

@@ -21,6 +21,7 @@ template <typename T, int V, bool VEC>
 struct WarpRow {
   using type = T;
   static constexpr int width = V;
+  static constexpr bool vec = VEC;
   static __device__ __forceinline__ int expert(int i, int lane) {
     return VEC ? 128 * (i >> 2) + 4 * lane + (i & 3) : 32 * i + lane;
   }
@@ -73,6 +74,82 @@ struct WarpRow {
     }
   }
 };
+
+// The next rows of a warp on their way to shared memory, kAhead of them, so that a warp waits for none that it has not
+// asked for kAhead rows ago.  A lane copies and reads its own pieces alone: its own wait is enough.  (Rows that are not
+// read four values at a time are read where they are used.)
+constexpr int kAhead = 3;
+template <typename Row>
+struct RowRing {
+  using T = typename Row::type;
+  static constexpr int kPiece = 4 * sizeof(T);
+  uint32_t base;  // of this warp's kAhead + 1 rows
+  int bytes;      // of one
+  static __host__ __device__ constexpr int row_bytes(int E) {
+    return Row::vec ? (static_cast<int>(sizeof(T)) * E + 15) / 16 * 16 : 0;
+  }
+  static __host__ __device__ constexpr size_t warp_bytes(int E) { return static_cast<size_t>(kAhead + 1) * row_bytes(E); }
+
+  // Row number i of the warp, at p (null: none; each call counts all the same).
+  __device__ __forceinline__ void ask(int i, const T* p, int E, int lane) const {
+    if constexpr (Row::vec) {
+      if (p) {
+        const uint32_t to = base + (i & kAhead) * bytes + kPiece * lane;
+#pragma unroll
+        for (int j = 0; j < Row::width / 4; ++j)
+          if (128 * j + 4 * lane < E)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + 32 * kPiece * j),
+                         "l"(p + 128 * j + 4 * lane), "n"(kPiece)
+                         : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  }
+  // Before the warp ends: nothing is on its way any more.
+  __device__ __forceinline__ void end() const {
+    if constexpr (Row::vec) asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  // Row number i, asked for kAhead calls ago; values past the row are `fill`.
+  __device__ __forceinline__ void take(int i, const T* p, int E, int lane, float fill, float (&v)[Row::width]) const {
+    if constexpr (Row::vec) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+      const uint32_t at = base + (i & kAhead) * bytes + kPiece * lane;
+#pragma unroll
+      for (int j = 0; j < Row::width / 4; ++j) {
+        const bool on = 128 * j + 4 * lane < E;
+        if constexpr (sizeof(T) == 4) {
+          uint4 q = make_uint4(0u, 0u, 0u, 0u);
+          if (on) q = lds128(at + 32 * kPiece * j);
+          v[4 * j] = __uint_as_float(q.x), v[4 * j + 1] = __uint_as_float(q.y), v[4 * j + 2] = __uint_as_float(q.z),
+                v[4 * j + 3] = __uint_as_float(q.w);
+        } else {
+          uint32_t x = 0, y = 0;
+          if (on) asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "r"(at + 32 * kPiece * j));
+          v[4 * j] = __uint_as_float(x << 16), v[4 * j + 1] = __uint_as_float(x & 0xffff0000u);
+          v[4 * j + 2] = __uint_as_float(y << 16), v[4 * j + 3] = __uint_as_float(y & 0xffff0000u);
+        }
+        if (!on) v[4 * j] = v[4 * j + 1] = v[4 * j + 2] = v[4 * j + 3] = fill;
+      }
+    } else {
+      Row::load(p, E, lane, fill, v);
+    }
+  }
+  // One value of row number i, which every lane of the warp has taken and not yet asked over.
+  __device__ __forceinline__ float one(int i, const T* p, int e) const {
+    if constexpr (!Row::vec) return to_float(p[e]);
+    const uint32_t at = base + (i & kAhead) * bytes + sizeof(T) * e;
+    if constexpr (sizeof(T) == 4) {
+      float v;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+      return v;
+    } else {
+      uint16_t v;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+      return __uint_as_float(static_cast<uint32_t>(v) << 16);
+    }
+  }
+};
+static_assert((kAhead & (kAhead + 1)) == 0, "rows of the ring are numbered by bits");
 
 // The larger value, NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -177,7 +254,7 @@ __device__ __forceinline__ SoftmaxRow softmax_row(const float (&l)[V], float top
     sum = add2(sum, e);
   }
   const float total = warp_sum(sum.x + sum.y);
-  r.inv = total == 0.f ? 0.f : __frcp_rn(total);
+  r.inv = total == 0.f ? 0.f : reciprocal(total);
 #pragma unroll
   for (int i = 0; i < V; ++i) s[i] *= r.inv;
   return r;
