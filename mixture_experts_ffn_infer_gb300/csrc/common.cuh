@@ -130,6 +130,7 @@ cudaError_t launch_maybe_overlapped(void (*kern)(P...), int grid, int block, siz
 
 // ---------------------------------------------------------------- api.cu
 bool encode_rows_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows);
+bool encode_dense_map(CUtensorMap* m, const void* base, uint64_t rows);
 int device_sms();
 
 // ---------------------------------------------------------------- launchers

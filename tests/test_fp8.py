@@ -196,6 +196,45 @@ def test_product_of_many_units(rows, E, n_out, k):
     check_product(x, w, wv, ragged(2, rows, E))
 
 
+@pytest.mark.parametrize("rows,E,n_out,k,sizes", [
+    (100, 19, 2048, 272, None),                    # few rows of many experts
+    (1300, 4, 2001, 7168, [130, 0, 1, 1169]),      # tiles of 256 rows: their second half with 2 rows, none, 17
+    (1400, 3, 2000, 7168, [0, 511, 777]),
+    (6000, 3, 1000, 2064, [257, 3000, 2500])])     # (rows that no expert has)
+def test_product_of_each_tile(rows, E, n_out, k, sizes):
+    x, w, wv = make(7, rows, E, n_out, k)
+    offsets = ragged(3, rows, E) if sizes is None else [sum(sizes[:e]) for e in range(E + 1)]
+    for out_type in DTYPES:
+        check_product(x, w, wv, offsets, out_type)
+
+
+def test_large_tiles_with_positions_weights_and_values_that_are_not_finite():
+    rows, E, n_out, k = 1300, 2, 2003, 7168
+    x, w, wv = make(8, rows, E, n_out, k)
+    x.scales[700, 3], x.codes[20, 7000] = math.inf, 0x7f
+    offsets = [0, 645, rows]
+    want, size = plain.product(plain.values(x.codes.cpu(), x.scales.cpu()), wv, offsets)
+    at = torch.randperm(rows + 9, generator=gen(1))[:rows].to(torch.int32)
+    at[130], at[900] = rows + 9, -5
+    weight = torch.rand(rows + 9, generator=gen(2)) * 3 - 1
+    room = torch.full((rows + 9, n_out + 5), 9.0, dtype=torch.bfloat16, device="cuda")
+    mx.fp8_grouped_product(x, w, torch.tensor(offsets, dtype=torch.int32, device="cuda"), out=room[:, 3:3 + n_out],
+                           out_pos=at.cuda(), row_weight=weight.cuda())
+    got = room.cpu().double()
+    assert (got[:, :3] == 9).all() and (got[:, 3 + n_out:] == 9).all()
+    on = (at >= 0) & (at < rows + 9)
+    odd = torch.zeros(rows, dtype=torch.bool)
+    odd[[20, 700]] = True
+    assert not got[at[odd].long(), 3:3 + n_out].isfinite().any()
+    on &= ~odd
+    to, f = at[on].long(), weight.double()[at[on].long()][:, None]
+    tol = plain.tolerance(want, size, k, torch.bfloat16)
+    assert within(got[to, 3:3 + n_out], want[on] * f, tol[on] * f.abs(), 1e-30)
+    rest = torch.ones(rows + 9, dtype=torch.bool)
+    rest[at[(at >= 0) & (at < rows + 9)].long()] = False
+    assert (got[rest] == 9).all()
+
+
 def test_rows_of_no_expert_stay():
     x, w, wv = make(5, 400, 3, 260, 144)
     for offsets in ([7, 7, 150, 390], [0, 0, 0, 0], [400, 400, 400, 400], [129, 130, 131, 132]):
