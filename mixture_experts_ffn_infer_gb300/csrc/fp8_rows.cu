@@ -4,8 +4,8 @@
 // fp8_rows_kernel       - quantise, write to each position of the row.  A thread holds
 //                         16 consecutive columns (32 bytes read, 16 written) from the read
 //                         to the codes, eight threads a block of 128: its largest
-//                         magnitude takes three exchanges.  A CTA a row, or a warp where many
-//                         narrow rows come.
+//                         magnitude takes three exchanges.  A CTA a row, several where few
+//                         come, or a warp where many narrow ones do.
 // fp8_dequantise_kernel - codes and scales to bf16, 16 columns at a time, four a thread
 //                         under way at once.
 // fp8_pack_kernel       - a CTA a packed block.
@@ -22,7 +22,7 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kPiece = 16;  // columns a thread holds together
-constexpr int kMaxThreads = 1024, kSplitThreads = 256;
+constexpr int kFewThreads = 64, kSplitThreads = 256;
 
 __device__ __forceinline__ void load_piece(const uint16_t* p, bool wide, uint32_t (&w)[8]) {
   if (wide) {
@@ -82,18 +82,19 @@ __device__ __forceinline__ void codes_of(const uint32_t (&raw)[8], const BlockSc
 
 // ITER passes of `width` pieces cover the row.
 template <int ITER, bool WARP>
-__global__ void __launch_bounds__(ITER == 1 ? kMaxThreads : kSplitThreads)
-fp8_rows_kernel(const Fp8RowsLaunch a, int32_t pitch, int32_t wide) {
+__global__ void __launch_bounds__(kSplitThreads)
+fp8_rows_kernel(const Fp8RowsLaunch a, int32_t pitch, int32_t wide, int32_t parts) {
   pdl_wait();
   pdl_launch_dependents();
   const int width = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int64_t t = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t t = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5) : blockIdx.x / parts;
+  const int first = WARP ? 0 : (blockIdx.x % parts) * (ITER * width);
   if (WARP && t >= a.n) return;
   const int np = a.d / kPiece;
   uint32_t raw[ITER][8];
 #pragma unroll
   for (int it = 0; it < ITER; ++it) {
-    const int c = it * width + tid;
+    const int c = first + it * width + tid;
 #pragma unroll
     for (int i = 0; i < 8; ++i) raw[it][i] = 0u;
     if (c < np) load_piece(a.x + t * a.x_ld + kPiece * c, wide != 0, raw[it]);
@@ -104,7 +105,7 @@ fp8_rows_kernel(const Fp8RowsLaunch a, int32_t pitch, int32_t wide) {
     at[j] = j >= a.k ? -1 : a.positions ? __ldg(a.positions + t * a.k + j) : 0;
 #pragma unroll
   for (int it = 0; it < ITER; ++it) {
-    const int c = it * width + tid;
+    const int c = first + it * width + tid;
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -238,21 +239,22 @@ fp8_transpose_kernel(const uint8_t* __restrict__ codes, const float* __restrict_
 
 cudaError_t launch_fp8_rows(const Fp8RowsLaunch& a, cudaStream_t s) {
   const int np = a.d / kPiece;
-  // Few rows: as many threads as the row has pieces.  More rows than the SMs hold at once: two pieces a thread, and
+  // Few rows: a piece a thread, 64 threads to a CTA, so that a row's stores to its positions are on several SMs (16 rows of
+  // 16,384 columns to 8 positions on one GB300: 6.1 us, 8.2 by a CTA a row).  More rows than the SMs hold at once: two pieces a thread, and
   // rows of up to 64 pieces one to a warp, eight to a CTA.
   const bool many = a.n > 2 * device_sms(), by_warp = many && np <= 64;
-  int iters = 1;
-  while (iters * (by_warp ? 32 : many ? kSplitThreads : kMaxThreads) < np) iters *= 2;
-  if (many && !by_warp && iters == 1) iters = 2;
-  const int threads = by_warp ? 256 : ((np + iters - 1) / iters + 31) / 32 * 32;
-  const int64_t grid = by_warp ? (a.n + 7) / 8 : a.n;
+  int iters = many && !by_warp ? 2 : 1;
+  while (many && iters * (by_warp ? 32 : kSplitThreads) < np) iters *= 2;
+  const int threads = by_warp ? 256 : many ? ((np + iters - 1) / iters + 31) / 32 * 32 : kFewThreads;
+  const int parts = many ? 1 : (np + kFewThreads - 1) / kFewThreads;
+  const int64_t grid = by_warp ? (a.n + 7) / 8 : a.n * parts;
   auto kern = by_warp      ? iters == 1 ? fp8_rows_kernel<1, true> : fp8_rows_kernel<2, true>
               : iters == 1 ? fp8_rows_kernel<1, false>
               : iters == 2 ? fp8_rows_kernel<2, false>
                            : fp8_rows_kernel<4, false>;
   return launch_maybe_overlapped(kern, static_cast<int>(grid), threads, 0, s, true, a,
                                  static_cast<int32_t>(moe_fp8_scale_pitch(a.d)),
-                                 static_cast<int32_t>(aligned32(a.x, a.x_ld)));
+                                 static_cast<int32_t>(aligned32(a.x, a.x_ld)), parts);
 }
 
 cudaError_t launch_fp8_dequantise(int64_t rows, int32_t d, const uint8_t* codes, const float* scales, uint16_t* out,
