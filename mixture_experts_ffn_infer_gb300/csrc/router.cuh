@@ -232,6 +232,14 @@ __device__ __forceinline__ float2 sigmoid_of(float2 l) {
 }
 __device__ __forceinline__ float sigmoid_of(float l) { return sigmoid_of(both(l)).x; }
 
+// The same with e^-l by one rounded product, which is within |l| 2^-24 of it (and what the others are): for sums over many
+// rows, whose own rounding is larger.  No value needs a bound: beyond the range of floats the reciprocal is 0 or 1.
+__device__ __forceinline__ float2 sigmoid_short(float2 l) {
+  const float2 h = mul2(l, both(-1.44269504f));
+  const float2 d = add2(both(1.0f), make_float2(exp2_approx(h.x), exp2_approx(h.y)));
+  return make_float2(reciprocal(d.x), reciprocal(d.y));
+}
+
 // What a row's softmax needs of the whole row: score = e^(l - shift) inv.  A row of -inf alone has
 // shift 0 and scores 0.
 struct SoftmaxRow {

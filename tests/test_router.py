@@ -207,7 +207,8 @@ def ids_of(seed, n, k, E):
 
 
 def loss_error(logits, live_rows):
-    """Relative: a share, and sums of positive values: a CTA's run of max(8, n / 456) rows by eight warps, eight warps,
+    """Relative: a share (a sigmoid's e^-l is within |l| 2^-24, below the 2 spread + 5 units that score_error has for more:
+    these logits have both signs), and sums of positive values: a CTA's run of max(8, n / 456) rows by eight warps, eight warps,
     up to 457 pieces by eight warps, 32 experts, E / 32 parts and the sequences by 256 threads (24 for up to 6000 of them and
     13 to join), besides a handful of products."""
     n, E = logits.shape
@@ -219,7 +220,10 @@ def loss_error(logits, live_rows):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("n,E,k,S,pad", [(1, 1, 1, 1, 0), (1, 384, 8, 1, 0), (64, 16, 4, 1, 0), (65, 33, 2, 3, 1),
                                          (1001, 60, 3, 5, 37), (500, 384, 8, 500, 0), (3000, 130, 6, 40, 5),
-                                         (130, 1024, 32, 2, 0), (2000, 8, 2, 6000, 300)])
+                                         (130, 1024, 32, 2, 0), (2000, 8, 2, 6000, 300),
+                                         (20001, 64, 6, 7, 13), (12000, 384, 8, 3001, 0), (10001, 256, 16, 1, 0),
+                                         (9999, 500, 3, 9000, 77), (70001, 8, 1, 50, 1), (10000, 130, 9, 11, 0),
+                                         (9800, 64, 17, 5, 0)])
 def test_loss_and_counts(kind, dtype, n, E, k, S, pad):
     logits, ids = logits_of(n + E, n, E, dtype), ids_of(n, n, k, E)
     offsets = None if S == 1 and pad == 0 else ragged(S, n - pad, S)
