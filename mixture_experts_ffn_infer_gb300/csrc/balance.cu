@@ -335,7 +335,7 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
 #pragma unroll
       for (int i = 0; i < V / 2; ++i) {
         float2 t2;
-        const float2 s = sigmoid_of(make_float2(l[2 * i], l[2 * i + 1]), t2);
+        const float2 s = sigmoid_short(make_float2(l[2 * i], l[2 * i + 1]), t2);
         total2 = add2(total2, s);
         dot2 = fma2(c[i], s, dot2);
         v[i] = mul2(mul2(t2, s), s);  // s (1 - s): e^-l s is 1 - s

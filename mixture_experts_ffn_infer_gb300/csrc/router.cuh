@@ -219,21 +219,24 @@ __device__ __forceinline__ float2 exp_of(float2 x) {
   return fma2(t, r, t);
 }
 
-// 1 / (1 + e^-l), NaN of a NaN; t gets e^-l, never infinite.  From -88.1 down t is above 2^127 and its reciprocal is
-// flushed to 0.  The reciprocal is within an ulp: together below 2^-21 of the score.
-__device__ __forceinline__ float2 sigmoid_of(float2 l, float2& t) {
-  t = exp_of(make_float2(max_nan(min_nan(-l.x, 88.1f), -128.f), max_nan(min_nan(-l.y, 88.1f), -128.f)));
+// 1 / (1 + e^-l), NaN of a NaN.  From -88.1 down e^-l is above 2^127 and its reciprocal is flushed to 0.  The
+// reciprocal is within an ulp: together below 2^-21 of the score.
+__device__ __forceinline__ float2 sigmoid_of(float2 l) {
+  const float2 t = exp_of(make_float2(max_nan(min_nan(-l.x, 88.1f), -128.f), max_nan(min_nan(-l.y, 88.1f), -128.f)));
   const float2 d = add2(both(1.0f), t);
   return make_float2(reciprocal(d.x), reciprocal(d.y));
-}
-__device__ __forceinline__ float2 sigmoid_of(float2 l) {
-  float2 t;
-  return sigmoid_of(l, t);
 }
 __device__ __forceinline__ float sigmoid_of(float l) { return sigmoid_of(both(l)).x; }
 
 // The same with e^-l by one rounded product, which is within |l| 2^-24 of it (and what the others are): for sums over many
-// rows, whose own rounding is larger.  No value needs a bound: beyond the range of floats the reciprocal is 0 or 1.
+// rows and gradients, whose own roundings are no smaller.
+__device__ __forceinline__ float2 sigmoid_short(float2 l, float2& t) {
+  const float2 h = mul2(l, both(-1.44269504f));
+  t = make_float2(exp2_approx(min_nan(h.x, 127.f)), exp2_approx(min_nan(h.y, 127.f)));
+  const float2 d = add2(both(1.0f), t);
+  return make_float2(reciprocal(d.x), reciprocal(d.y));
+}
+// (No value needs a bound here: beyond the range of floats the reciprocal is 0 or 1.)
 __device__ __forceinline__ float2 sigmoid_short(float2 l) {
   const float2 h = mul2(l, both(-1.44269504f));
   const float2 d = add2(both(1.0f), make_float2(exp2_approx(h.x), exp2_approx(h.y)));
