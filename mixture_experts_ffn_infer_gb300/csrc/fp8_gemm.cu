@@ -7,19 +7,22 @@
 // accumulators); every block has a factor of its own for each row, so each block's sums
 // are read from tensor memory and added to fp32 registers times that factor.
 //
-//  * Unit = a tile of up to 128 rows of one expert x NB blocks of 128 weight rows: M = 128,
-//    N = 128 NB.  A chunk is one block of K: one bulk copy brings its weights, one TMA box
-//    the tile's rows.
-//  * Where many rows come, a pair of CTAs takes a tile of 256 rows x 256 weight rows (M = 256,
-//    tcgen05 cta_group::2): each brings its own 128 rows and half of the weights, 32 KB a
-//    chunk instead of 48, and sums its rows' part.
-//  * Tensor memory holds 4 / NB chunks' sums, so that the MMAs of the next chunks run while
-//    one is read.
+//  * Unit = a tile of rows of one expert x blocks of 128 weight rows.  A chunk is one block of K:
+//    one bulk copy brings its weights, one TMA box the tile's rows.  Four kinds:
+//      few   32 rows x one block, the weights as the MMA's M = 128 and the rows as its N = 16 or
+//            32: an epilogue thread has a weight row and 16 of the tile's
+//      one   128 rows x one block, M = N = 128
+//      two   128 rows x two blocks, N = 256
+//      pair  256 rows x two blocks by a pair of CTAs (M = 256, tcgen05 cta_group::2): each brings
+//            its own 128 rows and half of the weights, 32 KB a chunk instead of 48, and sums
+//            its rows' part
+//    An epilogue thread of the last three owns a row and 64 weight rows of each block; a warp
+//    whose rows do not exist only frees the buffers.
+//  * Tensor memory holds 2 to 8 chunks' sums, so that the MMAs of the next chunks run while one
+//    is read.
 //  * A warp of its own lays the chunks' factors out in shared memory, four chunks at a time:
 //    the rows' scales times the weights'.  (Global loads in the epilogue, even four chunks
 //    ahead, held up its reads of tensor memory.)
-//  * An epilogue thread owns a row and 64 weight rows of each block; a warp whose rows do not
-//    exist only frees the buffers.
 //
 // Warps (384 threads, one CTA per SM, persistent over units):
 //   0 weight copies   1 MMA issue   2 row copies   3 factors   4-11 epilogue
@@ -29,9 +32,10 @@
 // warps take 280 cycles), the release, the next MMAs.  The MMAs' operands take most of shared
 // memory's cycles, and whatever else goes there waits: a test of a barrier that is complete
 // already takes 180 cycles beside MMAs of N = 128.  So barriers are tested ahead where that
-// can be, and nothing on that way may come from local memory: see `fresh`.  8192 x 7168 x 7168
-// on one GB300: 318 us in a row on one set of operands, 348 in turn with others (2.42 PFLOP/s),
-// some 850 cycles a chunk (a loop of the same steps without units, 690).
+// can be (the issuing thread's two together: one row of 7168 x 7168 20.0 -> 16.2 us), and
+// nothing on that way may come from local memory: see `fresh`.  8192 x 7168 x 7168 on one
+// GB300: 318 us in a row on one set of operands, 348 in turn with others (2.42 PFLOP/s), some
+// 850 cycles a chunk (a loop of the same steps without units, 690).
 //
 // Within an expert up to eight tiles run a weight block one after another, so that they
 // take place at the same time and share it through L2.  Every wait is bounded; after one
@@ -49,7 +53,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kTile = 128;  // rows of a CTA's tile
 constexpr int kMaxExperts = 1024;
 constexpr int kChunkTiles = 8;
-constexpr int kRowBytes = kTile * 128;
+constexpr int kFewTile = 32;  // where few rows come
 constexpr uint32_t kTmemCols = 512;
 constexpr int kWarpWeights = 0, kWarpIssue = 1, kWarpRows = 2, kWarpScales = 3, kWarpEpi = 4, kEpiWarps = 8;
 constexpr int kThreads = 32 * (kWarpEpi + kEpiWarps);
@@ -59,13 +63,20 @@ constexpr int kSlots = 4;  // groups of four chunks' factors
 constexpr int kRegsLow = 72, kRegsEpi = 216;
 constexpr int kRegsLaunch = 32 * kWarpEpi * kRegsLow + 32 * kEpiWarps * kRegsEpi;
 
-template <int NB, bool PAIR>
+enum Kind { kOne, kTwo, kPair, kFew };
+
+template <Kind KIND>
 struct Cfg {
-  static_assert(NB == 2 || !PAIR, "a pair's unit has two blocks");
-  static constexpr int kWBytes = (PAIR ? 1 : NB) * 128 * 128;  // of this CTA
+  static constexpr bool kIsPair = KIND == kPair, kIsFew = KIND == kFew;
+  static constexpr int NB = KIND == kTwo || KIND == kPair ? 2 : 1;  // weight blocks of a unit
+  static constexpr int kRows = kIsFew ? kFewTile : kTile;           // of this CTA's tile
+  static constexpr int kTileRows = kIsPair ? 2 * kTile : kRows;
+  static constexpr int kRowBytes = kRows * 128;
+  static constexpr int kWBytes = (kIsPair ? 1 : NB) * 128 * 128;  // of this CTA
   static constexpr int kStage = kWBytes + kRowBytes;
-  static constexpr int kStages = kStage == 48 * 1024 ? 4 : 5;
-  static constexpr int kBuffers = 4 / NB;
+  static constexpr int kStages = kIsFew ? 10 : KIND == kTwo ? 4 : 5;
+  static constexpr int kColumns = kIsFew ? kFewTile : 128 * NB;  // of a buffer
+  static constexpr int kBuffers = kIsFew ? 8 : 4 / NB;
   static constexpr int kNumBars = 2 * kStages + 2 * kBuffers + 2 * kSlots + 1;
   static constexpr int kBarOff = kStages * kStage;
   static constexpr int kSlotOff = kBarOff + kNumBars * 8;  // tensor memory's address, the abort flag
@@ -74,11 +85,11 @@ struct Cfg {
   static constexpr int kTurn = 1024;  // an epilogue warp's
   // a group's factors: four chunks' of each row and block
   static constexpr int kScaleOff = kTurnOff + kEpiWarps * kTurn;
-  static constexpr int kScales = NB * kTile * 16;
+  static constexpr int kScales = NB * kRows * 16;
   static constexpr int kSmem = 1024 + kScaleOff + kSlots * kScales;
   static_assert(kStage % 1024 == 0, "operand tiles stay 1024-byte aligned");
   static_assert(kSmem <= 232448, "shared memory per CTA");
-  static_assert(kBuffers * NB * 128 <= static_cast<int>(kTmemCols), "tensor memory");
+  static_assert(kBuffers * kColumns <= static_cast<int>(kTmemCols), "tensor memory");
 };
 
 struct Args {
@@ -181,6 +192,13 @@ __device__ __forceinline__ void add_scaled(float2 (&acc)[8], const uint32_t (&p)
   }
 }
 
+// acc += f * p
+__device__ __forceinline__ void add_product(float2& acc, uint32_t p0, uint32_t p1, uint32_t f0, uint32_t f1) {
+  asm("{\n\t.reg .b64 p, f;\n\tmov.b64 p, {%1, %2};\n\tmov.b64 f, {%3, %4};\n\tfma.rn.f32x2 %0, p, f, %0;\n\t}"
+      : "+l"(reinterpret_cast<unsigned long long&>(acc))
+      : "r"(p0), "r"(p1), "r"(f0), "r"(f1));
+}
+
 // wait_bounded with a shorter way through: the clock (of the GPU, in 2^20 ns) is looked at every 1024 tries, and the wait
 // gives up about a second after the first look.
 __device__ __forceinline__ uint32_t millis() {
@@ -250,8 +268,8 @@ __device__ __forceinline__ int first_row(const Args& a, int e) {
 // Unit number x.  Expert e's units are consecutive, T tiles x upt: its tiles in chunks of eight, weight block after
 // weight block within a chunk, tile after tile within a weight block.
 // (upt_inv: ceil(2^64 / upt), by which a 32-bit quotient is one multiplication.)
-// TILE: rows of a tile, of which a pair's second CTA has the second half.
-template <int TILE>
+// TILE: rows of a tile, ROWS of them a CTA's (a pair's second CTA has the second half).
+template <int TILE, int ROWS>
 __device__ __forceinline__ Unit unit_of(const Args& a, const int32_t* first_tile, int x, int rank) {
   const int upt = a.upt;
   const int t = upt == 1 ? x : static_cast<int>(__umul64hi(static_cast<uint64_t>(x), a.upt_inv));
@@ -268,15 +286,15 @@ __device__ __forceinline__ Unit unit_of(const Args& a, const int32_t* first_tile
   Unit un;
   un.e = lo;
   un.u = u;
-  un.row0 = first_row(a, lo) + tile * TILE + rank * kTile;
-  un.nv = min(kTile, first_row(a, lo + 1) - un.row0);  // (not above 0: no rows)
+  un.row0 = first_row(a, lo) + tile * TILE + rank * ROWS;
+  un.nv = min(ROWS, first_row(a, lo + 1) - un.row0);  // (not above 0: no rows)
   return un;
 }
 
 // What every role of a CTA works with.
-template <int NB, bool PAIR>
+template <Kind KIND>
 struct Role {
-  using C = Cfg<NB, PAIR>;
+  using C = Cfg<KIND>;
   uint8_t* smem;
   uint32_t* err;
   uint32_t base, tmem;  // shared and tensor memory
@@ -310,7 +328,7 @@ struct Role {
     return wait_on(at, parity, reinterpret_cast<volatile uint32_t*>(smem + C::kSlotOff) + 1, err);
   }
   __device__ __forceinline__ Unit unit(const Args& a, int x) const {
-    return unit_of<PAIR ? 2 * kTile : kTile>(a, reinterpret_cast<const int32_t*>(smem + C::kPlanOff), x, rank);
+    return unit_of<C::kTileRows, C::kRows>(a, reinterpret_cast<const int32_t*>(smem + C::kPlanOff), x, rank);
   }
 };
 
@@ -423,13 +441,14 @@ __device__ __forceinline__ void store_columns(const Args& a, float2 (&acc)[32], 
   if (to >= 0) top = fmaxf(top, mine);
 }
 
-template <int NB, int OUT, bool PAIR>
+template <Kind KIND, int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 fp8_product_kernel(const __grid_constant__ Maps maps, const Args a) {
-  using C = Cfg<NB, PAIR>;
-  constexpr int kStages = C::kStages, kBuffers = C::kBuffers, kTileRows = PAIR ? 2 * kTile : kTile;
+  using C = Cfg<KIND>;
+  constexpr int NB = C::NB, kStages = C::kStages, kBuffers = C::kBuffers, kTileRows = C::kTileRows;
+  constexpr bool PAIR = C::kIsPair, FEW = C::kIsFew;
   extern __shared__ uint8_t smem_raw[];
-  Role<NB, PAIR> r0;
+  Role<KIND> r0;
   r0.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   r0.base = smem_u32(r0.smem);
   r0.err = a.err;
@@ -580,15 +599,17 @@ fp8_product_kernel(const __grid_constant__ Maps maps, const Args a) {
       if (elect_one()) {
         const auto r = r0.fresh();
         // kind::f8f6f4 with e4m3 operands: format code 0, the same bits as f16
-        constexpr uint32_t idesc = idesc_f16_f32(kTileRows, 128 * NB);
+        uint32_t idesc = idesc_f16_f32(FEW ? 128 : kTileRows, C::kColumns);
         uint32_t s = 0, sp = 0, b = 0, bp = 1;
-        bool ok = true, there = false;
+        bool ok = true, there = false, empty = false;
         for (int x = r.first; ok && x < r.total; x += r.stride) {
+          if constexpr (FEW) idesc = idesc_f16_f32(128, r.unit(a, x).nv <= 16 ? 16 : 32);
           for (int c = 0; c < r.chunks; ++c) {
             const uint32_t w = r.base + s * C::kStage;
-            const uint64_t ad = desc_kmajor_sw128(w + C::kWBytes), bd = desc_kmajor_sw128(w);
-            const uint32_t d = r.tmem + b * (128 * NB);
-            if ((!there && !r.wait(r.full(s), sp)) || !r.wait(r.acc_empty(b), bp)) {
+            const uint64_t rows = desc_kmajor_sw128(w + C::kWBytes), weights = desc_kmajor_sw128(w);
+            const uint64_t ad = FEW ? weights : rows, bd = FEW ? rows : weights;
+            const uint32_t d = r.tmem + b * C::kColumns;
+            if ((!there && !r.wait(r.full(s), sp)) || (!empty && !r.wait(r.acc_empty(b), bp))) {
               ok = false;
               break;
             }
@@ -600,7 +621,9 @@ fp8_product_kernel(const __grid_constant__ Maps maps, const Args a) {
             commit_to<PAIR>(r.empty(s));
             if (++s == kStages) s = 0, sp ^= 1;
             if (++b == kBuffers) b = 0, bp ^= 1;
+            // looked at ahead, so that one answer does not wait for the other (of two buffers none is free so early)
             there = mbar_test(r.full(s), sp);
+            if constexpr (kBuffers > 2) empty = mbar_test(r.acc_empty(b), bp);
           }
         }
         // every MMA issued above has completed once this arrives
@@ -621,15 +644,19 @@ fp8_product_kernel(const __grid_constant__ Maps maps, const Args a) {
         const Unit un = r.unit(a, x);
         const float* ws = a.w_scales + (static_cast<int64_t>(un.e) * a.nblocks + NB * un.u) * r.chunks;
         const int other = NB == 2 && 2 * un.u + 1 < a.nblocks ? r.chunks : 0;  // to the second block's
-        float4 next[4];
+        constexpr int kMine = C::kRows / 32;
+        float4 next[kMine];
         float next_w[NB][4];
         auto read = [&](int c0) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < kMine; ++i) {
             next[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (32 * i + lane < un.nv && c0 < r.chunks)
               next[i] = __ldg(reinterpret_cast<const float4*>(
                                   a.x_scales + (static_cast<int64_t>(un.row0) + 32 * i + lane) * a.x_pitch) + (c0 >> 2));
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int m = 0; m < NB; ++m) next_w[m][i] = c0 + i < r.chunks ? __ldg(ws + m * other + c0 + i) : 0.f;
           }
@@ -640,12 +667,18 @@ fp8_product_kernel(const __grid_constant__ Maps maps, const Args a) {
           ok = __all_sync(kAll, r.wait(r.scales_empty(s), ((g / kSlots) & 1) ^ 1));
           if (!ok) break;
           float4* to = reinterpret_cast<float4*>(r.smem + C::kScaleOff + s * C::kScales);
+          if constexpr (FEW) {  // of each chunk all rows' together
+            float* at = reinterpret_cast<float*>(to) + lane;
+            at[0] = next_w[0][0] * next[0].x, at[32] = next_w[0][1] * next[0].y;
+            at[64] = next_w[0][2] * next[0].z, at[96] = next_w[0][3] * next[0].w;
+          } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < kMine; ++i)
 #pragma unroll
-            for (int m = 0; m < NB; ++m)
-              to[kTile * m + 32 * i + lane] = make_float4(next_w[m][0] * next[i].x, next_w[m][1] * next[i].y,
-                                                         next_w[m][2] * next[i].z, next_w[m][3] * next[i].w);
+              for (int m = 0; m < NB; ++m)
+                to[kTile * m + 32 * i + lane] = make_float4(next_w[m][0] * next[i].x, next_w[m][1] * next[i].y,
+                                                           next_w[m][2] * next[i].z, next_w[m][3] * next[i].w);
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(r.scales_full(s));
           read(c0 + 4);
@@ -658,7 +691,7 @@ fp8_product_kernel(const __grid_constant__ Maps maps, const Args a) {
     // lane quarter; half of each block's columns
     const int q = warp & 3, hf = (warp - kWarpEpi) >> 2;
     const int tok = q * 32 + lane;
-    const uint32_t tcol0 = r.tmem + (static_cast<uint32_t>(q * 32) << 16) + 64u * hf;
+    const uint32_t tcol0 = r.tmem + (static_cast<uint32_t>(q * 32) << 16) + (FEW ? 16u : 64u) * hf;
     uint8_t* turn = r.smem + C::kTurnOff + (warp - kWarpEpi) * C::kTurn;
     uint32_t it = 0, g = 0;
     bool ok = true, there = false, scales_there = false;
@@ -670,83 +703,164 @@ fp8_product_kernel(const __grid_constant__ Maps maps, const Args a) {
         else mbar_arrive(r.acc_empty(b));
       }
     };
-    for (int x = r.first; ok && x < r.total; x += r.stride) {
-      const Unit un = r.unit(a, x);
-      const bool any = q * 32 < un.nv, valid = tok < un.nv;
-      const int64_t row = static_cast<int64_t>(un.row0) + tok;
-      float2 acc[NB][4][8];
+    if constexpr (FEW) {
+      // Lanes are weight rows here, columns the tile's rows: the first 16 of them of warps 4 to 7, the others of 8 to 11.
+      for (int x = r.first; ok && x < r.total; x += r.stride) {
+        const Unit un = r.unit(a, x);
+        const bool any = 16 * hf < un.nv;
+        float2 acc[8];
 #pragma unroll
-      for (int m = 0; m < NB; ++m)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) acc[m][i >> 3][i & 7] = make_float2(0.f, 0.f);
+        for (int i = 0; i < 8; ++i) acc[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
-      for (int c0 = 0; c0 < r.chunks; c0 += 4, ++g) {
-        if (!__all_sync(kAll, scales_there)) {
-          ok = __all_sync(kAll, r.wait(r.scales_full(g % kSlots), (g / kSlots) & 1));
-          if (!ok) break;
-        }
-        const uint32_t from = r.base + C::kScaleOff + (g % kSlots) * C::kScales;
-        float factor[NB][4];
-#pragma unroll
-        for (int m = 0; m < NB; ++m) {
-          const uint4 w = lds128(from + 16 * (kTile * m + tok));
-          factor[m][0] = __uint_as_float(w.x), factor[m][1] = __uint_as_float(w.y), factor[m][2] = __uint_as_float(w.z),
-          factor[m][3] = __uint_as_float(w.w);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (c0 + j >= r.chunks) break;
-          const int b = it % kBuffers;
-          if (!__all_sync(kAll, there)) {
-            ok = __all_sync(kAll, r.wait(r.acc_full(b), (it / kBuffers) & 1));
+        for (int c0 = 0; c0 < r.chunks; c0 += 4, ++g) {
+          if (!__all_sync(kAll, scales_there)) {
+            ok = __all_sync(kAll, r.wait(r.scales_full(g % kSlots), (g / kSlots) & 1));
             if (!ok) break;
           }
-          ++it;
-          tc_fence_after();
-          if (any) {
-            const uint32_t tcol = tcol0 + static_cast<uint32_t>(b) * (128 * NB);
-            constexpr int kPieces = 4 * NB;
-            // 16 columns are read while the 16 before them are added
-            uint32_t p[2][16];
-            tmem_ld16(tcol, p[0]);
+          const uint32_t from = r.base + C::kScaleOff + (g % kSlots) * C::kScales + 64 * hf;
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-              tmem_ld_wait();
-              if (i + 1 < kPieces) {
-                tmem_ld16(tcol + 128 * ((i + 1) >> 2) + 16 * ((i + 1) & 3), p[(i + 1) & 1]);
-              } else {
-                release(b);
-                there = mbar_test(r.acc_full(it % kBuffers), (it / kBuffers) & 1);
-                if (j == 3 || c0 + j + 1 >= r.chunks)
-                  scales_there = mbar_test(r.scales_full((g + 1) % kSlots), ((g + 1) / kSlots) & 1);
-              }
-              add_scaled(acc[i >> 2][i & 3], p[i & 1], factor[i >> 2][j]);
+          for (int j = 0; j < 4; ++j) {
+            if (c0 + j >= r.chunks) break;
+            uint4 f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = lds128(from + 128 * j + 16 * i);
+            const int b = it % kBuffers;
+            if (!__all_sync(kAll, there)) {
+              ok = __all_sync(kAll, r.wait(r.acc_full(b), (it / kBuffers) & 1));
+              if (!ok) break;
             }
-          } else {
+            ++it;
+            tc_fence_after();
+            uint32_t p[16];
+            if (any) {
+              tmem_ld16(tcol0 + static_cast<uint32_t>(b) * C::kColumns, p);
+              tmem_ld_wait();
+            }
             release(b);
-            there = scales_there = false;
+            there = mbar_test(r.acc_full(it % kBuffers), (it / kBuffers) & 1);
+            if (j == 3 || c0 + j + 1 >= r.chunks)
+              scales_there = mbar_test(r.scales_full((g + 1) % kSlots), ((g + 1) / kSlots) & 1);
+            if (any) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                add_product(acc[2 * i], p[4 * i], p[4 * i + 1], f[i].x, f[i].y);
+                add_product(acc[2 * i + 1], p[4 * i + 2], p[4 * i + 3], f[i].z, f[i].w);
+              }
+            }
           }
+          if (!ok) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(r.scales_empty(g % kSlots));
         }
         if (!ok) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(r.scales_empty(g % kSlots));
-      }
-      if (!ok) break;
-      if (!any) continue;
-      int to = -1;
-      float f = 1.f;
-      if (valid) {
-        to = a.out_pos ? __ldg(a.out_pos + row) : static_cast<int>(row);
-        if (to >= a.out_rows) to = -1;
-        if (a.row_weight && to >= 0) f = __ldg(a.row_weight + to);
-      }
-      float top = 0.f;  // largest magnitude, for f16's range
+        if (!any) continue;
+        // of row 16 hf + lane
+        int to = -1;
+        float f = 1.f;
+        if (lane < 16 && 16 * hf + lane < un.nv) {
+          const int64_t row = static_cast<int64_t>(un.row0) + 16 * hf + lane;
+          to = a.out_pos ? __ldg(a.out_pos + row) : static_cast<int>(row);
+          if (to >= a.out_rows) to = -1;
+          if (a.row_weight && to >= 0) f = __ldg(a.row_weight + to);
+        }
+        const int n = 128 * un.u + tok;  // this lane's weight row
+        float top = 0.f;
 #pragma unroll
-      for (int m = 0; m < NB; ++m) {
-        const int at = 128 * (NB * un.u + m) + 64 * hf;
-        if (at < a.n_out) store_columns<OUT>(a, reinterpret_cast<float2(&)[32]>(acc[m]), f, to, at, turn, top);
+        for (int i = 0; i < 16; ++i) {
+          const int t = __shfl_sync(kAll, to, i);
+          const float v = (i & 1 ? acc[i >> 1].y : acc[i >> 1].x) * __shfl_sync(kAll, f, i);
+          if (t < 0 || n >= a.n_out) continue;
+          const int64_t at = t * a.out_ld + n;
+          if constexpr (OUT == MOE_FP8_OUT_F32) {
+            static_cast<float*>(a.out)[at] = v;
+          } else if constexpr (OUT == MOE_FP8_OUT_F16) {
+            top = fmaxf(top, fabsf(v));
+            static_cast<__half*>(a.out)[at] = __float2half_rn(v);
+          } else {
+            static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+          }
+        }
+        if (OUT == MOE_FP8_OUT_F16 && __any_sync(kAll, top >= 65520.f) && lane == 0) atomicOr(r.err, DEV_ERR_RANGE);
       }
-      if (OUT == MOE_FP8_OUT_F16 && __any_sync(kAll, top >= 65520.f) && lane == 0) atomicOr(r.err, DEV_ERR_RANGE);
+    } else {
+      for (int x = r.first; ok && x < r.total; x += r.stride) {
+        const Unit un = r.unit(a, x);
+        const bool any = q * 32 < un.nv, valid = tok < un.nv;
+        const int64_t row = static_cast<int64_t>(un.row0) + tok;
+        float2 acc[NB][4][8];
+#pragma unroll
+        for (int m = 0; m < NB; ++m)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[m][i >> 3][i & 7] = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int c0 = 0; c0 < r.chunks; c0 += 4, ++g) {
+          if (!__all_sync(kAll, scales_there)) {
+            ok = __all_sync(kAll, r.wait(r.scales_full(g % kSlots), (g / kSlots) & 1));
+            if (!ok) break;
+          }
+          const uint32_t from = r.base + C::kScaleOff + (g % kSlots) * C::kScales;
+          float factor[NB][4];
+#pragma unroll
+          for (int m = 0; m < NB; ++m) {
+            const uint4 w = lds128(from + 16 * (kTile * m + tok));
+            factor[m][0] = __uint_as_float(w.x), factor[m][1] = __uint_as_float(w.y), factor[m][2] = __uint_as_float(w.z),
+            factor[m][3] = __uint_as_float(w.w);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (c0 + j >= r.chunks) break;
+            const int b = it % kBuffers;
+            if (!__all_sync(kAll, there)) {
+              ok = __all_sync(kAll, r.wait(r.acc_full(b), (it / kBuffers) & 1));
+              if (!ok) break;
+            }
+            ++it;
+            tc_fence_after();
+            if (any) {
+              const uint32_t tcol = tcol0 + static_cast<uint32_t>(b) * (128 * NB);
+              constexpr int kPieces = 4 * NB;
+              // 16 columns are read while the 16 before them are added
+              uint32_t p[2][16];
+              tmem_ld16(tcol, p[0]);
+#pragma unroll
+              for (int i = 0; i < kPieces; ++i) {
+                tmem_ld_wait();
+                if (i + 1 < kPieces) {
+                  tmem_ld16(tcol + 128 * ((i + 1) >> 2) + 16 * ((i + 1) & 3), p[(i + 1) & 1]);
+                } else {
+                  release(b);
+                  there = mbar_test(r.acc_full(it % kBuffers), (it / kBuffers) & 1);
+                  if (j == 3 || c0 + j + 1 >= r.chunks)
+                    scales_there = mbar_test(r.scales_full((g + 1) % kSlots), ((g + 1) / kSlots) & 1);
+                }
+                add_scaled(acc[i >> 2][i & 3], p[i & 1], factor[i >> 2][j]);
+              }
+            } else {
+              release(b);
+              there = scales_there = false;
+            }
+          }
+          if (!ok) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(r.scales_empty(g % kSlots));
+        }
+        if (!ok) break;
+        if (!any) continue;
+        int to = -1;
+        float f = 1.f;
+        if (valid) {
+          to = a.out_pos ? __ldg(a.out_pos + row) : static_cast<int>(row);
+          if (to >= a.out_rows) to = -1;
+          if (a.row_weight && to >= 0) f = __ldg(a.row_weight + to);
+        }
+        float top = 0.f;  // largest magnitude, for f16's range
+#pragma unroll
+        for (int m = 0; m < NB; ++m) {
+          const int at = 128 * (NB * un.u + m) + 64 * hf;
+          if (at < a.n_out) store_columns<OUT>(a, reinterpret_cast<float2(&)[32]>(acc[m]), f, to, at, turn, top);
+        }
+        if (OUT == MOE_FP8_OUT_F16 && __any_sync(kAll, top >= 65520.f) && lane == 0) atomicOr(r.err, DEV_ERR_RANGE);
+      }
     }
   }
   __syncthreads();
@@ -761,10 +875,12 @@ fp8_product_kernel(const __grid_constant__ Maps maps, const Args a) {
   if constexpr (PAIR) pair_sync();
 }
 
-template <int NB, int OUT, bool PAIR>
+template <Kind KIND, int OUT>
 cudaError_t launch(const Fp8ProductLaunch& g, cudaStream_t s) {
-  using C = Cfg<NB, PAIR>;
-  auto kern = fp8_product_kernel<NB, OUT, PAIR>;
+  using C = Cfg<KIND>;
+  constexpr int NB = C::NB;
+  constexpr bool PAIR = C::kIsPair;
+  auto kern = fp8_product_kernel<KIND, OUT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   if constexpr (NB == 2) {
@@ -808,8 +924,7 @@ cudaError_t launch(const Fp8ProductLaunch& g, cudaStream_t s) {
       return cudaErrorInvalidValue;
   if (PAIR && !encode_dense_map(&maps.weights, w->packed, moe_fp8_packed_bytes(w) / 128)) return cudaErrorInvalidValue;
   // The most units there can be: an expert's last tile may be short.
-  const int64_t tile = PAIR ? 2 * kTile : kTile;
-  const int64_t tiles = static_cast<int64_t>(g.rows) / tile + (g.rows < w->num_experts ? g.rows : w->num_experts);
+  const int64_t tiles = static_cast<int64_t>(g.rows) / C::kTileRows + (g.rows < w->num_experts ? g.rows : w->num_experts);
   const int64_t units = tiles * a.upt, most = PAIR ? g.num_sms / 2 : g.num_sms, at_once = units < most ? units : most;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(PAIR ? 2 * at_once : at_once));
@@ -827,15 +942,15 @@ cudaError_t launch(const Fp8ProductLaunch& g, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kern, maps, a);
 }
 
-// Which of the three variants: the one with the least estimate of its time, in quarters of 100 ns: rounds of units over the
-// SMs (the pairs) x chunks x the time of a chunk measured (380 ns with one block, 500 with two, 475 of a pair, and a
-// pair's 0.8 us more to start), the experts' last tiles being half full where the rows are not known to the host.
-// Where weights are read for few rows each, a chunk's time is that of its bytes, and two blocks take 700.  Measured, in us
-// on one GB300 (rows x n_out x k: one block | two | pair):
-//   256 x 7168 x 7168: 22.8 | 29.1 | 29.9                  512: 41.0 | 30.8 | 30.8        8192: - | 333 | 318
-//   2048 x 2048 x 7168: 41.2 | 30.8 | 31.2                 1024: 23.0 | 28.9 | 29.6
-//   64 experts x 2048 x 2048, 8 rows each: 48.8 | 51.8 | 69.0         1024 each: 354 | 289 | 301
-//   256 experts x 4096 x 7168, 16 rows each: 1115 | 1045 | 1441       32 experts, 2048 each: 2043 | 1564 | 1523
+// Which of the four kinds: the one with the least estimate of its time, in units of 25 ns: rounds of units over the SMs
+// (the pairs) x chunks x the time of a chunk measured (300 ns with one block, 500 with two, 475 of a pair, and a pair's
+// 0.8 us more to start), the experts' last tiles being half full where the rows are not known to the host.  Where weights
+// are read for few rows each, a chunk's time is that of its bytes: 375 ns with one block, a little more by tiles of 128
+// rows than by those of 32, and 700 with two.  Measured, in us on one GB300 (rows x n_out x k: few | one | two | pair):
+//   1 x 7168 x 7168: 16.2 | 18.2 | 26.7 | 32.6             256: 41.8 | 20.1 | 29.2 | 30.5      512: 80 | 35.5 | 31.4 | 31.3
+//   1024 x 7168 x 7168: 155 | 52.2 | 57.4 | 57.5           2048: 305 | 102 | 85.8 | 83.5       8192: 1187 | 393 | 330 | 317
+//   64 experts x 2048 x 2048, 8 rows each: 45.0 | 47.4 | 51.3 | 68.5     64: 79 | 50.1 | 55.6 | 72.6     1024: 967 | 332 | 287 | 302
+//   256 experts x 4096 x 7168, 16 rows each: 1064 | 1080 | 1034 | 1386   32 experts, 2048 each: 5565 | 1784 | 1530 | 1499
 template <int OUT>
 cudaError_t launch_out(const Fp8ProductLaunch& g, cudaStream_t s) {
   const int64_t experts = g.rows < g.w->num_experts ? g.rows : g.w->num_experts, k = fp8_blocks(g.w->k);
@@ -843,13 +958,17 @@ cudaError_t launch_out(const Fp8ProductLaunch& g, cudaStream_t s) {
     const int64_t half_full = (g.rows + tile / 2 * (experts - 1) + tile - 1) / tile;
     return ((half_full > experts ? half_full : experts) * units + at_once - 1) / at_once;
   };
-  const bool few = g.rows <= 64 * experts;
-  const int64_t one = rounds(kTile, fp8_blocks(g.w->n_out), g.num_sms) * k * 15;
-  const int64_t two = rounds(kTile, fp8_units(g.w), g.num_sms) * k * (few ? 28 : 20);
-  const int64_t pair = rounds(2 * kTile, fp8_units(g.w), g.num_sms / 2) * k * 19 + 30;
+  const int64_t sms = g.num_sms, blocks = fp8_blocks(g.w->n_out), units = fp8_units(g.w);
+  const int64_t one = rounds(kTile, blocks, sms), two = rounds(kTile, units, sms);
+  if (g.rows <= 64 * experts) {
+    const int64_t few = rounds(kFewTile, blocks, sms);
+    if (few * 15 < one * 16 && few * 15 < two * 28) return launch<kFew, OUT>(g, s);
+    return one * 16 <= two * 28 ? launch<kOne, OUT>(g, s) : launch<kTwo, OUT>(g, s);
+  }
+  const int64_t pair = rounds(2 * kTile, units, sms / 2) * k * 19 + 30;
   const bool mapped = moe_fp8_packed_bytes(g.w) / 128 <= 0x7fffffffu;  // a map's rows are counted in 32 bits
-  if (mapped && !few && pair < one && pair < two) return launch<2, OUT, true>(g, s);
-  return one <= two ? launch<1, OUT, false>(g, s) : launch<2, OUT, false>(g, s);
+  if (mapped && pair < one * k * 12 && pair < two * k * 20) return launch<kPair, OUT>(g, s);
+  return one * 12 <= two * 20 ? launch<kOne, OUT>(g, s) : launch<kTwo, OUT>(g, s);
 }
 
 }  // namespace

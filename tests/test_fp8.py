@@ -235,6 +235,30 @@ def test_large_tiles_with_positions_weights_and_values_that_are_not_finite():
     assert (got[rest] == 9).all()
 
 
+@pytest.mark.parametrize("out_type", DTYPES)
+@pytest.mark.parametrize("sizes,n_out,k", [([32], 300, 272), ([17], 1001, 144), ([33, 0, 16, 41], 129, 1552), ([64], 64, 640)])
+def test_few_rows_with_positions_and_weights(out_type, sizes, n_out, k):
+    rows, E = sum(sizes), len(sizes)
+    x, w, wv = make(rows, rows, E, n_out, k)
+    offsets = [sum(sizes[:e]) for e in range(E + 1)]
+    check_product(x, w, wv, offsets, out_type)
+    want, size = plain.product(plain.values(x.codes.cpu(), x.scales.cpu()), wv, offsets)
+    tol = plain.tolerance(want, size, k, DTYPES[out_type])
+    at = torch.randperm(rows + 6, generator=gen(1))[:rows].to(torch.int32)
+    at[2], at[rows - 1] = -1, rows + 6
+    weight = torch.rand(rows + 6, generator=gen(2)) * 3 - 1
+    room = torch.full((rows + 6, n_out + 3), 9.0, dtype=DTYPES[out_type], device="cuda")
+    mx.fp8_grouped_product(x, w, torch.tensor(offsets, dtype=torch.int32, device="cuda"), out=room[:, 1:1 + n_out],
+                           out_pos=at.cuda(), row_weight=weight.cuda(), out_type=out_type)
+    got = room.cpu().double()
+    on = (at >= 0) & (at < rows + 6)
+    to, f = at[on].long(), weight.double()[at[on].long()][:, None]
+    assert within(got[to, 1:1 + n_out], want[on] * f, tol[on] * f.abs(), 1e-30)
+    rest = torch.ones(rows + 6, dtype=torch.bool)
+    rest[to] = False
+    assert (got[rest] == 9).all() and (got[:, 0] == 9).all() and (got[:, 1 + n_out:] == 9).all()
+
+
 def test_rows_of_no_expert_stay():
     x, w, wv = make(5, 400, 3, 260, 144)
     for offsets in ([7, 7, 150, 390], [0, 0, 0, 0], [400, 400, 400, 400], [129, 130, 131, 132]):
