@@ -75,7 +75,7 @@ size_t moe_balance_workspace_size(const moe_router *r, int64_t n_tokens, int64_t
 /* The balance loss and the counts.
  *   topk_ids     [n, top_k] int32; entries outside [0, E) are not counted
  *   seq_offsets  [num_sequences + 1] int32, ascending from >= 0 to <= n; NULL: one sequence of all rows
- *                (num_sequences = 1).  Anything else gives a loss of NaN and counts of 0.
+ *                (num_sequences = 1).  Anything else gives a loss of NaN, and counts that mean nothing.
  *   counts       [num_sequences, E] int32 out
  *   loss         [1] fp32 out
  *   workspace    moe_balance_workspace_size bytes, 256-byte aligned
