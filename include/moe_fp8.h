@@ -4,7 +4,7 @@
  *
  * Rows: e4m3 codes [rows][cols], dense, and one fp32 scale per 128 columns,
  * [rows][moe_fp8_scale_pitch(cols)] (the last block may be short; entries past it
- * are never read and not written).  Value = code * scale.  cols is a multiple of
+ * are not used and not written).  Value = code * scale.  cols is a multiple of
  * 16; both bases are 16-byte aligned.
  * Quantising a block with largest magnitude a, as MOE_ACT_FP8_DYNAMIC does:
  *   scale = a / 448 in fp32, 1 for a block of zeros
@@ -40,7 +40,8 @@ int64_t moe_fp8_scale_pitch(int64_t cols);
 
 /* Rows quantised: row t of x to row positions[t * k + j] for each j.
  *   x          [n] rows of d bf16, x_ld elements apart (>= d, a multiple of 8); 16-byte aligned
- *   positions  [n, k] int32; NULL: k = 1 and row t.  Entries outside [0, out_rows) are skipped.
+ *   positions  [n, k] int32; NULL: k = 1 and row t.  Entries outside [0, out_rows) are skipped; a row that two
+ *              entries name holds parts of either.
  *   codes, scales  [out_rows] rows
  * d a multiple of 16 up to 16384. */
 moe_status moe_fp8_quantise(int64_t n, int32_t k, int32_t d, const void *x, int64_t x_ld, const int32_t *positions,
@@ -88,7 +89,8 @@ size_t moe_fp8_packed_bytes(const moe_fp8_weights *w);
  *                   num_experts is 1: all rows.
  *   out             [out_rows] rows of n_out (out_type), out_ld elements apart (>= n_out), aligned to their
  *                   elements (fastest with 32-byte aligned rows)
- *   out_pos         [rows] int32, NULL = r.  Rows sent outside [0, out_rows) are skipped.
+ *   out_pos         [rows] int32, NULL = r.  Rows sent outside [0, out_rows) are skipped; a row that two are sent to
+ *                   holds parts of either.
  *   row_weight      [out_rows] fp32 or NULL = 1
  *   workspace       MOE_FP8_PRODUCT_WORKSPACE bytes, 256-byte aligned; its error word accumulates until
  *                   moe_get_error reads it (zero it once).  f16 results beyond its range raise MOE_ERR_RANGE. */

@@ -78,7 +78,8 @@ size_t moe_balance_workspace_size(const moe_router *r, int64_t n_tokens, int64_t
  *                (num_sequences = 1).  Anything else gives a loss of NaN, and counts that mean nothing.
  *   counts       [num_sequences, E] int32 out
  *   loss         [1] fp32 out
- *   workspace    moe_balance_workspace_size bytes, 256-byte aligned
+ *   workspace    moe_balance_workspace_size bytes, 256-byte aligned; calls that may run at the same time (two
+ *                captured graphs, two streams) need one each
  * num_sequences 1 to 65536.  n = 0: counts and loss are set to 0. */
 moe_status moe_balance_loss(const moe_router *r, int64_t n_tokens, const void *logits, int64_t logits_ld,
                             const int32_t *topk_ids, float coef, const int32_t *seq_offsets, int64_t num_sequences,
@@ -91,7 +92,8 @@ moe_status moe_balance_loss(const moe_router *r, int64_t n_tokens, const void *l
  *   counts       [num_sequences, E] as moe_balance_loss wrote them, or NULL: no such part
  *   coef, seq_offsets, num_sequences   as in moe_balance_loss; not used without counts
  *   d_loss       [1] fp32, NULL = 1
- *   d_logits     [n] rows of E in the logits' type, d_ld elements apart (>= E); may be logits itself (same stride)
+ *   d_logits     [n] rows of E in the logits' type, d_ld elements apart (>= E); may be logits itself (same stride), else
+ *                nothing that logits' rows hold
  * Every row is written, one without a part with zeros. */
 moe_status moe_route_backward(const moe_router *r, int64_t n_tokens, const void *logits, int64_t logits_ld,
                               const int32_t *topk_ids, const float *d_weight, float coef, const int32_t *counts,

@@ -660,7 +660,7 @@ route_pairs_kernel(const RouteLaunch a) {
     float sure = -kInf;
     for (int j = deep - 1; j > 0 && __any_sync(kAll, found > 16); --j) {
       const float t = __shfl_sync(kAll, sorted, j - 1, 16);
-      if (found > 16) {
+      if (found > 16 && t < kInf) {  // (an infinite one is left to the whole warp)
         sure = t - margin(t), low = sure - margin(t);
         mask = 0;
 #pragma unroll

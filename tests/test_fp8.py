@@ -417,6 +417,33 @@ def test_a_block_of_them_beside_the_librarys_own():
     assert torch.equal(got, out) and mx.moe_get_error(ws) == mx.MOE_OK
 
 
+@pytest.mark.parametrize("rows,E,n_out,k", [(1300, 1, 2048, 7168), (5000, 2, 640, 304), (700, 1, 384, 640), (40, 3, 512, 400)])
+def test_captured_products_follow_their_inputs(rows, E, n_out, k):
+    # each kind of tile, captured and replayed on other rows and other offsets, with another product in front
+    x, w, _ = make(1, rows, E, n_out, k)
+    other, _, _ = make(2, rows, E, n_out, k)
+    first, second = ragged(1, rows, E), ragged(2, rows, E)
+    off = torch.tensor(first, dtype=torch.int32, device="cuda")
+    held = mx.Fp8Rows(x.codes.clone(), x.scales.clone())
+    out, ws = torch.zeros(rows, n_out, dtype=torch.float32, device="cuda"), mx.mx_workspace()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        for _ in range(2):
+            mx.fp8_grouped_product(held, w, off, out=out, out_type=mx.MOE_FP8_OUT_F32, ws=ws)
+    for rows_now, offsets in ((x, first), (other, second), (x, second)):
+        held.codes.copy_(rows_now.codes)
+        held.scales.copy_(rows_now.scales)
+        off.copy_(torch.tensor(offsets, dtype=torch.int32))
+        graph.replay()
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        want = mx.fp8_grouped_product(rows_now, w, off, out_type=mx.MOE_FP8_OUT_F32, ws=ws, stream=stream.cuda_stream)
+        torch.cuda.synchronize()
+        assert same_bits(out, want)
+    assert mx.moe_get_error(ws) == mx.MOE_OK
+
+
 def test_other_streams_share_a_workspace():
     x, w, _ = make(1, 2000, 2, 600, 512)
     off = torch.tensor([0, 900, 2000], dtype=torch.int32, device="cuda")

@@ -180,6 +180,21 @@ def test_close_scores_among_many_rows(kind):
     check_many(x, k, kind, b, True)
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("infinite", [1, 5, 8, 9, 40])
+def test_infinite_biases_among_many_rows(kind, infinite):
+    n, E, k = 6000, 384, 8
+    x = logits_of(infinite, n, E)
+    x[:3000] = x[:3000].round()                   # many equal ones: more candidates than a half has room for
+    x[::7, 3] = -INF                              # masked, whatever the bias
+    b = torch.randn(E, generator=gen(5)) * 0.05
+    b[torch.randperm(E, generator=gen(infinite))[:infinite]] = INF
+    b[3] = INF
+    check_many(x, k, kind, b, True)
+    b[b == INF] = 1e30
+    check_many(x, k, kind, b, False)
+
+
 def test_the_callers_tensors_and_nothing_around_them():
     n, E, k = 70, 48, 5
     x = logits_of(1, n, E).cuda()
