@@ -20,8 +20,8 @@
 // HBM would bound all three; what they spend beyond it is a row's way through its reductions
 // (202 instructions a row of 384 in the first, 385 in the gradient, issued in 50 to 60 % of
 // the cycles) with the warps that registers leave.  65,536 x 384 fp32, sigmoid, k = 8, 16
-// sequences, on one GB300: loss 27.3 us (3.7 TB/s), 20 of them the first kernel; gradient
-// 40.6 us (5.1 TB/s).  (Two rows a warp, half the instructions a row and half the warps: 21.5
+// sequences, on one GB300: loss 26.1 us (3.9 TB/s), 19 of them the first kernel; gradient
+// 39.3 us (5.2 TB/s).  (Two rows a warp, half the instructions a row and half the warps: 21.5
 // for the first kernel's 21.)
 #include "router.cuh"
 
@@ -445,8 +445,8 @@ static cudaError_t allow_smem(K kern, size_t bytes) {
 }
 
 BalancePlan balance_plan(int64_t n) {
-  // A row a warp at least; at most what the SMs hold at once of 384 experts (67 KB each: three an SM).
-  constexpr int64_t kMost = 456, kLeast = 8;
+  // A row a warp at least; at most what the SMs hold at once of 384 experts (64 registers a thread: four an SM).
+  constexpr int64_t kMost = 608, kLeast = 8;
   int64_t chunk = (n + kMost - 1) / kMost;
   if (chunk < kLeast) chunk = kLeast;
   if (chunk > n) chunk = n < 1 ? 1 : n;

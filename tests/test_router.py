@@ -223,12 +223,12 @@ def ids_of(seed, n, k, E):
 
 def loss_error(logits, live_rows):
     """Relative: a share (a sigmoid's e^-l is within |l| 2^-24, below the 2 spread + 5 units that score_error has for more:
-    these logits have both signs), and sums of positive values: a CTA's run of max(8, n / 456) rows by eight warps, eight warps,
-    up to 457 pieces by eight warps, 32 experts, E / 32 parts and the sequences by 256 threads (24 for up to 6000 of them and
+    these logits have both signs), and sums of positive values: a CTA's run of max(8, n / 608) rows by eight warps, eight warps,
+    up to 609 pieces by eight warps, 32 experts, E / 32 parts and the sequences by 256 threads (24 for up to 6000 of them and
     13 to join), besides a handful of products."""
     n, E = logits.shape
-    run = max(8, n / 456)
-    return (2 * plain.score_error(logits) + run / 8 + 8 + 58 + 8 + 5 + E / 32 + 24 + 13 + 10) * EPS
+    run = max(8, n / 608)
+    return (2 * plain.score_error(logits) + run / 8 + 8 + 77 + 8 + 5 + E / 32 + 24 + 13 + 10) * EPS
 
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
