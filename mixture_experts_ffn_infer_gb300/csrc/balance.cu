@@ -34,14 +34,15 @@ constexpr float kTiny = 1e-20f;
 
 // The scores of a row and what makes shares of them (0 where every logit is -inf).
 template <typename Row>
-__device__ __forceinline__ float share_scores(bool sigmoid, const float (&l)[Row::width], float2 (&s)[Row::width / 2]) {
+__device__ __forceinline__ float share_scores(bool sigmoid, const float (&l)[Row::width], float2 (&s)[Row::width / 2],
+                                              uint32_t mask) {
   constexpr int V = Row::width;
   float shift = 0.f;
   if (!sigmoid) {
     float top = l[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) top = max_nan(top, l[i]);
-    top = warp_max_nan(top);
+    top = lanes_max_nan<Row::lanes>(top, mask);
     shift = top == -kInf ? 0.f : top;
   }
   float2 sum = both(0.f);
@@ -51,7 +52,7 @@ __device__ __forceinline__ float share_scores(bool sigmoid, const float (&l)[Row
     s[i] = sigmoid ? sigmoid_short(v) : softmax_term(v, shift);
     sum = add2(sum, s[i]);
   }
-  const float total = warp_sum(sum.x + sum.y);
+  const float total = lanes_sum<Row::lanes>(sum.x + sum.y, mask);
   return total == 0.f ? 0.f : reciprocal(total);
 }
 
@@ -81,28 +82,32 @@ __device__ __forceinline__ const int32_t* hold_offsets(const int32_t* offsets, i
 }
 
 template <typename Row>
+constexpr int kRowsAtOnce = 32 * kRowWarps / Row::lanes;  // of a CTA
+
+template <typename Row>
 __global__ void __launch_bounds__(32 * kRowWarps, Row::width <= 12 ? 4 : 1)
 balance_rows_kernel(const BalanceLaunch a, const BalancePlan plan) {
   using T = typename Row::type;
-  constexpr int V = Row::width;
+  constexpr int V = Row::width, L = Row::lanes, kRows = kRowsAtOnce<Row>;
   __shared__ int32_t held[kHeld];
-  extern __shared__ __align__(16) float joined[];  // [warps][E], the counts [E], the rings
+  extern __shared__ __align__(16) float joined[];  // [rows at once][E], the counts [E], the rings
   pdl_wait();
   pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = threadIdx.x / L, lane = threadIdx.x % L;
+  const uint32_t mask = lanes_mask<L>();
   const int E = a.r.num_experts, k = a.r.top_k;
   const bool sigmoid = a.r.score == MOE_SCORE_SIGMOID;
   const int64_t r0 = blockIdx.x * plan.chunk, r1 = min(r0 + plan.chunk, a.n);
   const T* logits = static_cast<const T*>(a.logits);
-  // this warp's rows: r0 + warp and every eighth from there on
-  const int64_t first = r0 + warp;
-  const RowRing<Row> ring{smem_u32(joined + (kRowWarps + 1) * E) + static_cast<uint32_t>(warp * RowRing<Row>::warp_bytes(E)),
+  // this warp's (or part of one's) rows: r0 + sub and every kRows-th from there on
+  const int64_t first = r0 + sub;
+  const RowRing<Row> ring{smem_u32(joined + (kRows + 1) * E) + static_cast<uint32_t>(sub * RowRing<Row>::warp_bytes(E)),
                           RowRing<Row>::row_bytes(E)};
   auto row_at = [&](int64_t t) { return t < r1 ? logits + t * a.ld : nullptr; };
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) ring.ask(i, row_at(first + kRowWarps * i), E, lane);
+  for (int i = 0; i < kAhead; ++i) ring.ask(i, row_at(first + kRows * i), E, lane);
   const int32_t* offsets = hold_offsets(a.offsets, a.sequences, held);
-  int32_t* hist = reinterpret_cast<int32_t*>(joined + kRowWarps * E);
+  int32_t* hist = reinterpret_cast<int32_t*>(joined + kRows * E);
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
   for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
   __syncthreads();
@@ -110,7 +115,7 @@ balance_rows_kernel(const BalanceLaunch a, const BalancePlan plan) {
   int number = 0;  // t's in the ring
   // the chosen experts of the next two rows, one a lane
   auto id_at = [&](int64_t t) { return lane < k && t < r1 ? a.ids[t * k + lane] : -1; };
-  int ids[2] = {id_at(first), id_at(first + kRowWarps)};
+  int ids[2] = {id_at(first), id_at(first + kRows)};
   for (int s = sequence_of(offsets, a.sequences, a.n, r0); s < a.sequences; ++s) {
     const int64_t lo = max(r0, offset_at(offsets, a.n, s)), hi = min(r1, offset_at(offsets, a.n, s + 1));
     if (lo >= r1) break;
@@ -118,16 +123,16 @@ balance_rows_kernel(const BalanceLaunch a, const BalancePlan plan) {
     float2 sum[V / 2];
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) sum[i] = both(0.f);
-    for (; t < hi; t += kRowWarps, ++number) {
+    for (; t < hi; t += kRows, ++number) {
       const bool in = t >= lo;  // (rows in front of the first sequence are not)
       float l[V];
       ring.take(number, logits + t * a.ld, E, lane, -kInf, l);
-      ring.ask(number + kAhead, row_at(t + kRowWarps * kAhead), E, lane);
+      ring.ask(number + kAhead, row_at(t + kRows * kAhead), E, lane);
       if (in && ids[0] >= 0 && ids[0] < E) atomicAdd(hist + ids[0], 1);
       ids[0] = ids[1];
-      ids[1] = id_at(t + 2 * kRowWarps);
+      ids[1] = id_at(t + 2 * kRows);
       float2 q[V / 2];
-      const float inv = share_scores<Row>(sigmoid, l, q);
+      const float inv = share_scores<Row>(sigmoid, l, q, mask);
       if (in) {
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) sum[i] = fma2(q[i], both(inv), sum[i]);
@@ -135,13 +140,13 @@ balance_rows_kernel(const BalanceLaunch a, const BalancePlan plan) {
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (Row::expert(i, lane) < E) joined[warp * E + Row::expert(i, lane)] = i & 1 ? sum[i >> 1].y : sum[i >> 1].x;
+      if (Row::expert(i, lane) < E) joined[sub * E + Row::expert(i, lane)] = i & 1 ? sum[i >> 1].y : sum[i >> 1].x;
     __syncthreads();
     const int64_t piece = static_cast<int64_t>(blockIdx.x) + s;
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kRowWarps; ++w) v += joined[w * E + e];
+      for (int w = 0; w < kRows; ++w) v += joined[w * E + e];
       a.sums[piece * E + e] = v;
       a.hist[piece * E + e] = hist[e];
       hist[e] = 0;
@@ -252,19 +257,20 @@ template <typename Row>
 __global__ void __launch_bounds__(32 * kRowWarps, kGradResident<Row>)
 route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
   using T = typename Row::type;
-  constexpr int V = Row::width;
-  extern __shared__ __align__(16) float scatter[];  // [warps][32 V]: ds at the chosen experts, zeros elsewhere; the rings
+  constexpr int V = Row::width, L = Row::lanes;
+  extern __shared__ __align__(16) float scatter[];  // [rows at once][L V]: ds at the chosen experts, zeros elsewhere; the rings
   __shared__ int lives[kRowWarps];
   __shared__ int32_t held[kHeld];
   pdl_wait();
   pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int subs = blockDim.x / L, sub = threadIdx.x / L, lane = threadIdx.x % L;
+  const uint32_t mask = lanes_mask<L>();
   const int E = a.r.num_experts, k = a.r.top_k;
   const bool sigmoid = a.r.score == MOE_SCORE_SIGMOID;
   const int32_t* offsets = a.counts ? hold_offsets(a.offsets, a.sequences, held) : nullptr;
-  float* ds = scatter + warp * (32 * V);
+  float* ds = scatter + sub * (L * V);
 #pragma unroll
-  for (int i = 0; i < V; ++i) ds[32 * i + lane] = 0.f;
+  for (int i = 0; i < V; ++i) ds[L * i + lane] = 0.f;
   float factor = 0.f;  // d_loss coef E / (S k)
   if (a.counts) {
     __syncthreads();
@@ -272,19 +278,19 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
     for (int s = threadIdx.x; s < a.sequences; s += blockDim.x)
       live += offset_at(offsets, a.n, s + 1) > offset_at(offsets, a.n, s) ? 1 : 0;
     live = __reduce_add_sync(kAll, live);
-    if (lane == 0) lives[warp] = live;
+    if ((threadIdx.x & 31) == 0) lives[threadIdx.x >> 5] = live;
     __syncthreads();
     live = 0;
     for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) live += lives[w];
     factor = (a.d_loss ? __ldg(a.d_loss) : 1.f) * (a.coef * static_cast<float>(E) / (static_cast<float>(k) * live));
   }
-  __syncwarp();
+  __syncwarp(mask);
   const uint32_t ds_at = smem_u32(ds + 4 * lane);  // this lane's first four
-  // a warp's rows follow one another, so that a sequence's counts stay in its registers
-  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp) * run, t1 = min(t0 + run, a.n);
+  // a warp's (or part of one's) rows follow one another, so that a sequence's counts stay in its registers
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * subs + sub) * run, t1 = min(t0 + run, a.n);
   if (t0 >= t1) return;
   const T* logits = static_cast<const T*>(a.logits);
-  const RowRing<Row> ring{smem_u32(scatter + (blockDim.x >> 5) * (32 * V)) + static_cast<uint32_t>(warp * RowRing<Row>::warp_bytes(E)),
+  const RowRing<Row> ring{smem_u32(scatter + subs * (L * V)) + static_cast<uint32_t>(sub * RowRing<Row>::warp_bytes(E)),
                           RowRing<Row>::row_bytes(E)};
   auto row_at = [&](int64_t t) { return t < t1 ? logits + t * a.ld : nullptr; };
 #pragma unroll
@@ -319,7 +325,7 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
     const int number = static_cast<int>(t - t0);
     ring.take(number, logits + t * a.ld, E, lane, -kInf, l);
     ring.ask(number + kAhead, row_at(t + kAhead), E, lane);
-    __syncwarp();  // (the row is in the ring for every lane)
+    __syncwarp(mask);  // (the row is in the ring for every lane)
     const float lj = id >= 0 ? ring.one(number, logits + t * a.ld, id) : -kInf;
     if (a.counts && t >= until) {
       // sequences that end at or in front of t are over; between two (and behind the last) there are none
@@ -352,7 +358,7 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) top = max_nan(top, l[i]);
-      top = warp_max_nan(top);
+      top = lanes_max_nan<L>(top, mask);
       shift = top == -kInf ? 0.f : top;
 #pragma unroll
       for (int i = 0; i < V / 2; ++i) {
@@ -361,7 +367,7 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
         dot2 = fma2(c[i], v[i], dot2);
       }
     }
-    const float total = warp_sum(total2.x + total2.y), inv = total == 0.f ? 0.f : reciprocal(total);
+    const float total = lanes_sum<L>(total2.x + total2.y, mask), inv = total == 0.f ? 0.f : reciprocal(total);
     // (NaN of a row that holds one: total is)
     const bool bad = total != total;
     float dot = dot2.x + dot2.y, dj = 0.f;  // dj: ds of the lane's chosen expert
@@ -370,32 +376,32 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
       dj = g;
       if (a.r.normalise) {
         const float chosen = id >= 0 ? sj : 0.f;
-        const float sum = warp_sum(chosen) + kTiny, with = warp_sum(g * chosen);
+        const float sum = lanes_sum<L>(chosen, mask) + kTiny, with = lanes_sum<L>(g * chosen, mask);
         dj = __fdividef(g - __fdividef(with, sum), sum);
       }
-      const uint32_t same = __match_any_sync(kAll, id);
-      if (__any_sync(kAll, id >= 0 && (same & (same - 1u)) != 0)) {
+      const uint32_t same = __match_any_sync(mask, id);
+      if (__any_sync(mask, id >= 0 && (same & (same - 1u)) != 0)) {
         // an expert named twice: its entries in order
         for (int j = 0; j < k; ++j) {
           if (lane == j && id >= 0) ds[id] += dj;
-          __syncwarp();
+          __syncwarp(mask);
         }
       } else if (id >= 0) {
         ds[id] = dj;
       }
-      __syncwarp();
+      __syncwarp(mask);
     }
     // d = (c scale + rest + ds) v
     float scale = 0.f, rest = 0.f;
     if (sigmoid) {
       if (a.counts) {
-        dot = warp_sum(dot) * inv;
+        dot = lanes_sum<L>(dot, mask) * inv;
         scale = inv;
         rest = -dot * inv;
       }
     } else {
       // of the shares: v inv
-      dot = warp_sum(fmaf(dot, inv, id >= 0 ? dj * sj : 0.f));
+      dot = lanes_sum<L>(fmaf(dot, inv, id >= 0 ? dj * sj : 0.f), mask);
       scale = inv;
       rest = -dot * inv;
     }
@@ -405,13 +411,13 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
       if constexpr (Row::vec) {
 #pragma unroll
         for (int j = 0; j < V / 4; ++j) {
-          const uint4 q = lds128(ds_at + 512 * j);
+          const uint4 q = lds128(ds_at + 16 * L * j);
           add[4 * j] = __uint_as_float(q.x), add[4 * j + 1] = __uint_as_float(q.y), add[4 * j + 2] = __uint_as_float(q.z),
                   add[4 * j + 3] = __uint_as_float(q.w);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) add[i] = ds[32 * i + lane];
+        for (int i = 0; i < V; ++i) add[i] = ds[L * i + lane];
       }
     }
 #pragma unroll
@@ -428,9 +434,9 @@ route_grad_kernel(const RouteGradLaunch a, const int64_t run) {
       for (int i = 0; i < V; ++i) d[i] = kNaN;
     }
     Row::store(static_cast<T*>(a.d_logits) + t * a.d_ld, E, lane, d);
-    __syncwarp();
+    __syncwarp(mask);
     if (id >= 0) ds[id] = 0.f;
-    __syncwarp();
+    __syncwarp(mask);
   }
   ring.end();
 }
@@ -454,12 +460,22 @@ BalancePlan balance_plan(int64_t n) {
   return BalancePlan{chunk, static_cast<int32_t>(chunks < 1 ? 1 : chunks)};  // without rows one CTA, for the ticket
 }
 
+// More rows than the SMs hold at once, one to a warp: short ones several to a warp, so that what is done once a row is done for
+// all of them.  (For fewer rows the way through one counts, which is the same: 5,000 rows take 9 and 6.5 us either way.)  On
+// one GB300, us, several | one: loss of 50,000 x 48 12.7 | 15.8, of 200,000 x 8 15.8 | 34.2; gradient of 50,000 x 48 21.4 | 26.5, of
+// 200,000 x 8 33 | 80.
+template <typename F>
+static cudaError_t with_rows_of(const moe_router& r, int64_t n, bool vec, F f) {
+  return n > 32 * static_cast<int64_t>(device_sms()) ? with_short_row(r, vec, f) : with_row(r, vec, f);
+}
+
 cudaError_t launch_balance(const BalanceLaunch& a, cudaStream_t s) {
   const BalancePlan plan = balance_plan(a.n);
-  cudaError_t e = with_row(a.r, rows_by_four(a.r, a.logits, a.ld), [&](auto row) {
+  cudaError_t e = with_rows_of(a.r, a.n, rows_by_four(a.r, a.logits, a.ld), [&](auto row) {
     using Row = decltype(row);
     auto kern = balance_rows_kernel<Row>;
-    const size_t smem = (kRowWarps + 1) * sizeof(float) * a.r.num_experts + kRowWarps * RowRing<Row>::warp_bytes(a.r.num_experts);
+    const size_t smem = (kRowsAtOnce<Row> + 1) * sizeof(float) * a.r.num_experts +
+                        kRowsAtOnce<Row> * RowRing<Row>::warp_bytes(a.r.num_experts);
     const cudaError_t st = allow_smem(kern, smem);
     if (st != cudaSuccess) return st;
     return launch_maybe_overlapped(kern, plan.chunks, 32 * kRowWarps, smem, s, true, a, plan);
@@ -484,13 +500,14 @@ cudaError_t launch_route_grad(const RouteGradLaunch& a, cudaStream_t s) {
   int warps = 1;
   while (warps < kRowWarps && a.n > sms * warps) warps *= 2;
   const bool vec = rows_by_four(a.r, a.logits, a.ld) && rows_by_four(a.r, a.d_logits, a.d_ld);
-  return with_row(a.r, vec, [&](auto row) {
+  return with_rows_of(a.r, a.n, vec, [&](auto row) {
+    using Row = decltype(row);
     // one round of the CTAs that the SMs hold
-    const int64_t most = sms * kGradResident<decltype(row)> * kRowWarps, run = (a.n + most - 1) / most;
-    const int64_t ctas = (a.n + run * warps - 1) / (run * warps);
-    const size_t smem = static_cast<size_t>(warps) * (sizeof(float) * 32 * decltype(row)::width +
-                                                      RowRing<decltype(row)>::warp_bytes(a.r.num_experts));
-    auto kern = route_grad_kernel<decltype(row)>;
+    const int64_t subs = warps * 32 / Row::lanes, most = sms * kGradResident<Row> * kRowsAtOnce<Row>;
+    const int64_t run = (a.n + most - 1) / most, ctas = (a.n + run * subs - 1) / (run * subs);
+    const size_t smem = static_cast<size_t>(subs) * (sizeof(float) * Row::lanes * Row::width +
+                                                     RowRing<Row>::warp_bytes(a.r.num_experts));
+    auto kern = route_grad_kernel<Row>;
     const cudaError_t st = allow_smem(kern, smem);
     if (st != cudaSuccess) return st;
     return launch_maybe_overlapped(kern, static_cast<int>(ctas), 32 * warps, smem, s, true, a, run);

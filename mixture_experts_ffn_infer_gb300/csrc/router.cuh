@@ -14,23 +14,23 @@ constexpr float kNaN = __builtin_nanf("");
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// A row of E values over a warp, V to a lane.  VEC: four neighbours to a lane, read
-// and written together (E and the row stride multiples of 4, rows aligned to four
-// values); else every 32nd.
-template <typename T, int V, bool VEC>
+// A row of E values over LANES lanes of a warp, V to a lane.  VEC: four neighbours to a lane,
+// read and written together (E and the row stride multiples of 4, rows aligned to four
+// values); else every LANES-th.
+template <typename T, int V, bool VEC, int LANES = 32>
 struct WarpRow {
   using type = T;
-  static constexpr int width = V;
+  static constexpr int width = V, lanes = LANES;
   static constexpr bool vec = VEC;
   static __device__ __forceinline__ int expert(int i, int lane) {
-    return VEC ? 128 * (i >> 2) + 4 * lane + (i & 3) : 32 * i + lane;
+    return VEC ? 4 * LANES * (i >> 2) + 4 * lane + (i & 3) : LANES * i + lane;
   }
   // Values past the row are `fill`.
   static __device__ __forceinline__ void load(const T* p, int E, int lane, float fill, float (&v)[V]) {
     if constexpr (VEC) {
 #pragma unroll
       for (int j = 0; j < V / 4; ++j) {
-        const int e = 128 * j + 4 * lane;
+        const int e = 4 * LANES * j + 4 * lane;
         if (e < E) {
           if constexpr (sizeof(T) == 4) {
             const float4 q = *reinterpret_cast<const float4*>(p + e);
@@ -46,14 +46,14 @@ struct WarpRow {
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = 32 * i + lane < E ? to_float(p[32 * i + lane]) : fill;
+      for (int i = 0; i < V; ++i) v[i] = LANES * i + lane < E ? to_float(p[LANES * i + lane]) : fill;
     }
   }
   static __device__ __forceinline__ void store(T* p, int E, int lane, const float (&v)[V]) {
     if constexpr (VEC) {
 #pragma unroll
       for (int j = 0; j < V / 4; ++j) {
-        const int e = 128 * j + 4 * lane;
+        const int e = 4 * LANES * j + 4 * lane;
         if (e >= E) continue;
         if constexpr (sizeof(T) == 4) {
           *reinterpret_cast<float4*>(p + e) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
@@ -67,9 +67,9 @@ struct WarpRow {
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (32 * i + lane < E) {
-          if constexpr (sizeof(T) == 4) p[32 * i + lane] = v[i];
-          else p[32 * i + lane] = __float2bfloat16_rn(v[i]);
+        if (LANES * i + lane < E) {
+          if constexpr (sizeof(T) == 4) p[LANES * i + lane] = v[i];
+          else p[LANES * i + lane] = __float2bfloat16_rn(v[i]);
         }
     }
   }
@@ -98,9 +98,9 @@ struct RowRing {
         const uint32_t to = base + (i & kAhead) * bytes + kPiece * lane;
 #pragma unroll
         for (int j = 0; j < Row::width / 4; ++j)
-          if (128 * j + 4 * lane < E)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + 32 * kPiece * j),
-                         "l"(p + 128 * j + 4 * lane), "n"(kPiece)
+          if (4 * Row::lanes * j + 4 * lane < E)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + Row::lanes * kPiece * j),
+                         "l"(p + 4 * Row::lanes * j + 4 * lane), "n"(kPiece)
                          : "memory");
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -117,15 +117,15 @@ struct RowRing {
       const uint32_t at = base + (i & kAhead) * bytes + kPiece * lane;
 #pragma unroll
       for (int j = 0; j < Row::width / 4; ++j) {
-        const bool on = 128 * j + 4 * lane < E;
+        const bool on = 4 * Row::lanes * j + 4 * lane < E;
         if constexpr (sizeof(T) == 4) {
           uint4 q = make_uint4(0u, 0u, 0u, 0u);
-          if (on) q = lds128(at + 32 * kPiece * j);
+          if (on) q = lds128(at + Row::lanes * kPiece * j);
           v[4 * j] = __uint_as_float(q.x), v[4 * j + 1] = __uint_as_float(q.y), v[4 * j + 2] = __uint_as_float(q.z),
                 v[4 * j + 3] = __uint_as_float(q.w);
         } else {
           uint32_t x = 0, y = 0;
-          if (on) asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "r"(at + 32 * kPiece * j));
+          if (on) asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "r"(at + Row::lanes * kPiece * j));
           v[4 * j] = __uint_as_float(x << 16), v[4 * j + 1] = __uint_as_float(x & 0xffff0000u);
           v[4 * j + 2] = __uint_as_float(y << 16), v[4 * j + 3] = __uint_as_float(y & 0xffff0000u);
         }
@@ -167,6 +167,25 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
+}
+
+// The same over each LANES lanes; mask: the caller's.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v, uint32_t mask) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(mask, v, o);
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_max_nan(float v, uint32_t mask) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(mask, v, o));
+  return v;
+}
+// The lanes that share this thread's row.
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_mask() {
+  return LANES == 32 ? 0xffffffffu : ((1u << (LANES & 31)) - 1u) << (threadIdx.x & 31 & ~(LANES - 1));
 }
 
 // Two values at a time (each rounded as one alone would be): an issue slot for both.
@@ -346,6 +365,20 @@ cudaError_t with_row(const moe_router& r, bool vec, F f) {
     if (E <= 256) return f(WarpRow<T, 8, false>{});
     if (E <= 512) return f(WarpRow<T, 16, false>{});
     return f(WarpRow<T, 32, false>{});
+  };
+  return r.logits_type == MOE_LOGITS_F32 ? by_width(float{}) : by_width(__nv_bfloat16{});
+}
+// The same with two or four short rows to a warp, whose lanes hold the chosen experts too; else as above.
+template <typename F>
+cudaError_t with_short_row(const moe_router& r, bool vec, F f) {
+  auto by_width = [&](auto type) -> cudaError_t {
+    using T = decltype(type);
+    const int E = r.num_experts, k = r.top_k;
+    if (vec && E <= 32 && k <= 8) return f(WarpRow<T, 4, true, 8>{});
+    if (vec && E <= 64 && k <= 16) return f(WarpRow<T, 4, true, 16>{});
+    if (!vec && E <= 16 && k <= 8) return f(WarpRow<T, 2, false, 8>{});
+    if (!vec && E <= 64 && k <= 16) return f(WarpRow<T, 4, false, 16>{});
+    return with_row(r, vec, f);
   };
   return r.logits_type == MOE_LOGITS_F32 ? by_width(float{}) : by_width(__nv_bfloat16{});
 }

@@ -223,12 +223,12 @@ def ids_of(seed, n, k, E):
 
 def loss_error(logits, live_rows):
     """Relative: a share (a sigmoid's e^-l is within |l| 2^-24, below the 2 spread + 5 units that score_error has for more:
-    these logits have both signs), and sums of positive values: a CTA's run of max(8, n / 608) rows by eight warps, eight warps,
-    up to 609 pieces by eight warps, 32 experts, E / 32 parts and the sequences by 256 threads (24 for up to 6000 of them and
+    these logits have both signs), and sums of positive values: a CTA's run of max(8, n / 608) rows, 8 to 32 at a time, as many
+    sums to join, up to 609 pieces by eight warps, 32 experts, E / 32 parts and the sequences by 256 threads (24 for up to 6000 of them and
     13 to join), besides a handful of products."""
     n, E = logits.shape
     run = max(8, n / 608)
-    return (2 * plain.score_error(logits) + run / 8 + 8 + 77 + 8 + 5 + E / 32 + 24 + 13 + 10) * EPS
+    return (2 * plain.score_error(logits) + run / 8 + 32 + 77 + 8 + 5 + E / 32 + 24 + 13 + 10) * EPS
 
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
@@ -238,7 +238,8 @@ def loss_error(logits, live_rows):
                                          (130, 1024, 32, 2, 0), (2000, 8, 2, 6000, 300),
                                          (20001, 64, 6, 7, 13), (12000, 384, 8, 3001, 0), (10001, 256, 16, 1, 0),
                                          (9999, 500, 3, 9000, 77), (70001, 8, 1, 50, 1), (10000, 130, 9, 11, 0),
-                                         (9800, 64, 17, 5, 0)])
+                                         (9800, 64, 17, 5, 0), (6000, 9, 5, 3, 0), (7001, 50, 12, 400, 6), (5500, 24, 12, 50, 0),
+                                         (5001, 32, 8, 5001, 0), (6000, 1, 1, 2, 5)])
 def test_loss_and_counts(kind, dtype, n, E, k, S, pad):
     logits, ids = logits_of(n + E, n, E, dtype), ids_of(n, n, k, E)
     offsets = None if S == 1 and pad == 0 else ragged(S, n - pad, S)
@@ -323,7 +324,10 @@ def check_gradient(logits, ids, kind, offsets=None, coef=None, d_loss=None, out=
 
 
 CASES = [(1, 1, 1, 1, 0), (1, 384, 8, 1, 0), (64, 16, 4, 1, 0), (65, 33, 2, 3, 1), (1001, 60, 3, 5, 37),
-         (300, 384, 8, 300, 0), (3000, 130, 6, 40, 5), (130, 1024, 32, 2, 0), (500, 8, 2, 2000, 100)]
+         (300, 384, 8, 300, 0), (3000, 130, 6, 40, 5), (130, 1024, 32, 2, 0), (500, 8, 2, 2000, 100),
+         # several rows to a warp
+         (6001, 8, 2, 7, 9), (5003, 9, 5, 3000, 0), (7001, 50, 12, 400, 6), (5500, 24, 12, 1, 0), (5001, 64, 16, 3, 100),
+         (5001, 32, 8, 5001, 0), (9000, 48, 13, 31, 0)]
 
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
