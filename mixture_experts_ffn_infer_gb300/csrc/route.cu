@@ -9,8 +9,9 @@
 //  2. the values from there up (less a margin for the short scores), some k + 3, one to
 //     a lane, and their scores again, within 2^-21 of each;
 //  3. the rank of each among them, by comparing with all: no step waits for the last.
-// Step 2 finds more than 32 only where many values are equal; such rows take the slow
-// way, k maxima over all values in 64 bits.
+// Step 2 finds more than 32 only where many values are equal or a few lanes hold most of the
+// large ones; for the latter a sort of all lanes bounds them closer, the others take the
+// slow way, k maxima over all values in 64 bits.
 //
 // The choice is that of the exact scores.  With a bias (or groups) fp32 scores order two
 // experts wrongly where they are closer than the scores' errors: neighbours among the
@@ -183,7 +184,7 @@ __device__ __noinline__ int exact_rank(const typename Row::type* p, int E, bool 
 }
 
 // The j-th largest (from 1) of the lanes' values.  K. Batcher's bitonic sort (1968): 15 exchanges; up to the 16th, of the
-// larger values of pairs of lanes, 10 (a value no larger, with one or two more from it up among all).  dirs: bit i of a
+// larger values of pairs of lanes, 10 (a value no larger, with one or two more from it up among all; not with `all`).  dirs: bit i of a
 // lane is whether it keeps the larger one in exchange i.  (Nine maxima of the warp one after the other took 130
 // instructions.)
 __device__ __forceinline__ uint32_t sort_directions(int lane) {
@@ -198,12 +199,12 @@ __device__ __forceinline__ uint32_t sort_directions(int lane) {
   for (int o = 8; o > 0; o /= 2, ++i) dirs |= (lane & o) == 0 ? 1u << i : 0u;
   return dirs;
 }
-__device__ __forceinline__ float warp_nth(float v, int j, uint32_t dirs) {
+__device__ __forceinline__ float warp_nth(float v, int j, uint32_t dirs, bool all) {
   auto exchange = [&](int o, int i) {
     const float w = __shfl_xor_sync(kAll, v, o);
     v = dirs >> i & 1u ? fmaxf(v, w) : fminf(v, w);
   };
-  if (j <= 16) {
+  if (j <= 16 && !all) {
     v = fmaxf(v, __shfl_xor_sync(kAll, v, 16));
     exchange(1, 0);
     exchange(2, 1), exchange(1, 2);
@@ -219,12 +220,60 @@ __device__ __forceinline__ float warp_nth(float v, int j, uint32_t dirs) {
   return __shfl_sync(kAll, v, j - 1);
 }
 
-// The kept groups' bits.  x: the warp's choices (-inf: not to be chosen), by way of `row` in shared memory; unsure: the
-// last kept and the first other group are too close.
+// The exact value of group g: the sum of its two largest choices.  Of its experts (their choices in fp32 in `row`) those from
+// `low` up are looked at, by a lane each.
+template <typename T>
+__device__ __forceinline__ double exact_group(const float* row, int g, int size, float low, bool sigmoid, float shift, double total,
+                                              const float* bias, const T* p) {
+  Best one{0.0, -1}, two{0.0, -1};
+  for (int e = g * size + (threadIdx.x & 31); e < (g + 1) * size; e += 32) {
+    if (!(row[e] >= low && row[e] > -kInf)) continue;
+    const float l = to_float(p[e]);
+    const double x = (sigmoid ? exact_sigmoid(l) : exact_softmax(l, shift, total)) + (bias ? static_cast<double>(bias[e]) : 0.0);
+    if (one.e < 0 || x > one.x) two = one, one = Best{x, e};
+    else if (two.e < 0 || x > two.x) two = Best{x, e};
+  }
+  const Best first = warp_best(one);
+  const Best second = warp_best(one.e == first.e ? two : one);
+  return first.x + (second.e >= 0 ? second.x : 0.0);
+}
+// Which of the groups in `near` (their bits) are the `slots` best, exactly: of equal ones those of lowest index.  second: on lane
+// g * share, group g's second largest choice in fp32 (its only one's where it has one).
+template <typename T>
+__device__ __noinline__ uint32_t exact_groups(uint32_t near, int slots, const float* row, int size, int share, float second,
+                                              float wide, bool sigmoid, float shift, int E, const float* bias, const T* p) {
+  const int lane = threadIdx.x & 31;
+  double total = 0.0;
+  if (!sigmoid) {
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) total += exp(static_cast<double>(to_float(p[e])) - static_cast<double>(shift));
+    total = warp_sum(total);
+  }
+  Best mine{0.0, -1};  // lane g: group g's
+#pragma unroll 1
+  for (uint32_t left = near; left != 0; left &= left - 1) {
+    const int g = __ffs(left) - 1;
+    const double v = exact_group(row, g, size, __shfl_sync(kAll, second, g * share) - wide, sigmoid, shift, total, bias, p);
+    if (lane == g) mine = Best{v, g};
+  }
+  uint32_t kept = 0;
+#pragma unroll 1
+  for (int j = 0; j < slots; ++j) {
+    const Best b = warp_best(mine);
+    if (b.e < 0) break;
+    kept |= 1u << b.e;
+    if (b.e == lane) mine.e = -1;
+  }
+  return kept;
+}
+
+// The kept groups' bits.  x: the warp's choices (-inf: not to be chosen), by way of `row` in shared memory.  Groups whose values
+// are too close to the last kept one's and the first other's for fp32 are told apart in 64 bits.
 template <typename Row>
 __device__ __forceinline__ uint32_t kept_groups(const moe_router& r, const float (&x)[Row::width], float* row, float most,
-                                                bool& unsure) {
+                                                float shift, const float* bias, const typename Row::type* p) {
   const int E = r.num_experts, lane = threadIdx.x & 31;
+  const bool sigmoid = r.score == MOE_SCORE_SIGMOID;
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < Row::width; ++i) {
@@ -248,7 +297,9 @@ __device__ __forceinline__ uint32_t kept_groups(const moe_router& r, const float
   }
   // one value a group, on its first lane
   const bool mine = lane % share == 0 && one > -kInf;
-  uint32_t key = mine ? key_of(one + (two > -kInf ? two : 0.f)) : 0u, kept = 0, last = 0;
+  const float value = one + (two > -kInf ? two : 0.f);
+  const uint32_t own = mine ? key_of(value) : 0u;
+  uint32_t key = own, kept = 0, last = 0;
   for (int j = 0; j < r.top_groups; ++j) {
     const uint32_t best = __reduce_max_sync(kAll, key);
     if (best == 0) break;
@@ -259,14 +310,23 @@ __device__ __forceinline__ uint32_t kept_groups(const moe_router& r, const float
   }
   const uint32_t next = __reduce_max_sync(kAll, key);
   if (next != 0) {
-    const float a = value_of(last), b = value_of(next);
-    unsure = !(a - b > tolerance(r.score == MOE_SCORE_SIGMOID, 4.f * most, fabsf(a) + fabsf(b)));  // of four scores
+    // (twice as far as two sums of two scores may be off)
+    const float a = value_of(last), b = value_of(next), wide = tolerance(sigmoid, 4.f * most, fabsf(a) + fabsf(b));
+    if (!(a - b > wide)) {
+      const bool in = kept >> (lane / share) & 1u;
+      const bool close = mine && (in ? !(value - b > wide) : !(a - value > wide));
+      uint32_t near = 0;  // by group
+      for (uint32_t left = __ballot_sync(kAll, close); left != 0; left &= left - 1) near |= 1u << ((__ffs(left) - 1) / share);
+      const int slots = __popc(near & kept);
+      kept = (kept & ~near) | exact_groups(near, slots, row, size, share, two > -kInf ? two : one, wide, sigmoid, shift, E, bias,
+                                           p);
+    }
   }
   return kept;
 }
 
-// Row t by a warp.  bias: of this lane's experts, -inf of one that is not to be chosen, whatever its score.
-template <typename Row>
+// Row t by a warp (GROUPS: more than one).  bias: of this lane's experts, -inf of one that is not to be chosen, whatever its score.
+template <typename Row, bool GROUPS>
 __device__ __forceinline__ void route_row(const RouteLaunch& a, int group_inv, int64_t t, const float (&bias)[Row::width],
                                           uint32_t dirs, int* list, float* group_row) {
   using T = typename Row::type;
@@ -276,7 +336,7 @@ __device__ __forceinline__ void route_row(const RouteLaunch& a, int group_inv, i
   const int E = r.num_experts, k = r.top_k;
   const bool sigmoid = r.score == MOE_SCORE_SIGMOID;
   const bool by_logit = a.bias == nullptr;  // the choice within the groups is the logits' order
-  const bool by_score = !by_logit || r.groups > 1;
+  const bool by_score = !by_logit || GROUPS;
   const int deep = by_logit ? k : k + 1;    // of the logits' order nothing is unsure
   const T* p = static_cast<const T*>(a.logits) + t * a.ld;
   int32_t* ids = a.ids + t * k;
@@ -313,7 +373,7 @@ __device__ __forceinline__ void route_row(const RouteLaunch& a, int group_inv, i
     for (int i = 0; i < V; i += 2) {
       const float2 l = make_float2(x[i], x[i + 1]);
       float2 s;
-      if (r.groups > 1) {
+      if (GROUPS) {
         s = sigmoid_of(l);
       } else {
         const float2 h = mul2(l, both(-1.44269504f));
@@ -338,8 +398,8 @@ __device__ __forceinline__ void route_row(const RouteLaunch& a, int group_inv, i
     if (lane < k) ids[lane] = -1, weight[lane] = kNaN;
     return;
   }
-  if (r.groups > 1) {
-    const uint32_t kept = kept_groups<Row>(r, x, group_row, most, slow);
+  if constexpr (GROUPS) {
+    const uint32_t kept = kept_groups<Row>(r, x, group_row, most, soft.shift, a.bias, p);
     if (by_logit) Row::load(p, E, lane, -kInf, x);
     local = -kInf;
 #pragma unroll
@@ -349,21 +409,28 @@ __device__ __forceinline__ void route_row(const RouteLaunch& a, int group_inv, i
       local = fmaxf(local, x[i]);
     }
   }
-  // the k + 1st largest of the lanes' largest, less the margin of the short scores (twice their error)
-  float low = deep <= 32 ? warp_nth(local, deep, dirs) : -kInf;
-  if (!by_logit) low -= fmaf(0x1p-21f, fabsf(low), fmaxf(0x1p-18f, tolerance(sigmoid, most, 0.f)));
-  if (!(low > -kInf)) low = -3.4028234663852886e38f;  // all that can be chosen
-  uint32_t mask = 0;
-#pragma unroll
-  for (int i = 0; i < V; ++i) mask |= x[i] >= low ? 1u << i : 0u;
+  // the k + 1st largest of the lanes' largest, less the margin of the short scores (twice their error); that of all lanes where
+  // the shorter sort's leaves too many from there up
   int found = 0;
-  for (uint32_t who; (who = __ballot_sync(kAll, mask != 0)) != 0;) {
-    if (mask != 0) {
-      const int at = found + __popc(who & ((1u << lane) - 1u));
-      if (at < 32) list[at] = Row::expert(__ffs(mask) - 1, lane);
-      mask &= mask - 1;
+#pragma unroll 1
+  for (bool all = false;; all = true) {
+    float low = deep <= 32 ? warp_nth(local, deep, dirs, all) : -kInf;
+    if (!by_logit) low -= fmaf(0x1p-21f, fabsf(low), fmaxf(0x1p-18f, tolerance(sigmoid, most, 0.f)));
+    if (!(low > -kInf)) low = -3.4028234663852886e38f;  // all that can be chosen
+    uint32_t mask = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) mask |= x[i] >= low ? 1u << i : 0u;
+    found = 0;
+    for (uint32_t who; (who = __ballot_sync(kAll, mask != 0)) != 0;) {
+      if (mask != 0) {
+        const int at = found + __popc(who & ((1u << lane) - 1u));
+        if (at < 32) list[at] = Row::expert(__ffs(mask) - 1, lane);
+        mask &= mask - 1;
+      }
+      found += __popc(who);
     }
-    found += __popc(who);
+    if (found <= 32 || all || deep > 16) break;
+    __syncwarp();
   }
   __syncwarp();
   if (found > 32) slow = true;
@@ -434,7 +501,7 @@ __device__ __forceinline__ void bias_of(const RouteLaunch& a, int lane, float (&
 template <typename Row>
 constexpr int kResident = Row::width <= 16 ? 4 : 2;
 
-template <typename Row>
+template <typename Row, bool GROUPS>
 __global__ void __launch_bounds__(32 * kWarps, kResident<Row>)
 route_kernel(const RouteLaunch a, const int group_inv) {
   __shared__ int list[kWarps][32];
@@ -447,7 +514,7 @@ route_kernel(const RouteLaunch a, const int group_inv) {
   const uint32_t dirs = sort_directions(lane);
   const int64_t rows = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp; t < a.n; t += rows)
-    route_row<Row>(a, group_inv, t, bias, dirs, list[warp], group_row + warp * a.r.num_experts);
+    route_row<Row, GROUPS>(a, group_inv, t, bias, dirs, list[warp], group_row + warp * a.r.num_experts);
 }
 
 // ---------------------------------------------------------------- two rows a warp
@@ -543,7 +610,7 @@ __device__ __noinline__ void route_whole(const RouteLaunch& a, int64_t t, int* l
   const int lane = threadIdx.x & 31;
   float bias[Row::width];
   bias_of<Row>(a, lane, bias);
-  route_row<Row>(a, 0, t, bias, sort_directions(lane), list, nullptr);
+  route_row<Row, false>(a, 0, t, bias, sort_directions(lane), list, nullptr);
 }
 
 template <typename Row>
@@ -767,8 +834,8 @@ cudaError_t launch_route(const RouteLaunch& a, cudaStream_t s) {
   const size_t smem = a.r.groups > 1 ? static_cast<size_t>(warps) * a.r.num_experts * sizeof(float) : 0;
   return with_row(a.r, rows_by_four(a.r, a.logits, a.ld), [&](auto row) {
     const int64_t most = sms * kResident<decltype(row)> * kWarps / warps;
-    return launch_maybe_overlapped(route_kernel<decltype(row)>, static_cast<int>(ctas < most ? ctas : most), 32 * warps, smem,
-                                   s, true, a, inv);
+    auto kern = a.r.groups > 1 ? route_kernel<decltype(row), true> : route_kernel<decltype(row), false>;
+    return launch_maybe_overlapped(kern, static_cast<int>(ctas < most ? ctas : most), 32 * warps, smem, s, true, a, inv);
   });
 }
 

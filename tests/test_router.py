@@ -181,6 +181,38 @@ def test_close_scores_among_many_rows(kind):
 
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top,k,with_bias", [(64, 8, 3, 6, True), (64, 8, 3, 6, False), (40, 5, 2, 4, True), (32, 32, 5, 4, True)])
+def test_groups_closer_than_fp32_tells_apart(kind, E, groups, top, k, with_bias):
+    # groups of the same logits, moved by less than fp32 scores tell apart, by nothing, or masked
+    size = E // groups
+    x = logits_of(E, 1, size, std=1.0).repeat(1, groups).repeat(30, 1)
+    x[10:] *= 1 + torch.randint(-2, 3, (20, E), generator=gen(1)) * 2.0**-23
+    x[5, :size], x[6, size:2 * size], x[7, ::2] = -INF, -INF, -INF
+    x[8, 0], x[9, E - 1] = 9.0, 9.0
+    x[25:] = logits_of(2, 5, E)
+    b = None
+    if with_bias:
+        b = (torch.randn(size, generator=gen(2)) * 0.1).repeat(groups)
+        b[1] += 2.0**-20
+    check_choice(x, k, kind, b, groups, top)
+    if with_bias:
+        b[3], b[E // 2] = INF, -INF
+        check_choice(x, k, kind, b, groups, top)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_rows_of_more_candidates_than_lanes(kind):
+    # the largest values all in a few lanes' columns, so that what the shorter sort bounds are more than 32
+    n, E, k = 30, 512, 12
+    x = logits_of(3, n, E, std=0.5)
+    for t in range(n):
+        x[t, torch.arange(E) % 128 // 4 % 16 < 3 + t % 9] += 4
+    check_choice(x, k, kind)
+    check_choice(x, k, kind, torch.randn(E, generator=gen(1)) * 0.01)
+    check_choice(x.to(torch.bfloat16), k, kind)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("infinite", [1, 5, 8, 9, 40])
 def test_infinite_biases_among_many_rows(kind, infinite):
     n, E, k = 6000, 384, 8
