@@ -220,14 +220,14 @@ __device__ __forceinline__ float warp_nth(float v, int j, uint32_t dirs, bool al
   return __shfl_sync(kAll, v, j - 1);
 }
 
-// The exact value of group g: the sum of its two largest choices.  Of its experts (their choices in fp32 in `row`) those from
-// `low` up are looked at, by a lane each.
+// The exact value of group g: the sum of its two largest choices.  Of its experts (their choices in fp32 in `row`, -inf: not to
+// be chosen) those from `low` (finite) up are looked at, by a lane each.
 template <typename T>
 __device__ __forceinline__ double exact_group(const float* row, int g, int size, float low, bool sigmoid, float shift, double total,
                                               const float* bias, const T* p) {
   Best one{0.0, -1}, two{0.0, -1};
   for (int e = g * size + (threadIdx.x & 31); e < (g + 1) * size; e += 32) {
-    if (!(row[e] >= low && row[e] > -kInf)) continue;
+    if (!(row[e] >= low)) continue;
     const float l = to_float(p[e]);
     const double x = (sigmoid ? exact_sigmoid(l) : exact_softmax(l, shift, total)) + (bias ? static_cast<double>(bias[e]) : 0.0);
     if (one.e < 0 || x > one.x) two = one, one = Best{x, e};
@@ -253,7 +253,9 @@ __device__ __noinline__ uint32_t exact_groups(uint32_t near, int slots, const fl
 #pragma unroll 1
   for (uint32_t left = near; left != 0; left &= left - 1) {
     const int g = __ffs(left) - 1;
-    const double v = exact_group(row, g, size, __shfl_sync(kAll, second, g * share) - wide, sigmoid, shift, total, bias, p);
+    // (every expert that can be chosen where the bound is none: below the range, or inf - inf of infinite choices)
+    const float low = fmaxf(__shfl_sync(kAll, second, g * share) - wide, -3.4028234663852886e38f);
+    const double v = exact_group(row, g, size, low, sigmoid, shift, total, bias, p);
     if (lane == g) mine = Best{v, g};
   }
   uint32_t kept = 0;

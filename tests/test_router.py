@@ -227,6 +227,24 @@ def test_infinite_biases_among_many_rows(kind, infinite):
     check_many(x, k, kind, b, False)
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top,k,infinite", [
+    (32, 32, 1, 1, [5]), (32, 32, 3, 2, [9, 4, 31, 17, 2]),                   # groups of one expert
+    (64, 8, 1, 4, [8, 13]), (64, 8, 2, 6, [8, 13]), (64, 8, 2, 6, [40, 41, 42, 9, 10]),
+    (64, 8, 4, 8, [8, 9, 26, 31, 40, 45, 56, 63]),                            # two in each of as many as are kept
+    (64, 8, 2, 8, [8, 9, 26, 31, 40, 45, 56, 63]), (64, 8, 3, 20, [1, 2, 12, 30, 62, 63]),
+    (256, 8, 1, 8, [255, 254]), (60, 2, 1, 7, [59, 31])])
+def test_groups_of_infinite_biases(kind, E, groups, top, k, infinite):
+    x = logits_of(E + top, 20, E)
+    x[3, infinite[0]] = -INF                      # masked, whatever the bias
+    x[4] = 0.25
+    b = torch.randn(E, generator=gen(2)) * 0.1
+    b[infinite] = INF
+    check_choice(x, k, kind, b, groups, top)
+    b[b == INF] = 3e38                            # in range each, and not their sum
+    check_choice(x, k, kind, b, groups, top)
+
+
 def test_the_callers_tensors_and_nothing_around_them():
     n, E, k = 70, 48, 5
     x = logits_of(1, n, E).cuda()
