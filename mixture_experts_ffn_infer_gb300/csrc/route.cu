@@ -36,9 +36,6 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);  // (-0 is +0)
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ float value_of(uint32_t key) {
-  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
-}
 
 // Scores in 64 bits.
 __device__ __forceinline__ double exact_sigmoid(float l) { return 1.0 / (1.0 + exp(-static_cast<double>(l))); }
@@ -237,11 +234,11 @@ __device__ __forceinline__ double exact_group(const float* row, int g, int size,
   const Best second = warp_best(one.e == first.e ? two : one);
   return first.x + (second.e >= 0 ? second.x : 0.0);
 }
-// Which of the groups in `near` (their bits) are the `slots` best, exactly: of equal ones those of lowest index.  second: on lane
-// g * share, group g's second largest choice in fp32 (its only one's where it has one).
+// Which of the groups in `near` (their bits) are the `slots` best, exactly: of equal ones those of lowest index.  low: on lane
+// g * share, from where in fp32 group g's experts can be among its two largest.
 template <typename T>
-__device__ __noinline__ uint32_t exact_groups(uint32_t near, int slots, const float* row, int size, int share, float second,
-                                              float wide, bool sigmoid, float shift, int E, const float* bias, const T* p) {
+__device__ __noinline__ uint32_t exact_groups(uint32_t near, int slots, const float* row, int size, int share, float low,
+                                              bool sigmoid, float shift, int E, const float* bias, const T* p) {
   const int lane = threadIdx.x & 31;
   double total = 0.0;
   if (!sigmoid) {
@@ -253,9 +250,7 @@ __device__ __noinline__ uint32_t exact_groups(uint32_t near, int slots, const fl
 #pragma unroll 1
   for (uint32_t left = near; left != 0; left &= left - 1) {
     const int g = __ffs(left) - 1;
-    // (every expert that can be chosen where the bound is none: below the range, or inf - inf of infinite choices)
-    const float low = fmaxf(__shfl_sync(kAll, second, g * share) - wide, -3.4028234663852886e38f);
-    const double v = exact_group(row, g, size, low, sigmoid, shift, total, bias, p);
+    const double v = exact_group(row, g, size, __shfl_sync(kAll, low, g * share), sigmoid, shift, total, bias, p);
     if (lane == g) mine = Best{v, g};
   }
   uint32_t kept = 0;
@@ -269,8 +264,9 @@ __device__ __noinline__ uint32_t exact_groups(uint32_t near, int slots, const fl
   return kept;
 }
 
-// The kept groups' bits.  x: the warp's choices (-inf: not to be chosen), by way of `row` in shared memory.  Groups whose values
-// are too close to the last kept one's and the first other's for fp32 are told apart in 64 bits.
+// The kept groups' bits.  x: the warp's choices (-inf: not to be chosen), by way of `row` in shared memory.  A group's value is off
+// by its two choices' errors, each relative to the choice (the sum may be small beside them), and its own rounding.  Kept groups
+// that another one may reach, within the errors of both, and those others are told apart in 64 bits.
 template <typename Row>
 __device__ __forceinline__ uint32_t kept_groups(const moe_router& r, const float (&x)[Row::width], float* row, float most,
                                                 float shift, const float* bias, const typename Row::type* p) {
@@ -299,30 +295,31 @@ __device__ __forceinline__ uint32_t kept_groups(const moe_router& r, const float
   }
   // one value a group, on its first lane
   const bool mine = lane % share == 0 && one > -kInf;
-  const float value = one + (two > -kInf ? two : 0.f);
-  const uint32_t own = mine ? key_of(value) : 0u;
-  uint32_t key = own, kept = 0, last = 0;
+  const float less = two > -kInf ? two : 0.f, value = one + less;
+  uint32_t key = mine ? key_of(value) : 0u, kept = 0;
   for (int j = 0; j < r.top_groups; ++j) {
     const uint32_t best = __reduce_max_sync(kAll, key);
     if (best == 0) break;
     const int at = __ffs(__ballot_sync(kAll, key == best)) - 1;
     kept |= 1u << (at / share);
-    last = best;
     if (lane == at) key = 0;
   }
-  const uint32_t next = __reduce_max_sync(kAll, key);
-  if (next != 0) {
-    // (twice as far as two sums of two scores may be off)
-    const float a = value_of(last), b = value_of(next), wide = tolerance(sigmoid, 4.f * most, fabsf(a) + fabsf(b));
-    if (!(a - b > wide)) {
-      const bool in = kept >> (lane / share) & 1u;
-      const bool close = mine && (in ? !(value - b > wide) : !(a - value > wide));
-      uint32_t near = 0;  // by group
-      for (uint32_t left = __ballot_sync(kAll, close); left != 0; left &= left - 1) near |= 1u << ((__ffs(left) - 1) / share);
-      const int slots = __popc(near & kept);
-      kept = (kept & ~near) | exact_groups(near, slots, row, size, share, two > -kInf ? two : one, wide, sigmoid, shift, E, bias,
-                                           p);
-    }
+  // The least and the most that the exact value may be (twice as far as it may be off).  An infinite choice's group has exactly
+  // that value; a sum past fp32's range may be anything.
+  const float wide = tolerance(sigmoid, 2.f * most, fabsf(one) + fabsf(less));
+  const bool in = kept >> (lane / share) & 1u, infinite = one == kInf;
+  const uint32_t least = key_of(infinite ? kInf : fmaxf(value - wide, -kInf)),
+                 greatest = key_of(infinite ? kInf : fminf(value + wide, kInf));
+  const uint32_t last = __reduce_min_sync(kAll, mine && in ? least : kAll),
+                 next = __reduce_max_sync(kAll, mine && !in ? greatest : 0u);
+  if (last <= next) {
+    const bool close = mine && (in ? least <= next : greatest >= last);
+    uint32_t near = 0;  // by group
+    for (uint32_t left = __ballot_sync(kAll, close); left != 0; left &= left - 1) near |= 1u << ((__ffs(left) - 1) / share);
+    const int slots = __popc(near & kept);
+    // (every expert that can be chosen where the bound is none: below the range, or inf - inf of infinite choices)
+    const float low = fmaxf((two > -kInf ? two : one) - wide, -3.4028234663852886e38f);
+    kept = (kept & ~near) | exact_groups(near, slots, row, size, share, low, sigmoid, shift, E, bias, p);
   }
   return kept;
 }

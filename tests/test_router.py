@@ -245,6 +245,26 @@ def test_groups_of_infinite_biases(kind, E, groups, top, k, infinite):
     check_choice(x, k, kind, b, groups, top)
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top,k", [(64, 8, 3, 5), (32, 4, 2, 3), (256, 8, 4, 8)])
+@pytest.mark.parametrize("large", [1000.0, 3e5])
+def test_groups_whose_sums_are_small_beside_their_choices(kind, E, groups, top, k, large):
+    # a group's two largest choices are near +large and -large: each rounds by large 2^-24, and their sum is small
+    size, n = E // groups, 300
+    for noise in (1e-4, 1e-3):
+        x = (logits_of(E, 1, size).repeat(1, groups) * (1 + noise * torch.randn(n, E, generator=gen(1)))).float()
+        x[n - 1] = x[n - 1, :size].repeat(groups)                             # equal groups
+        sums = torch.full((groups, size), -INF)
+        sums[:, 1], sums[:, 4] = large, -large
+        check_choice(x, k, kind, sums.flatten(), groups, top)
+        sums[:, 2:] = -large                                                  # which one is second is unsure too
+        check_choice(x, k, kind, sums.flatten(), groups, top)
+        sums[::2] = 0.0                                                       # beside groups of ordinary choices
+        check_choice(x, k, kind, sums.flatten(), groups, top)
+        sums[1::2, 1] = INF
+        check_choice(x, k, kind, sums.flatten(), groups, top)
+
+
 def test_the_callers_tensors_and_nothing_around_them():
     n, E, k = 70, 48, 5
     x = logits_of(1, n, E).cuda()
