@@ -24,14 +24,15 @@
  *
  * Balance loss over sequences s of T_s rows each (rows seq_offsets[s] ..
  * seq_offsets[s + 1] - 1), with S the number of those that have rows:
- *   q[t]     = s[t] / sum_e s[t][e]   (softmax: s[t] itself; 0 for a masked row)
+ *   q[t]     = s[t] / sum_e s[t][e]   (softmax: s[t] itself; 0 where every logit is -inf).  Quotients of the exact
+ *              scores: a row whose sigmoids fp32 does not hold has shares all the same
  *   count_se = entries of ids in the sequence's rows that are e
  *   loss     = coef / S * sum_s E / (top_k T_s^2) * sum_e count_se * sum_t q[t][e]
  * which is coef where every expert gets the same.  Counts are constants to the
  * gradient.  Rows of no sequence (padding behind the last) add nothing.
  *
  * Logits are fp32 or bf16, arithmetic is fp32, weights, bias and their gradients
- * fp32.  All pointers except the struct are device pointers; every call is
+ * fp32; in weights and their gradients a score below 2^-126 is 0.  All pointers except the struct are device pointers; every call is
  * asynchronous on `stream`, allocates nothing, does not synchronise and can be
  * captured.  Results do not depend on the order in which the GPU runs the work.
  * n = 0 is MOE_OK.

@@ -492,6 +492,52 @@ def test_gradient_into_strided_rows_and_in_place(dtype, kind):
     got, _ = check_gradient(logits, ids, kind, d_weights=d_weights, coef=1.0, out=lambda x: x)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,E,k", [(60, 384, 8), (33, 61, 3), (6000, 8, 2), (5001, 50, 12), (5600, 256, 8)])
+@pytest.mark.parametrize("level", [-35.0, -44.0, -60.0, -87.0, -89.0, -95.0, -300.0, -600.0])
+def test_sigmoid_shares_of_low_rows(dtype, n, E, k, level):
+    # A share does not depend on whether fp32 holds the scores that it is of.
+    logits = (logits_of(n + E, n, E) * 2 + level).to(dtype)
+    logits[::3] = logits_of(n, len(logits[::3]), E, dtype)                  # beside ordinary rows
+    logits[4, 1:] = -INF
+    ids, offsets = ids_of(n, n, k, E), ragged(3, n, 4)
+    loss, counts = mx.balance_loss(logits.cuda(), ids.cuda(), 0.01, mx.MOE_SCORE_SIGMOID, seq_offsets=offsets.cuda())
+    want, want_counts = plain.balance(logits, ids, 0.01, "sigmoid", offsets)
+    assert torch.equal(counts.cpu(), want_counts)
+    # shares as loss_error has them, of rows of a spread below 20; e^-l of low rows is within |l| 2^-24, of those that go by the
+    # sigmoid up to 64 of these, in a score and in its row's sum
+    low = (2 * (12 + 2 * 20 + E / 32 + 5) + 2 * 64) * EPS
+    assert abs(loss.item() - want.item()) <= (loss_error(logits[::3], n) + low) * want.item()
+    # The gradient of the loss; and with that of weights whose scores are above 2^-126 (below, weights are 0).
+    finite = logits.clone()
+    finite[logits == -INF] = -690.0
+    for d_weights in (None, torch.randn(n, k, generator=gen(4))):
+        kw = dict(coef=5.0, offsets=offsets, d_weights=d_weights)
+        got = mx.route_backward(logits.cuda(), ids.cuda(), mx.MOE_SCORE_SIGMOID, counts=counts, coef=5.0, seq_offsets=offsets.cuda(),
+                                d_weights=None if d_weights is None else d_weights.cuda()).cpu().double()
+        grad, size = (f(finite, ids, "sigmoid", **kw) for f in (plain.gradient, plain.gradient_size))
+        tol = (6 * (12 + 2 * 20 + E / 32 + 5 + 64) + 2 * k + 30) * EPS
+        err = (got - grad).abs() - tol * size - torch.finfo(dtype).eps / 2 * (grad.abs() + tol * size)
+        none = 0.0 if d_weights is None else 1.2e-38 * 1e20 * d_weights.abs().sum(1, keepdim=True)
+        assert (err <= 1e-37 + none).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("level", [-1000.0, -1e4, None])
+def test_sigmoid_shares_of_rows_below_every_float(dtype, level):
+    # there the shares are a softmax's; the type's lowest value masks nothing
+    n, E, k = 90, 40, 4
+    logits = torch.full((n, E), torch.finfo(dtype).min, dtype=dtype) if level is None else (logits_of(1, n, E) + level).to(dtype)
+    ids = ids_of(2, n, k, E)
+    loss, counts = mx.balance_loss(logits.cuda(), ids.cuda(), 1.0, mx.MOE_SCORE_SIGMOID)
+    want, _ = plain.balance(logits, ids, 1.0, "softmax")
+    assert abs(loss.item() - want.item()) <= loss_error(logits, n) * want.item()
+    got = mx.route_backward(logits.cuda(), ids.cuda(), mx.MOE_SCORE_SIGMOID, counts=counts, coef=3.0).cpu().double()
+    grad, size = (f(logits, ids, "softmax", coef=3.0) for f in (plain.gradient, plain.gradient_size))
+    tol = (6 * plain.score_error(logits) + 2 * k + 30) * EPS
+    assert ((got - grad).abs() - tol * size - torch.finfo(dtype).eps / 2 * (grad.abs() + tol * size)).max() <= 1e-37
+
+
 # ---------------------------------------------------------------- as a program runs them
 
 def test_the_same_bits_each_time_and_in_a_graph():
