@@ -371,6 +371,45 @@ def test_no_rows():
     assert mx.route_backward(torch.zeros(0, E).cuda(), torch.zeros(0, k, dtype=torch.int32).cuda(), 0).shape == (0, E)
 
 
+def test_the_callers_workspace_again_and_again():
+    # one buffer, of the size that is asked for, for calls of all sizes one behind the other: nothing of the last is left
+    calls = []
+    for seed, (n, E, k, S, kind) in enumerate([(20000, 384, 8, 9, "sigmoid"), (3, 16, 2, 1, "softmax"), (6000, 8, 2, 3000, "sigmoid"),
+                                               (0, 64, 4, 5, "softmax"), (5001, 1000, 32, 2, "softmax"), (40, 33, 3, 60, "sigmoid"),
+                                               (20000, 384, 8, 9, "sigmoid"), (1, 1, 1, 1, "sigmoid")]):
+        offsets = None if S == 1 else ragged(seed, n, S).cuda()
+        r = mx.moe_router(E, k, mx.MOE_SCORES[kind], mx.MOE_LOGITS_F32, 1, 1, 1, 1.0)
+        calls.append((mx.moe_balance_workspace_size(r, n, S), (logits_of(seed, n, E).cuda(), ids_of(seed, n, k, E).cuda(), 0.5,
+                                                               mx.MOE_SCORES[kind]), offsets))
+    want = [mx.balance_loss(*args, seq_offsets=offsets) for _, args, offsets in calls]
+    room = torch.full((256 + max(b for b, _, _ in calls) + 512,), 0xff, dtype=torch.uint8, device="cuda")
+
+    def all_calls():
+        return [mx.balance_loss(*args, seq_offsets=offsets, ws=room[256:256 + b]) for b, args, offsets in calls]
+
+    def same(got):
+        return all(torch.equal(a, b) and torch.equal(c, d) for (a, c), (b, d) in zip(got, want))
+
+    assert same(all_calls()) and same(all_calls())
+    assert (room[:256] == 0xff).all() and (room[-512:] == 0xff).all()
+    for (b, args, offsets), (loss, counts) in zip(calls, want):
+        room.fill_(0xff)
+        got = mx.balance_loss(*args, seq_offsets=offsets, ws=room[256:256 + b])
+        assert torch.equal(got[0], loss) and torch.equal(got[1], counts)
+        assert (room[:256] == 0xff).all() and (room[256 + b:] == 0xff).all()
+    with pytest.raises(mx.MoeError):
+        mx.balance_loss(*calls[0][1], seq_offsets=calls[0][2], ws=room[256:256 + calls[0][0] - 1])
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = all_calls()
+    for _ in range(3):
+        room.fill_(0x7f)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(got)
+
+
 # ---------------------------------------------------------------- the gradient
 
 def check_gradient(logits, ids, kind, offsets=None, coef=None, d_loss=None, out=None, **kw):
