@@ -47,7 +47,8 @@ int64_t moe_fp8_scale_pitch(int64_t cols);
 moe_status moe_fp8_quantise(int64_t n, int32_t k, int32_t d, const void *x, int64_t x_ld, const int32_t *positions,
                             int64_t out_rows, void *codes, float *scales, cudaStream_t stream);
 
-/* bf16 values of `rows` rows (rounded once): out rows out_ld elements apart, a multiple of 8; 16-byte aligned. */
+/* bf16 values of `rows` rows: code * scale rounded to fp32, as a product reads it, and that to bf16.  out rows out_ld elements
+ * apart, a multiple of 8; 16-byte aligned. */
 moe_status moe_fp8_dequantise(int64_t rows, int32_t d, const void *codes, const float *scales, void *out,
                               int64_t out_ld, cudaStream_t stream);
 
@@ -81,8 +82,9 @@ size_t moe_fp8_packed_bytes(const moe_fp8_weights *w);
 
 /* Products grouped by expert: rows expert_offsets[e] .. expert_offsets[e + 1] - 1 of x belong to expert e.
  *   out[p(r)] = row_weight[p(r)] * sum_b x_scale[r][b] w_scale[e][n / 128][b] * sum_{c in block b} X[r][c] W_e[n][c]
- * with p(r) = out_pos[r]; the block's products are summed in fp32 on the tensor cores, the blocks in fp32, and the
- * result is rounded once.
+ * with p(r) = out_pos[r]; a block's products are summed in fp32 on the tensor cores, the two scales' product is fp32, the
+ * blocks are summed in fp32 (a block's sum times its scales added with one rounding), the row weight multiplies in fp32,
+ * and that is rounded to out_type.
  *   rows            rows of x, below 2^31; (rows / 128 + E) * ceil(n_out / 128) at most 2^31 - 4097
  *   expert_offsets  [E + 1] int32, ascending from >= 0 to <= rows; anything else computes nothing and raises
  *                   MOE_ERR_ROUTING.  Rows of no expert are left alone, empty experts cost nothing.  NULL, where

@@ -97,6 +97,22 @@ def test_rows_of_odd_values():
     assert torch.equal(back.nan_to_num(7.0), want.nan_to_num(7.0))
 
 
+def test_values_are_rounded_to_fp32_and_then_to_bf16():
+    # scales by which some codes' products have more bits than fp32 and round there to halfway between two bf16
+    codes = torch.arange(0x78, 0x7f, dtype=torch.uint8)                    # 256 to 448: four bits
+    scales = (2**23 + torch.randint(0, 2**23, (1 << 18,), generator=gen(1))).float() * 2.0**-30
+    v = codes.view(torch.float8_e4m3fn).double()[None] * scales.double()[:, None]
+    half = (v.float().view(torch.int32) & 0xffff == 0x8000) & (v.float().double() != v)
+    scales = scales[half.any(1)]
+    assert len(scales) > 4
+    r = mx.Fp8Rows(torch.zeros(len(scales), 16, dtype=torch.uint8), torch.zeros(len(scales), 4))
+    r.codes[:, :7], r.codes[:, 8:15] = codes, codes | 0x80
+    r.scales[:, 0] = scales
+    got = mx.fp8_dequantise(mx.Fp8Rows(r.codes.cuda(), r.scales.cuda())).cpu()
+    want = (r.codes.view(torch.float8_e4m3fn).float() * r.scales[:, :1]).to(torch.bfloat16)
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("n,k,d", [(1, 1, 256), (7, 3, 400), (350, 8, 128), (320, 9, 1040), (33, 20, 2048)])
 def test_positions(n, k, d):
     x = bf16(n, n, d)
