@@ -265,6 +265,20 @@ def test_groups_whose_sums_are_small_beside_their_choices(kind, E, groups, top, 
         check_choice(x, k, kind, sums.flatten(), groups, top)
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_scores_that_64_bits_do_not_tell_apart(kind):
+    # sigmoids that are 1, softmax scores that are 0: equal, so that the lowest index goes first (without a bias the logits')
+    E, k = 64, 6
+    order = torch.stack([torch.randperm(E, generator=gen(s)) for s in range(30)])
+    x = (40.0 + order) if kind == "sigmoid" else -800.0 * order
+    b = torch.zeros(E)
+    for bias in (None, b, b.index_fill(0, torch.arange(20, 50), 0.5)):
+        check_choice(x.float(), k, kind, bias)
+        check_many(x.float().repeat(200, 1), k, kind, bias, True)
+    for bias in (None, b):
+        check_choice(x.float(), k, kind, bias, 8, 3)
+
+
 def test_the_callers_tensors_and_nothing_around_them():
     n, E, k = 70, 48, 5
     x = logits_of(1, n, E).cuda()
@@ -631,6 +645,35 @@ def test_another_stream():
     s.synchronize()
     for a, b in ((ids, want_ids), (w, want_w), (loss, want_loss), (counts, want_counts), (grad, want_grad)):
         assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    # 4,400,000 rows of 512: 2.25e9 logits, and as many gradients
+    n, E, k = 4_400_000, 512, 8
+    x = torch.empty(n, E, dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    bias = (torch.randn(E, generator=gen(2)) * 0.05).cuda()
+    ids, w = mx.route(x, k, mx.MOE_SCORE_SIGMOID, bias=bias)
+    offsets = torch.tensor([0, n - 70, n - 5], dtype=torch.int32).cuda()
+    loss, counts = mx.balance_loss(x, ids, 1.0, mx.MOE_SCORE_SIGMOID, seq_offsets=offsets)
+    q, want = torch.zeros(E, dtype=torch.float64, device="cuda"), 0.0
+    for a in range(0, n - 70, 1 << 18):
+        s = torch.sigmoid(x[a:min(a + (1 << 18), n - 70)].double())
+        q += (s / s.sum(1, keepdim=True)).sum(0)
+    full = ids[:n - 70].flatten().bincount(minlength=E)
+    assert torch.equal(counts[0].long(), full)
+    want = ((full.double() * q).sum() * E / (k * (n - 70.0) ** 2)).item()
+    tail = slice(n - 70, n - 5)
+    last, last_counts = plain.balance(x[tail].cpu(), ids[tail].cpu(), 1.0, "sigmoid")
+    assert torch.equal(counts[1].cpu(), last_counts[0])
+    assert abs(loss.item() - (want + last.item()) / 2) <= loss_error(x[tail].cpu(), n) * want
+    grad = mx.route_backward(x, ids, mx.MOE_SCORE_SIGMOID, d_weights=w)
+    for a in (0, 4_194_304 - 20, n - 40):      # 2^31 elements lie at row 4,194,304
+        rows = slice(a, a + 40)
+        some, some_w = mx.route(x[rows], k, mx.MOE_SCORE_SIGMOID, bias=bias)
+        assert torch.equal(ids[rows], some) and ((w[rows] - some_w).abs() <= 32 * EPS * some_w).all()
+        assert torch.equal(grad[rows], mx.route_backward(x[rows], some, mx.MOE_SCORE_SIGMOID, d_weights=w[rows]))
+    assert torch.equal(mx.route_backward(x, ids, mx.MOE_SCORE_SIGMOID, d_weights=w, out=x), grad)
 
 
 def test_the_routing_plan_takes_the_choice():
