@@ -88,7 +88,9 @@ size_t moe_fp8_packed_bytes(const moe_fp8_weights *w);
  *   rows            rows of x, below 2^31; (rows / 128 + E) * ceil(n_out / 128) at most 2^31 - 4097
  *   expert_offsets  [E + 1] int32, ascending from >= 0 to <= rows; anything else computes nothing and raises
  *                   MOE_ERR_ROUTING.  Rows of no expert are left alone, empty experts cost nothing.  NULL, where
- *                   num_experts is 1: all rows.
+ *                   num_experts is 1: all rows.  The tiles' size is chosen by rows and num_experts, all that the host knows:
+ *                   where one of many experts has most of a few rows, a call may take twice as long as for that
+ *                   expert alone.
  *   out             [out_rows] rows of n_out (out_type), out_ld elements apart (>= n_out), aligned to their
  *                   elements (fastest with 32-byte aligned rows)
  *   out_pos         [rows] int32, NULL = r.  Rows sent outside [0, out_rows) are skipped; a row that two are sent to

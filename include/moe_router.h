@@ -12,9 +12,12 @@
  *            c within them, in descending order.
  *   weight   w[t][j] = scale * s[t][ids[t][j]], divided by
  *            sum_i s[t][ids[t][i]] + 1e-20 with normalise
- * The choice is that of the exact scores: it does not depend on how fp32 rounds
- * them (close ones are computed again in 64 bits); without a bias and with one
- * group it is the order of the logits.  Equal values go to the lowest index.
+ * The choice is that of scores, choices and groups' values in 64 bits: it does not
+ * depend on how fp32 rounds them (close ones are computed again); without a bias and
+ * with one group it is the order of the logits.  Equal values, those among them that
+ * 64 bits do not tell apart (sigmoids of logits above 37 are 1), go to the lowest index.
+ * Large top_k are slow: of 18 a tenth of the rows, of 24 nearly all take top_k maxima
+ * over all experts in 64 bits.
  *
  * A logit of -inf masks its expert: it is never chosen, has the score 0 and the
  * gradient 0.  A bias of -inf or NaN keeps its expert from being chosen.  Where
@@ -24,18 +27,18 @@
  *
  * Balance loss over sequences s of T_s rows each (rows seq_offsets[s] ..
  * seq_offsets[s + 1] - 1), with S the number of those that have rows:
- *   q[t]     = s[t] / sum_e s[t][e]   (softmax: s[t] itself; 0 where every logit is -inf).  Quotients of the exact
- *              scores: a row whose sigmoids fp32 does not hold has shares all the same
+ *   q[t]     = s[t] / sum_e s[t][e]   (softmax: s[t] itself; 0 where every logit is
+ *              -inf), of the exact scores: rows whose sigmoids fp32 does not hold too
  *   count_se = entries of ids in the sequence's rows that are e
  *   loss     = coef / S * sum_s E / (top_k T_s^2) * sum_e count_se * sum_t q[t][e]
  * which is coef where every expert gets the same.  Counts are constants to the
  * gradient.  Rows of no sequence (padding behind the last) add nothing.
  *
  * Logits are fp32 or bf16, arithmetic is fp32, weights, bias and their gradients
- * fp32; in weights and their gradients a score below 2^-126 is 0.  All pointers except the struct are device pointers; every call is
- * asynchronous on `stream`, allocates nothing, does not synchronise and can be
- * captured.  Results do not depend on the order in which the GPU runs the work.
- * n = 0 is MOE_OK.
+ * fp32; in weights and their gradients a score below 2^-126 is 0.  All pointers
+ * except the struct are device pointers; every call is asynchronous on `stream`,
+ * allocates nothing, does not synchronise and can be captured.  Results do not depend
+ * on the order in which the GPU runs the work.  n = 0 is MOE_OK.
  */
 #ifndef MOE_ROUTER_H
 #define MOE_ROUTER_H

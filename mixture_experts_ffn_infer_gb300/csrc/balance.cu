@@ -20,8 +20,8 @@
 // HBM would bound all three; what they spend beyond it is a row's way through its reductions
 // (202 instructions a row of 384 in the first, 385 in the gradient, issued in 50 to 60 % of
 // the cycles) with the warps that registers leave.  65,536 x 384 fp32, sigmoid, k = 8, 16
-// sequences, on one GB300: loss 26.1 us (3.9 TB/s), 19 of them the first kernel; gradient
-// 39.3 us (5.2 TB/s).  (Two rows a warp, half the instructions a row and half the warps: 21.5
+// sequences, on one GB300: loss 25.7 us (4.0 TB/s), 19 of them the first kernel; gradient
+// 39.5 us (5.2 TB/s).  (Two rows a warp, half the instructions a row and half the warps: 21.5
 // for the first kernel's 21.)
 #include "router.cuh"
 

@@ -951,6 +951,9 @@ cudaError_t launch(const Fp8ProductLaunch& g, cudaStream_t s) {
 //   1024 x 7168 x 7168: 155 | 52.2 | 57.4 | 57.5           2048: 305 | 102 | 85.8 | 83.5       8192: 1187 | 393 | 330 | 317
 //   64 experts x 2048 x 2048, 8 rows each: 45.0 | 47.4 | 51.3 | 68.5     64: 79 | 50.1 | 55.6 | 72.6     1024: 967 | 332 | 287 | 302
 //   256 experts x 4096 x 7168, 16 rows each: 1064 | 1080 | 1034 | 1386   32 experts, 2048 each: 5565 | 1784 | 1530 | 1499
+// Who has the rows is not known here.  Where one expert has them all, tiles of 32 rows are the wrong ones: 1024 rows of 64
+// experts x 2048 x 2048 take 60 us evenly, 27 all of one expert, which by itself takes 15 (32 experts x 4096 x 7168, 512
+// rows: 163, 60, 25; all but one row each: 72 and 191).
 template <int OUT>
 cudaError_t launch_out(const Fp8ProductLaunch& g, cudaStream_t s) {
   const int64_t experts = g.rows < g.w->num_experts ? g.rows : g.w->num_experts, k = fp8_blocks(g.w->k);
